@@ -20,6 +20,7 @@ enum KernelId : int32_t {
   K_COMBINE = 7,
   K_BALANCE = 8,
   K_SELFTEST = 9,
+  K_GATE = 10,
 };
 
 // Status block at the start of every workspace (int32 words):

@@ -20,6 +20,8 @@ LIB_PATH = os.path.join(_HERE, "libmoe.so")
 MOE_OK = 0
 MOE_SCORE_SOFTMAX = 0
 MOE_SCORE_SIGMOID = 1
+MOE_F32 = 0
+MOE_BF16 = 1
 WS_STATUS_BYTES = 256
 
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
@@ -41,6 +43,14 @@ class RouteCfg(ctypes.Structure):
     _fields_ = [("score_fn", ctypes.c_int32), ("k", ctypes.c_int32),
                 ("n_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
                 ("group_topn", ctypes.c_int32)]
+
+
+class GateCfg(ctypes.Structure):
+    """moe_gate_cfg: the router with a balance bias."""
+    _fields_ = [("score_fn", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("n_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_topn", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
 
 
 class FfnSchedule(ctypes.Structure):
@@ -65,6 +75,7 @@ class PlacementC(ctypes.Structure):
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
+_F32 = ctypes.c_float
 _SZ = ctypes.c_size_t
 
 _SIGNATURES = {
@@ -117,6 +128,11 @@ _SIGNATURES = {
                                                         _I32, _I32, _I64, _I64, _I32,
                                                         ctypes.POINTER(FfnSchedule), _P, _P, _P,
                                                         _SZ, _P]),
+    "moe_gate": (ctypes.c_int, [_P, _I32, _I64, _I64, _I32, _P, ctypes.POINTER(GateCfg), _P, _P,
+                                _P]),
+    "moe_gate_backward": (ctypes.c_int, [_P, _I32, _I64, _I64, _I32, _P, _P,
+                                         ctypes.POINTER(GateCfg), _P, _P, _SZ, _P]),
+    "moe_gate_update_bias": (ctypes.c_int, [_P, _I32, _P, _F32, _P, _P]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_version": (ctypes.c_char_p, []),
 }
@@ -162,6 +178,22 @@ def _check(call: str, status: int):
 
 def _bf16(t: torch.Tensor, name: str):
     _need(t, torch.bfloat16, name)
+
+
+_TYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
+def _rows(t: torch.Tensor, name: str) -> int:
+    """The element type code of a 2-D fp32 or bf16 CUDA tensor whose rows are
+    contiguous (they may be further apart than their length)."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _TYPES or not t.is_cuda or t.dim() != 2 \
+            or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise TypeError(f"{name}: expected a CUDA matrix of float32 or bfloat16 with contiguous rows")
+    return _TYPES[t.dtype]
+
+
+def _ld(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 # ------------------------------------------------------------------ workspace
@@ -244,6 +276,52 @@ def moe_route(logits, cfg: RouteCfg, topk_ids, topk_w, ws=None, stream=None):
     _check("moe_route", lib().moe_route(_ptr(logits), T, E, ctypes.byref(cfg), _ptr(topk_ids),
                                         _ptr(topk_w), _ptr(ws), 0 if ws is None else ws.numel(),
                                         _stream(stream)))
+
+
+def moe_gate(logits, bias, cfg: GateCfg, topk_ids, topk_w, stream=None):
+    """Router with a balance bias: logits fp32 or bf16 [T, E], bias fp32 [E]
+    or None; topk_ids int32 and topk_w fp32 [T, k] are written."""
+    kind = _rows(logits, "logits")
+    _need(topk_ids, torch.int32, "topk_ids")
+    _need(topk_w, torch.float32, "topk_w")
+    T, E = logits.shape
+    if bias is not None:
+        _need(bias, torch.float32, "bias")
+        if bias.numel() != E:
+            raise ValueError("moe_gate: bias needs E entries")
+    if tuple(topk_ids.shape) != (T, cfg.k) or tuple(topk_w.shape) != (T, cfg.k):
+        raise ValueError("moe_gate: inconsistent shapes")
+    _check("moe_gate", lib().moe_gate(_ptr(logits), kind, _ld(logits), T, E, _ptr(bias),
+                                      ctypes.byref(cfg), _ptr(topk_ids), _ptr(topk_w),
+                                      _stream(stream)))
+
+
+def moe_gate_backward(logits, topk_ids, grad_w, cfg: GateCfg, grad_logits, ws, stream=None):
+    """Gradient of the logits for a gradient of moe_gate's weights, the chosen
+    experts held fixed; grad_logits has the logits' type and shape."""
+    kind = _rows(logits, "logits")
+    _need(topk_ids, torch.int32, "topk_ids")
+    _need(grad_w, torch.float32, "grad_w")
+    _need(grad_logits, logits.dtype, "grad_logits")
+    T, E = logits.shape
+    if tuple(topk_ids.shape) != (T, cfg.k) or tuple(grad_w.shape) != (T, cfg.k) \
+            or tuple(grad_logits.shape) != (T, E):
+        raise ValueError("moe_gate_backward: inconsistent shapes")
+    _check("moe_gate_backward", lib().moe_gate_backward(
+        _ptr(logits), kind, _ld(logits), T, E, _ptr(topk_ids), _ptr(grad_w), ctypes.byref(cfg),
+        _ptr(grad_logits), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def moe_gate_update_bias(counts, bias, rate: float, bias_out, stream=None):
+    """bias_out = bias + rate * sign(mean load - counts); bias_out may be bias."""
+    _need(counts, torch.int32, "counts")
+    _need(bias, torch.float32, "bias")
+    _need(bias_out, torch.float32, "bias_out")
+    E = counts.numel()
+    if bias.numel() != E or bias_out.numel() != E:
+        raise ValueError("moe_gate_update_bias: inconsistent shapes")
+    _check("moe_gate_update_bias", lib().moe_gate_update_bias(
+        _ptr(counts), E, _ptr(bias), float(rate), _ptr(bias_out), _stream(stream)))
 
 
 def moe_dispatch_layout(topk_ids, placement: DevicePlacement, slot, seg_counts, seg_offsets,

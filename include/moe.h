@@ -169,6 +169,76 @@ moe_status moe_route(const float *logits, int64_t T, int32_t E, const moe_route_
                      int32_t *topk_ids, float *topk_w, void *ws, size_t ws_bytes,
                      void *stream);
 
+/* Element types of tensors that come in more than one. */
+enum { MOE_F32 = 0, MOE_BF16 = 1 };
+
+/* Configuration of the router with a balance bias.
+ *  score_fn     MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID.
+ *  k            experts per token, 1 <= k <= 16, k <= topk_groups * E / n_groups.
+ *  n_groups     1 = no group limit; else E % n_groups == 0, n_groups <= 32.
+ *  topk_groups  groups kept (1..n_groups).
+ *  group_topn   experts summed into a group's score (1..E/n_groups, <= 8).
+ *  renormalize  1: the k weights sum to scale; 0: they are scale * score.
+ *  scale        factor of the weights, positive and finite. */
+typedef struct moe_gate_cfg {
+  int32_t score_fn;
+  int32_t k;
+  int32_t n_groups;
+  int32_t topk_groups;
+  int32_t group_topn;
+  int32_t renormalize;
+  float scale;
+} moe_gate_cfg;
+
+/* Router with a balance bias: the bias moves the choice of experts towards
+ * balanced loads and leaves their weights alone.  "14. Serving
+ * Mixture-of-Experts Models", "Follow one token through an MoE layer" (ids
+ * and weights for every token); "Mixture-of-Experts Inference", "MoE
+ * architecture recap" (groups first, then experts within them).
+ *   s_e = softmax(logits[t])_e or sigmoid(logits[t][e]);  c_e = s_e + bias[e]
+ *   a group's score is the sum of its group_topn largest c; the topk_groups
+ *   best groups are kept (n_groups > 1); the k largest c among their experts
+ *   are chosen, in descending order; ties go to the lower id.
+ *   topk_w = scale * s_e / (sum of the k chosen s), or scale * s_e.
+ *  The choice is the one of real arithmetic up to differences of c (or of
+ *  group scores) below about 2^-40 of their size; equal logits with equal
+ *  biases are exact ties.  The weights are within a few fp32 ulps.
+ *  A logit of -inf or NaN masks its expert: s = 0, it is chosen only when the
+ *  kept groups hold fewer than k unmasked experts (lower ids first, weight
+ *  0), it adds nothing to its group's score, and a group without an unmasked
+ *  expert ranks last.  Logits above FLT_MAX count as FLT_MAX, biases are
+ *  clamped to [-1e30, 1e30] (NaN: -1e30).
+ *  logits   device fp32 or bf16 [T, E] (logits_type), rows ld >= E elements
+ *           apart.
+ *  bias     device fp32 [E], or NULL for none.
+ *  topk_ids device int32 [T, k];  topk_w device fp32 [T, k].
+ *  Limits: E <= 512, k <= 16. */
+moe_status moe_gate(const void *logits, int32_t logits_type, int64_t ld, int64_t T, int32_t E,
+                    const float *bias, const moe_gate_cfg *cfg, int32_t *topk_ids, float *topk_w,
+                    void *stream);
+
+/* Gradient of moe_gate's weights with respect to the logits, the choice of
+ * experts held fixed (it and the bias carry no gradient):
+ *   grad_logits[t, e] = sum_j grad_w[t, j] * d topk_w[t, j] / d logits[t, e].
+ *  Softmax without renormalisation reaches every expert of the row; the
+ *  other forms reach the chosen ones and write zeros elsewhere.
+ *  topk_ids    device int32 [T, k], distinct in a row, as moe_gate wrote them.
+ *  grad_w      device fp32 [T, k].
+ *  grad_logits device, logits_type [T, E], contiguous (written whole).
+ *  ws: at least MOE_WS_STATUS_BYTES.  Device errors: MOE_ERR_DEVICE_INDEX (an
+ *  id outside [0, E); its assignment is skipped). */
+moe_status moe_gate_backward(const void *logits, int32_t logits_type, int64_t ld, int64_t T,
+                             int32_t E, const int32_t *topk_ids, const float *grad_w,
+                             const moe_gate_cfg *cfg, void *grad_logits, void *ws,
+                             size_t ws_bytes, void *stream);
+
+/* Balance step of the bias: bias_out[e] = bias[e] + rate * sign(mean load -
+ * counts[e]), the mean over the E experts compared exactly.  counts device
+ * int32 [E] (for example moe_dispatch_layout's seg_counts without replicas);
+ * bias_out may be bias.  Limits: E <= 512; rate >= 0, finite. */
+moe_status moe_gate_update_bias(const int32_t *counts, int32_t E, const float *bias, float rate,
+                                float *bias_out, void *stream);
+
 /* Dispatch layout: map every assignment a = t*k + j to a physical slot and
  * build the stable permutation into contiguous per-slot segments.
  * "14. Serving Mixture-of-Experts Models", "Follow one token", step 1 (a
