@@ -22,6 +22,10 @@ MOE_SCORE_SOFTMAX = 0
 MOE_SCORE_SIGMOID = 1
 MOE_F32 = 0
 MOE_BF16 = 1
+MOE_FP4_MX = 0
+MOE_FP4_NV = 1
+MOE_EPI_NONE = 0
+MOE_EPI_SWIGLU = 1
 WS_STATUS_BYTES = 256
 
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
@@ -133,6 +137,13 @@ _SIGNATURES = {
     "moe_gate_backward": (ctypes.c_int, [_P, _I32, _I64, _I64, _I32, _P, _P,
                                          ctypes.POINTER(GateCfg), _P, _P, _SZ, _P]),
     "moe_gate_update_bias": (ctypes.c_int, [_P, _I32, _P, _F32, _P, _P]),
+    "moe_fp4_scale_ld": (_I64, [_I32, _I32]),
+    "moe_quantize_fp4": (ctypes.c_int, [_P, _I32, _I64, _I64, _I32, _I32, _I32, _P, _P, _P]),
+    "moe_permute_fp4": (ctypes.c_int, [_P, _I64, _I32, _I32, _P, _I64, _I32, _I32, _P, _P, _P, _SZ,
+                                       _P]),
+    "moe_dequant_fp4": (ctypes.c_int, [_P, _P, _I64, _I32, _I32, _I32, _P, _I32, _P]),
+    "moe_fp4_packed_bytes": (_SZ, [_I32, _I32, _I32, _I32, _I32]),
+    "moe_pack_weights_fp4": (ctypes.c_int, [_P, _P, _I32, _I32, _I32, _I32, _I32, _P, _P]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_version": (ctypes.c_char_p, []),
 }
@@ -715,6 +726,90 @@ def moe_dequant_fp8(xq, x_scale, x_perm, masked_m=None, cap: int = 0, ws=None, s
     _check("moe_dequant_fp8", lib().moe_dequant_fp8(
         _ptr(xq), _ptr(x_scale), n_rows, H, cap, _ptr(masked_m), _ptr(x_perm), _ptr(ws),
         0 if ws is None else ws.numel(), _stream(stream)))
+
+
+# ------------------------------------------------------------------ FP4 rows and experts
+def moe_fp4_scale_ld(K: int, fmt: int) -> int:
+    return int(lib().moe_fp4_scale_ld(K, fmt))
+
+
+def new_fp4(rows: int, K: int, fmt: int, device=None):
+    """Allocate (torch) codes uint8 [rows, K/2] and scales uint8 [rows,
+    moe_fp4_scale_ld(K, fmt)] for rows of K elements."""
+    ld = moe_fp4_scale_ld(K, fmt)
+    if ld == 0:
+        raise ValueError("new_fp4: K must be a positive multiple of 32, fmt MOE_FP4_MX or MOE_FP4_NV")
+    dev = device or "cuda"
+    return (torch.empty(rows, K // 2, dtype=torch.uint8, device=dev),
+            torch.empty(rows, ld, dtype=torch.uint8, device=dev))
+
+
+def _fp4(codes, sf, fmt: int, call: str):
+    """(rows, K) of FP4 rows, checked."""
+    _need(codes, torch.uint8, "codes")
+    _need(sf, torch.uint8, "sf")
+    if codes.dim() != 2 or tuple(sf.shape) != (codes.shape[0], moe_fp4_scale_ld(2 * codes.shape[1], fmt)):
+        raise ValueError(f"{call}: inconsistent shapes")
+    return codes.shape[0], 2 * codes.shape[1]
+
+
+def moe_quantize_fp4(x, fmt: int, scale_exp: int, codes, sf, stream=None):
+    """Rows of x (fp32 or bf16 [n, K]) to FP4 codes and scales (new_fp4)."""
+    kind = _rows(x, "x")
+    n, K = _fp4(codes, sf, fmt, "moe_quantize_fp4")
+    if tuple(x.shape) != (n, K):
+        raise ValueError("moe_quantize_fp4: inconsistent shapes")
+    _check("moe_quantize_fp4", lib().moe_quantize_fp4(
+        _ptr(x), kind, _ld(x), n, K, fmt, int(scale_exp), _ptr(codes), _ptr(sf), _stream(stream)))
+
+
+def moe_permute_fp4(x, k: int, dest_row, fmt: int, scale_exp: int, codes, sf, ws, stream=None):
+    """Quantize each token row of x (bf16 [T, K]) once and write it to its k
+    dispatched rows of codes and sf; dest_row -1 is a drop."""
+    _bf16(x, "x")
+    _need(dest_row, torch.int32, "dest_row")
+    n, K = _fp4(codes, sf, fmt, "moe_permute_fp4")
+    T = x.shape[0]
+    if x.shape[1] != K or dest_row.numel() < T * k:
+        raise ValueError("moe_permute_fp4: inconsistent shapes")
+    _check("moe_permute_fp4", lib().moe_permute_fp4(
+        _ptr(x), T, K, k, _ptr(dest_row), n, fmt, int(scale_exp), _ptr(codes), _ptr(sf), _ptr(ws),
+        ws.numel(), _stream(stream)))
+
+
+def moe_dequant_fp4(codes, sf, fmt: int, scale_exp: int, out, stream=None):
+    """FP4 rows back to values, out fp32 or bf16 [n, K]."""
+    n, K = _fp4(codes, sf, fmt, "moe_dequant_fp4")
+    if not isinstance(out, torch.Tensor) or out.dtype not in _TYPES:
+        raise TypeError("out: expected float32 or bfloat16")
+    _need(out, out.dtype, "out")
+    if tuple(out.shape) != (n, K):
+        raise ValueError("moe_dequant_fp4: inconsistent shapes")
+    _check("moe_dequant_fp4", lib().moe_dequant_fp4(
+        _ptr(codes), _ptr(sf), n, K, fmt, int(scale_exp), _ptr(out), _TYPES[out.dtype],
+        _stream(stream)))
+
+
+class Fp4Weights:
+    """Expert weights in the grouped product's layout (moe_pack_weights_fp4)."""
+
+    def __init__(self, data: torch.Tensor, E: int, N: int, K: int, fmt: int, epilogue: int):
+        self.data, self.E, self.N, self.K, self.fmt, self.epilogue = data, E, N, K, fmt, epilogue
+
+
+def pack_weights_fp4(codes, sf, fmt: int, epilogue: int, stream=None) -> Fp4Weights:
+    """FP4 expert weights (codes uint8 [E, N, K/2], sf uint8 [E, N,
+    moe_fp4_scale_ld]) into a new Fp4Weights for products with `epilogue`."""
+    _need(codes, torch.uint8, "codes")
+    _need(sf, torch.uint8, "sf")
+    E, N, K = codes.shape[0], codes.shape[1], 2 * codes.shape[2]
+    if tuple(sf.shape) != (E, N, moe_fp4_scale_ld(K, fmt)):
+        raise ValueError("pack_weights_fp4: inconsistent shapes")
+    n = int(lib().moe_fp4_packed_bytes(E, N, K, fmt, epilogue))
+    data = torch.empty(n, dtype=torch.uint8, device=codes.device)
+    _check("moe_pack_weights_fp4", lib().moe_pack_weights_fp4(
+        _ptr(codes), _ptr(sf), E, N, K, fmt, epilogue, _ptr(data), _stream(stream)))
+    return Fp4Weights(data, E, N, K, fmt, epilogue)
 
 
 def moe_status_string(status: int) -> str:

@@ -464,6 +464,67 @@ moe_status moe_dequant_fp8(const uint8_t *xq, const float *x_scale, int64_t n_ro
                            int32_t cap, const int32_t *masked_m, uint16_t *x_perm, void *ws,
                            size_t ws_bytes, void *stream);
 
+/* Microscaled 4-bit floating point.  "Mixture-of-Experts Inference",
+ * "Communication pressure" (quantize activations before dispatch) and "Memory
+ * pressure" (a decode step is dominated by loading the expert weights).
+ * Codes are e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6, sign in the top bit), two to a
+ * byte, the even element in the low half: uint8 [rows, K/2].  Consecutive
+ * elements of a row share one scale byte:
+ *   MOE_FP4_MX  32 elements; E8M0, the value 2^(byte - 127); 255 is NaN;
+ *   MOE_FP4_NV  16 elements; E4M3 times the tensor's 2^scale_exp; 127 is NaN.
+ * Scale rows are moe_fp4_scale_ld(K, fmt) bytes apart: K / 256 rounded up,
+ * times 8 (MX) or 16 (NV); the bytes past K are zero.
+ * scale_exp: 0 for MX; -100..100 for NV.  Limits: K % 32 == 0, K <= 2^24. */
+enum { MOE_FP4_MX = 0, MOE_FP4_NV = 1 };
+
+/* Bytes between two rows of scales; 0 for invalid arguments. */
+int64_t moe_fp4_scale_ld(int32_t K, int32_t fmt);
+
+/* Rows to FP4.  With amax a block's largest magnitude:
+ *   MX  2^e with the smallest e in [-127, 127] that has amax <= 6 * 2^e;
+ *   NV  s = E4M3(amax / (6 * 2^scale_exp)), nearest even, at most 448;
+ *   code = e2m1(x / scale), nearest even, at most 6 in magnitude; 0 where s is 0.
+ * The codes are those of real arithmetic (no rounding but these).  A zero may
+ * carry either sign.  A block with an infinity or NaN gets the NaN scale and
+ * zero codes.
+ *  x  device fp32 or bf16 (x_type), rows ldx >= K elements and a multiple of
+ *     16 bytes apart, 16-byte aligned;
+ *  codes uint8 [n_rows, K/2], sf uint8 [n_rows, moe_fp4_scale_ld], 16-byte
+ *     aligned, contiguous. */
+moe_status moe_quantize_fp4(const void *x, int32_t x_type, int64_t ldx, int64_t n_rows, int32_t K,
+                            int32_t fmt, int32_t scale_exp, uint8_t *codes, uint8_t *sf,
+                            void *stream);
+
+/* FP4 dispatch: quantize each token row once (as moe_quantize_fp4) and write
+ * its codes and scales to its k dispatched rows.
+ *  x device bf16 [T, K]; dest_row device int32 [T*k] (-1: dropped); codes, sf:
+ *  n_rows rows.  Other out-of-range rows are skipped and reported as
+ *  MOE_ERR_DEVICE_INDEX. */
+moe_status moe_permute_fp4(const uint16_t *x, int64_t T, int32_t K, int32_t k,
+                           const int32_t *dest_row, int64_t n_rows, int32_t fmt, int32_t scale_exp,
+                           uint8_t *codes, uint8_t *sf, void *ws, size_t ws_bytes, void *stream);
+
+/* FP4 rows back to values: out[r, c] = code * scale, exact in fp32, and in
+ * bf16 for what moe_quantize_fp4 writes.  out device fp32 or bf16 [n_rows, K],
+ * contiguous, 16-byte aligned. */
+moe_status moe_dequant_fp4(const uint8_t *codes, const uint8_t *sf, int64_t n_rows, int32_t K,
+                           int32_t fmt, int32_t scale_exp, void *out, int32_t out_type,
+                           void *stream);
+
+/* What a grouped product does with its result. */
+enum { MOE_EPI_NONE = 0, MOE_EPI_SWIGLU = 1 };
+
+/* Expert weights in FP4 (codes [E, N, K/2], scales [E, N, moe_fp4_scale_ld])
+ * rearranged into the tiles that moe_grouped_product_fp4 streams; done once
+ * per set of weights.  epilogue is the product's: with MOE_EPI_SWIGLU rows
+ * 0..N/2-1 of an expert are gate, the others up.  packed: device, 16-byte
+ * aligned, moe_fp4_packed_bytes bytes (0 for invalid arguments), not
+ * overlapping the inputs.  Limits: N % 8 == 0 (SwiGLU: N % 16 == 0). */
+size_t moe_fp4_packed_bytes(int32_t E, int32_t N, int32_t K, int32_t fmt, int32_t epilogue);
+moe_status moe_pack_weights_fp4(const uint8_t *codes, const uint8_t *sf, int32_t E, int32_t N,
+                                int32_t K, int32_t fmt, int32_t epilogue, uint8_t *packed,
+                                void *stream);
+
 /* Grouped SwiGLU expert FFN over contiguous segments.  "14. Serving
  * Mixture-of-Experts Models", "Follow one token", step 3 (a grouped matrix
  * multiplication: one kernel processes every expert's segment with its own
