@@ -21,6 +21,7 @@ enum KernelId : int32_t {
   K_BALANCE = 8,
   K_SELFTEST = 9,
   K_GATE = 10,
+  K_FP4_PRODUCT = 11,
 };
 
 // Status block at the start of every workspace (int32 words):

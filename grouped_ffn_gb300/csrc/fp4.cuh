@@ -32,6 +32,6 @@ struct Fmt<1> {  // NV
 // Weight tiles: 256 weight rows (two halves of 128) x 256 elements of K.
 constexpr int kHalfRows = 128;
 constexpr int kTileCodes = 2 * kHalfRows * 128;
-constexpr int tile_bytes(int fmt) { return kTileCodes + 2 * kHalfRows * (fmt == 1 ? 16 : 8); }
+__host__ __device__ constexpr int tile_bytes(int fmt) { return kTileCodes + 2 * kHalfRows * (fmt == 1 ? 16 : 8); }
 
 }  // namespace fp4

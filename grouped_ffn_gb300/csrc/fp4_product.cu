@@ -1,0 +1,540 @@
+// Grouped product of FP4 rows with the experts' FP4 weights on block-scaled
+// tcgen05 (formats and the weight tiles: fp4.cuh).
+//
+//   out[r, n] = alpha_e sum_K x[r, K] w_e[n, K]     rows r of segment s, e = seg_expert[s]
+//   with SwiGLU: out = silu(alpha_e g) * (alpha_e u), g and u the two halves of N.
+//
+// The weights are the tensor core's M side (tiles of 2 x 128 weight rows, in
+// shared memory exactly as they lie in memory, so one bulk copy a step), the
+// rows its N side: N is the number of rows in the tile, rounded up to 16, so
+// a segment of a few rows moves few bytes and wastes little of the tensor
+// core.  A segment of n rows is cut into ceil(n / 112) tiles of equal size.
+//
+// Per CTA (one per SM, 224 threads), a ring of 4 stages of 256 elements of K:
+//   warp 0     weights (one bulk copy) and rows (TMA boxes of 16 rows)
+//   warp 1     copies the stage's scales into TMEM (tcgen05.cp) and issues 8
+//              block-scaled MMAs of K = 64 (4 steps x 2 weight halves)
+//   warps 2-5  epilogue: TMEM lane = weight row, column = row of x
+//   warp 6     the rows' scales into the layout that tcgen05.cp reads
+// TMEM: two accumulators of 2 x 112 columns, 48 columns of scales.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+
+#include <mutex>
+
+#include "common.cuh"
+#include "fp4.cuh"
+#include "umma.cuh"
+
+namespace {
+
+using namespace umma;
+
+constexpr int kMaxRows = 112;  // rows of x in a tile
+constexpr int kBoxRows = 16;
+constexpr int kStages = 4;
+constexpr int kMaxSegs = 1024;
+constexpr int kThreads = 224;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kAccCols = 2 * kMaxRows;
+constexpr int kScaleCol = 2 * kAccCols;  // 32 columns of weight scales, 16 of row scales
+
+constexpr int kXOff = fp4::kTileCodes + 4096;   // rows' codes within a stage
+constexpr int kXsOff = kXOff + kMaxRows * 128;  // rows' scales: 4 groups of 512 bytes
+constexpr int kStageBytes = kXsOff + 4 * 512;
+static_assert(kStageBytes % 1024 == 0 && kXOff % 1024 == 0, "swizzle atoms are 1024 bytes");
+
+struct __align__(8) Bars {
+  uint64_t full[kStages];
+  uint64_t empty[kStages];
+  uint64_t tfull[2];
+  uint64_t tempty[2];
+  uint64_t drain;
+};
+constexpr size_t kBarsOff = (size_t)kStages * kStageBytes;
+constexpr size_t kMiscOff = kBarsOff + sizeof(Bars);
+constexpr size_t kSegOff = kMiscOff + 24;
+constexpr size_t kSmemBytes = kSegOff + (size_t)(4 * kMaxSegs + 1) * 4 + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory of one SM");
+
+struct Params {
+  const int32_t *seg_offsets, *seg_expert;
+  const uint8_t *w;    // packed tiles
+  const uint8_t *sf;   // rows' scales
+  const float *alpha;  // per expert, or NULL
+  void *out;
+  int32_t *status;
+  int64_t n_rows;
+  int32_t S, E, nkb, nbn, sf_ld;
+  int32_t out_n;  // columns of out
+};
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar,
+                                          uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1], %2, [%3], %4;" ::"r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ void fence_proxy_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// 512 bytes of scales (32 rows of 16 bytes) to 4 TMEM columns, repeated in
+// the four lane quadrants: no swizzle, 8-row groups 128 bytes apart.
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
+  const uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 32 |
+                     (uint64_t)1 << 46;
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+
+template <int FMT>
+__device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                        uint32_t accumulate) {
+  if (FMT == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void store_out(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store_out(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// silu(g) u.  bf16 results: the fast exponential and division are far below
+// the rounding of the result; fp32 results take the accurate ones.
+__device__ __forceinline__ float swiglu(float g, float u, float *) {
+  return g / (1.0f + expf(-g)) * u;
+}
+__device__ __forceinline__ float swiglu(float g, float u, __nv_bfloat16 *) {
+  return __fdividef(g, 1.0f + __expf(-g)) * u;
+}
+
+// One tile: weight tile nb of expert e times rows [row0, row0 + n) of x.
+struct Tile {
+  int e, nb, n;
+  int64_t row0;
+};
+
+// Tiles in order (segment, weight tile, row tile): CTAs side by side read the
+// same weight tile.  CTA b takes tiles b, b + grid, ...
+struct Walk {
+  const int32_t *pre, *lo, *hi, *ex;
+  int S, nbn;
+  int64_t t, total;
+
+  __device__ __forceinline__ bool valid() const { return t < total; }
+  __device__ __forceinline__ void next() { t += gridDim.x; }
+  __device__ __forceinline__ Tile tile() const {
+    int a = 0, b = S;  // the last s with pre[s] * nbn <= t: its segment has tiles
+    while (b - a > 1) {
+      const int c = (a + b) >> 1;
+      if ((int64_t)pre[c] * nbn <= t)
+        a = c;
+      else
+        b = c;
+    }
+    const int mt = pre[a + 1] - pre[a];
+    const int r = (int)(t - (int64_t)pre[a] * nbn);
+    const int rows = hi[a] - lo[a];
+    const int per = ((rows + mt - 1) / mt + 15) & ~15;  // <= 112, and (mt - 1) * per < rows
+    Tile x;
+    x.e = ex[a];
+    x.nb = r / mt;
+    const int m = r - x.nb * mt;
+    x.row0 = lo[a] + m * per;
+    x.n = min(per, rows - m * per);
+    return x;
+  }
+};
+
+template <int FMT, bool SWIGLU, typename Y>
+__global__ void __launch_bounds__(kThreads, 1)
+    product_kernel(const __grid_constant__ CUtensorMap tmap_x, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  Bars *bars = reinterpret_cast<Bars *>(smem + kBarsOff);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kMiscOff);
+  volatile int32_t *abort_flag = reinterpret_cast<int32_t *>(smem + kMiscOff + 4);
+  volatile int32_t *epi_ok = reinterpret_cast<int32_t *>(smem + kMiscOff + 8);
+  int32_t *lo = reinterpret_cast<int32_t *>(smem + kSegOff);
+  int32_t *hi = lo + kMaxSegs;
+  int32_t *ex = hi + kMaxSegs;
+  int32_t *pre = ex + kMaxSegs;  // [S + 1] row tiles before segment s
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int32_t kid = moe::K_FP4_PRODUCT;
+  constexpr int kScaleBytes = fp4::Fmt<FMT>::kScaleBytes;
+  constexpr int kGroups = kScaleBytes / 4;  // 512-byte scale groups of 128 rows per stage
+  constexpr uint32_t kTileBytes = fp4::tile_bytes(FMT);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&bars->full[i], 2);  // the producer and the rows' scales
+      mbar_init(&bars->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->tfull[i], 1);
+      mbar_init(&bars->tempty[i], 128);
+    }
+    mbar_init(&bars->drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  moe::pdl_wait();
+  moe::pdl_trigger();
+  int decreasing = 0;  // offsets that go back name no segments at all
+  for (int s = threadIdx.x; s < p.S; s += kThreads) {
+    const int64_t a = p.seg_offsets[s], b = p.seg_offsets[s + 1];
+    const int e = p.seg_expert[s];
+    int mt = 0;
+    if (b < a) {
+      moe::report_error(p.status, MOE_ERR_DEVICE_INDEX, s, kid);
+      decreasing = 1;
+    }
+    if (b > a) {
+      if (a < 0 || b > p.n_rows || e < 0 || e >= p.E)
+        moe::report_error(p.status, MOE_ERR_DEVICE_INDEX, s, kid);
+      else
+        mt = (int)((b - a + kMaxRows - 1) / kMaxRows);
+    }
+    lo[s] = (int)a;
+    hi[s] = (int)b;
+    ex[s] = e;
+    pre[s] = mt;
+  }
+  const bool none = __syncthreads_or(decreasing) != 0;
+  if (warp == 0) warp_exclusive_scan(pre, p.S, lane);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  Walk walk{pre, lo, hi, ex, p.S, p.nbn, (int64_t)blockIdx.x,
+            none ? 0 : (int64_t)pre[p.S] * p.nbn};
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      prefetch_tmap(&tmap_x);
+      const uint64_t pol = policy_evict_first();
+      int stage = 0;
+      uint32_t phase = 0, armed = 0, armed_par = 0;
+      bool ok = true;
+      for (; walk.valid() && ok; walk.next()) {
+        const Tile ti = walk.tile();
+        const int boxes = (ti.n + kBoxRows - 1) / kBoxRows;
+        const uint8_t *w = p.w + ((int64_t)ti.e * p.nbn + ti.nb) * p.nkb * (int64_t)kTileBytes;
+        for (int kb = 0; kb < p.nkb; ++kb) {
+          if (!mbar_wait(&bars->empty[stage], phase ^ 1u, abort_flag, p.status, kid)) {
+            ok = false;
+            break;
+          }
+          uint8_t *st = smem + (size_t)stage * kStageBytes;
+          mbar_arrive_expect_tx(&bars->full[stage], kTileBytes + boxes * kBoxRows * 128);
+          bulk_load(st, w + (int64_t)kb * kTileBytes, kTileBytes, &bars->full[stage], pol);
+          for (int b = 0; b < boxes; ++b)
+            tma_load_2d(st + kXOff + b * kBoxRows * 128, &tmap_x, kb * 128,
+                        (int)ti.row0 + b * kBoxRows, &bars->full[stage]);
+          armed |= 1u << stage;
+          armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // Own copies land before the CTA exits.  After an abort the scales'
+      // arrival of a stage may never come, so it is made here; where it did
+      // come, the extra one counts towards a phase that nobody waits for.
+      if (!ok)
+        for (int i = 0; i < kStages; ++i)
+          if ((armed >> i) & 1u) mbar_arrive(&bars->full[i]);
+      for (int i = 0; i < kStages; ++i)
+        if ((armed >> i) & 1u) mbar_wait_drain(&bars->full[i], (armed_par >> i) & 1u);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (; walk.valid() && ok; walk.next()) {
+        const Tile ti = walk.tile();
+        const uint32_t nmma = (uint32_t)((ti.n + 15) & ~15);
+        // e2m1 operands (bits 7-9, 10-11), N / 8 at 17, scales E8M0 (1) or
+        // E4M3 (0) at 23, M = 128 at 27
+        const uint32_t idesc = (1u << 7) | (1u << 10) | ((nmma >> 3) << 17) |
+                               ((FMT == 0 ? 1u : 0u) << 23) | (1u << 27);
+        if (!mbar_wait(&bars->tempty[acc], acc_phase ^ 1u, abort_flag, p.status, kid)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + (uint32_t)(acc * kAccCols);
+        const uint32_t sfa = tmem_base + kScaleCol, sfb = sfa + 32;
+        for (int kb = 0; kb < p.nkb; ++kb) {
+          if (!mbar_wait(&bars->full[stage], phase, abort_flag, p.status, kid)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sw = smem_u32(smem + (size_t)stage * kStageBytes);
+          const uint32_t sx = sw + kXOff;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g)
+              copy_scales(sfa + (h * kGroups + g) * 4,
+                          sw + fp4::kTileCodes + (h * kGroups + g) * 512);
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) copy_scales(sfb + g * 4, sw + kXsOff + g * 512);
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            // NV: a group a step; MX: two steps share a group's 4 bytes
+            const int g = FMT == 1 ? s : s / 2;
+            const uint32_t id = FMT == 1 ? 0u : (uint32_t)(s & 1) * 2u;
+            const uint32_t idesc_s = idesc | (id << 4) | (id << 29);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              mma_fp4<FMT>(d + h * kMaxRows, sw128_desc(sw + h * 16384 + s * 32),
+                           sw128_desc(sx + s * 32), idesc_s, sfa + (h * kGroups + g) * 4,
+                           sfb + g * 4, (kb | s) != 0 ? 1u : 0u);
+          }
+          umma_commit(&bars->empty[stage]);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        umma_commit(&bars->tfull[acc]);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      umma_commit(&bars->drain);
+      mbar_wait_drain(&bars->drain, 0);
+    }
+  } else if (warp == 6) {
+    // ------------------------------------------- the rows' scales, per stage
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (; walk.valid() && ok; walk.next()) {
+      const Tile ti = walk.tile();
+      for (int kb = 0; kb < p.nkb; ++kb) {
+        // rows lane, lane + 32, ...: this step's scale bytes of each
+        uint32_t v[4][kGroups];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = lane + 32 * j;
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) v[j][g] = 0;
+          if (r < ti.n) {
+            const uint32_t *src = reinterpret_cast<const uint32_t *>(
+                p.sf + (ti.row0 + r) * p.sf_ld + kb * kScaleBytes);
+            if constexpr (FMT == 1) {
+              const uint4 u = __ldg(reinterpret_cast<const uint4 *>(src));
+              v[j][0] = u.x;
+              v[j][1] = u.y;
+              v[j][2] = u.z;
+              v[j][3] = u.w;
+            } else {
+              const uint2 u = __ldg(reinterpret_cast<const uint2 *>(src));
+              v[j][0] = u.x;
+              v[j][1] = u.y;
+            }
+          }
+        }
+        int got = 0;
+        if (lane == 0)
+          got = mbar_wait(&bars->empty[stage], phase ^ 1u, abort_flag, p.status, kid) ? 1 : 0;
+        if (!__shfl_sync(0xffffffffu, got, 0)) {
+          ok = false;
+          break;
+        }
+        uint8_t *dst = smem + (size_t)stage * kStageBytes + kXsOff + lane * 16;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+          *reinterpret_cast<uint4 *>(dst + g * 512) = make_uint4(v[0][g], v[1][g], v[2][g], v[3][g]);
+        fence_proxy_async_shared();  // tcgen05.cp reads them through the async proxy
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->full[stage]);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  } else {
+    // -------------------------------------------------- epilogue warps 2..5
+    const int q = warp & 3;  // TMEM lane quadrant this warp may access
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (; walk.valid(); walk.next()) {
+      const Tile ti = walk.tile();
+      if (warp == 2 && lane == 0)
+        epi_ok[acc] = mbar_wait(&bars->tfull[acc], acc_phase, abort_flag, p.status, kid) ? 1 : 0;
+      epilogue_bar();
+      if (!epi_ok[acc]) break;
+      tc_fence_after();
+      const float alpha = p.alpha ? __ldg(p.alpha + ti.e) : 1.0f;
+      const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kAccCols);
+      const int col0 = ti.nb * (SWIGLU ? 128 : 256) + q * 32 + lane;
+      Y *out = static_cast<Y *>(p.out) + ti.row0 * p.out_n + col0;
+#pragma unroll 1
+      for (int c = 0; c < ti.n; c += 16) {
+        uint32_t a[16], b[16];
+        tmem_ld16(tbase + c, a);
+        tmem_ld16(tbase + kMaxRows + c, b);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (c + i >= ti.n) break;
+          const float va = __uint_as_float(a[i]) * alpha, vb = __uint_as_float(b[i]) * alpha;
+          Y *o = out + (int64_t)(c + i) * p.out_n;
+          if (SWIGLU) {
+            if (col0 < p.out_n) store_out(o, swiglu(va, vb, (Y *)nullptr));
+          } else {
+            if (col0 < p.out_n) store_out(o, va);
+            if (col0 + 128 < p.out_n) store_out(o + 128, vb);
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&bars->tempty[acc]);
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------ host
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  });
+  return fn;
+}
+
+template <int FMT, bool SWIGLU, typename Y>
+moe_status launch(const CUtensorMap &m, const Params &p, int64_t max_tiles, cudaStream_t st) {
+  constexpr int kMaxDevices = 64;
+  static bool done[kMaxDevices] = {false};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+  if (dev < 0 || dev >= kMaxDevices || !done[dev]) {
+    if (cudaFuncSetAttribute(product_kernel<FMT, SWIGLU, Y>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)kSmemBytes) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    if (dev >= 0 && dev < kMaxDevices) done[dev] = true;
+  }
+  int64_t grid = moe_host::sm_count();
+  if (max_tiles < grid) grid = max_tiles;
+  return moe_host::launch_pdl(product_kernel<FMT, SWIGLU, Y>, dim3((unsigned)grid), dim3(kThreads),
+                              kSmemBytes, st, m, p);
+}
+
+template <int FMT, bool SWIGLU>
+moe_status launch_type(const CUtensorMap &m, const Params &p, int64_t max_tiles, int32_t out_type,
+                       cudaStream_t st) {
+  return out_type == MOE_F32 ? launch<FMT, SWIGLU, float>(m, p, max_tiles, st)
+                             : launch<FMT, SWIGLU, __nv_bfloat16>(m, p, max_tiles, st);
+}
+
+}  // namespace
+
+extern "C" moe_status moe_grouped_product_fp4(const uint8_t *codes, const uint8_t *sf,
+                                              int64_t n_rows, const int32_t *seg_offsets,
+                                              const int32_t *seg_expert, int32_t S, int32_t E,
+                                              const uint8_t *w_packed, int32_t N, int32_t K,
+                                              int32_t fmt, int32_t epilogue, const float *alpha,
+                                              void *out, int32_t out_type, void *ws,
+                                              size_t ws_bytes, void *stream) {
+  if (n_rows < 0 || S < 1 || E < 1 || N < 1 || K < 1) return MOE_ERR_INVALID_ARG;
+  if (fmt != MOE_FP4_MX && fmt != MOE_FP4_NV) return MOE_ERR_INVALID_ARG;
+  if (epilogue != MOE_EPI_NONE && epilogue != MOE_EPI_SWIGLU) return MOE_ERR_INVALID_ARG;
+  if (out_type != MOE_F32 && out_type != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  const bool swi = epilogue == MOE_EPI_SWIGLU;
+  if (S > kMaxSegs || K % 32 != 0 || K > (1 << 24) || N % (swi ? 16 : 8) != 0 ||
+      n_rows >= ((int64_t)1 << 31) - kBoxRows)
+    return MOE_ERR_UNSUPPORTED;
+  Params p{};
+  p.nkb = (K + fp4::kStepElems - 1) / fp4::kStepElems;
+  p.nbn = swi ? (N / 2 + 127) / 128 : (N + 255) / 256;
+  const int64_t max_tiles = ((n_rows + kMaxRows - 1) / kMaxRows + S) * p.nbn;
+  if (max_tiles >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+  if (!seg_offsets || !seg_expert || !w_packed) return MOE_ERR_INVALID_ARG;
+  if (moe_status s = moe_host::check_ws(ws, ws_bytes, moe::kStatusBytes)) return s;
+  if (n_rows == 0) return MOE_OK;
+  if (!codes || !sf || !out) return MOE_ERR_INVALID_ARG;
+  if (!moe_host::aligned16(codes) || !moe_host::aligned16(sf) || !moe_host::aligned16(w_packed) ||
+      !moe_host::aligned16(out))
+    return MOE_ERR_INVALID_ARG;
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (!fn) return MOE_ERR_CUDA;
+  // rows' codes: [n_rows, K / 2] bytes, boxes of 128 bytes x 16 rows
+  CUtensorMap m;
+  cuuint64_t dims[2] = {(cuuint64_t)K / 2, (cuuint64_t)n_rows};
+  cuuint64_t strides[1] = {(cuuint64_t)K / 2};
+  cuuint32_t box[2] = {128, kBoxRows};
+  cuuint32_t estr[2] = {1, 1};
+  if (fn(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(codes), dims, strides, box,
+         estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return MOE_ERR_CUDA;
+  p.seg_offsets = seg_offsets;
+  p.seg_expert = seg_expert;
+  p.w = w_packed;
+  p.sf = sf;
+  p.alpha = alpha;
+  p.out = out;
+  p.status = moe_host::status_ptr(ws);
+  p.n_rows = n_rows;
+  p.S = S;
+  p.E = E;
+  p.sf_ld = (int32_t)moe_fp4_scale_ld(K, fmt);
+  p.out_n = swi ? N / 2 : N;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (fmt == MOE_FP4_MX)
+    return swi ? launch_type<0, true>(m, p, max_tiles, out_type, st)
+               : launch_type<0, false>(m, p, max_tiles, out_type, st);
+  return swi ? launch_type<1, true>(m, p, max_tiles, out_type, st)
+             : launch_type<1, false>(m, p, max_tiles, out_type, st);
+}

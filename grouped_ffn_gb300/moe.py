@@ -144,6 +144,8 @@ _SIGNATURES = {
     "moe_dequant_fp4": (ctypes.c_int, [_P, _P, _I64, _I32, _I32, _I32, _P, _I32, _P]),
     "moe_fp4_packed_bytes": (_SZ, [_I32, _I32, _I32, _I32, _I32]),
     "moe_pack_weights_fp4": (ctypes.c_int, [_P, _P, _I32, _I32, _I32, _I32, _I32, _P, _P]),
+    "moe_grouped_product_fp4": (ctypes.c_int, [_P, _P, _I64, _P, _P, _I32, _I32, _P, _I32, _I32,
+                                               _I32, _I32, _P, _P, _I32, _P, _SZ, _P]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_version": (ctypes.c_char_p, []),
 }
@@ -810,6 +812,30 @@ def pack_weights_fp4(codes, sf, fmt: int, epilogue: int, stream=None) -> Fp4Weig
     _check("moe_pack_weights_fp4", lib().moe_pack_weights_fp4(
         _ptr(codes), _ptr(sf), E, N, K, fmt, epilogue, _ptr(data), _stream(stream)))
     return Fp4Weights(data, E, N, K, fmt, epilogue)
+
+
+def moe_grouped_product_fp4(codes, sf, seg_offsets, seg_expert, w: Fp4Weights, alpha, out, ws,
+                            stream=None):
+    """FP4 rows times the experts' FP4 weights, with the epilogue that w was
+    packed for: out fp32 or bf16 [n, N] (SwiGLU: [n, N/2]).  alpha fp32 [E] or
+    None holds each expert's factor (tensor scales of rows and weights)."""
+    n, K = _fp4(codes, sf, w.fmt, "moe_grouped_product_fp4")
+    _need(seg_offsets, torch.int32, "seg_offsets")
+    _need(seg_expert, torch.int32, "seg_expert")
+    if alpha is not None:
+        _need(alpha, torch.float32, "alpha")
+    if not isinstance(out, torch.Tensor) or out.dtype not in _TYPES:
+        raise TypeError("out: expected float32 or bfloat16")
+    _need(out, out.dtype, "out")
+    S = seg_expert.numel()
+    cols = w.N // 2 if w.epilogue == MOE_EPI_SWIGLU else w.N
+    if K != w.K or tuple(out.shape) != (n, cols) or seg_offsets.numel() != S + 1 \
+            or (alpha is not None and alpha.numel() != w.E):
+        raise ValueError("moe_grouped_product_fp4: inconsistent shapes")
+    _check("moe_grouped_product_fp4", lib().moe_grouped_product_fp4(
+        _ptr(codes), _ptr(sf), n, _ptr(seg_offsets), _ptr(seg_expert), S, w.E, _ptr(w.data), w.N, K,
+        w.fmt, w.epilogue, _ptr(alpha), _ptr(out), _TYPES[out.dtype], _ptr(ws), ws.numel(),
+        _stream(stream)))
 
 
 def moe_status_string(status: int) -> str:

@@ -670,6 +670,35 @@ moe_status moe_grouped_ffn_gather(const uint16_t *x, int64_t T, int32_t k,
                                   uint16_t *h, uint16_t *y_perm, void *ws, size_t ws_bytes,
                                   void *stream);
 
+/* Grouped product of FP4 rows with FP4 expert weights, one segment an expert.
+ * "14. Serving Mixture-of-Experts Models", "Follow one token", step 3 (one
+ * kernel processes every expert's segment with its own row count), on
+ * block-scaled tensor cores.  For segment s, e = seg_expert[s], row r in
+ * [seg_offsets[s], seg_offsets[s+1]) (fp32 accumulation, one rounding):
+ *   MOE_EPI_NONE    out[r, n] = alpha[e] * sum_K x[r, K] w[e, n, K],  n < N
+ *   MOE_EPI_SWIGLU  out[r, n] = silu(alpha[e] g) * (alpha[e] u),  n < N/2, with
+ *                   g from weight row n and u from weight row N/2 + n
+ * where x and w are the values of codes and scales without 2^scale_exp: fold
+ * those of the rows and the weights into alpha.
+ *  codes, sf   FP4 rows [n_rows, K] (moe_quantize_fp4, moe_permute_fp4).
+ *  seg_offsets device int32 [S+1], seg_expert device int32 [S].
+ *  w_packed    moe_pack_weights_fp4 of the same E, N, K, fmt and epilogue.
+ *  alpha       device fp32 [E], or NULL for 1.
+ *  out         device fp32 or bf16 (out_type) [n_rows, N or N/2], contiguous,
+ *              16-byte aligned; rows outside every segment are left unwritten.
+ *  Two calls (gate/up with SwiGLU, quantize, down) make an expert's FFN.
+ *  Limits: S <= 1024, K % 32 == 0, N % 8 == 0 (SwiGLU: N % 16 == 0), n_rows <
+ *  2^31 - 16.  ws: at least MOE_WS_STATUS_BYTES.  Device errors:
+ *  MOE_ERR_DEVICE_INDEX (an expert id or a segment outside its range: the
+ *  segment is skipped; offsets that decrease: nothing is computed),
+ *  MOE_ERR_DEVICE_TIMEOUT. */
+moe_status moe_grouped_product_fp4(const uint8_t *codes, const uint8_t *sf, int64_t n_rows,
+                                   const int32_t *seg_offsets, const int32_t *seg_expert,
+                                   int32_t S, int32_t E, const uint8_t *w_packed, int32_t N,
+                                   int32_t K, int32_t fmt, int32_t epilogue, const float *alpha,
+                                   void *out, int32_t out_type, void *ws, size_t ws_bytes,
+                                   void *stream);
+
 /* Combine: y[t] = bf16(acc) with acc = shared[t] (or 0) and, for j = 0..k-1
  * in order, acc = fmaf(topk_w[t,j], y_perm[dest_row[t*k+j]], acc) in fp32.
  * "14. Serving Mixture-of-Experts Models", "Follow one token", step 4 (the
