@@ -6,7 +6,19 @@
 //   groups by the sum of their group_topn largest c, then the k largest c of
 //   the kept groups (ties: lower id);   w = scale s  or  scale s / sum_k s.
 //
-// One warp per token; lane L holds experts L, L + 32, ... (VPL each).
+// One warp per token.  GB300 issues fp64 at a small fraction of the fp32 rate
+// and the choice needs more than fp32 only where two scores nearly meet, so
+// the warp chooses in fp32 with a bound on every score's error, and chooses
+// again in fp64 (select_exact) when a gap that decides something is within the
+// bounds: about one token in a thousand of a spread-out router.
+//
+// Layout: a group takes p = floor(32 / n_groups) neighbouring lanes and each
+// of them V consecutive experts (without groups p = 32), so a lane never
+// mixes groups and a row is read in order.  A score becomes a 32-bit key whose
+// unsigned order is the scores' (the low log2 V bits give way to the element's
+// position in its lane, which puts the lower of equal ones first).
+// Each lane sorts its V keys once; a round of the top-k is then one warp
+// reduction over the lanes' heads, and the winner moves up its list.
 #include <cuda_bf16.h>
 
 #include <cfloat>
@@ -19,8 +31,8 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxTopn = 8;
 constexpr float kBiasClamp = 1e30f;  // group sums of clamped biases stay finite
-// below this largest selected logit, sigmoid(l) is e^l to fp32 precision and
-// the renormalised weights are taken from e^(l - max l), which cannot vanish
+// below this logit sigmoid(l) is e^l to fp32 precision; where the largest chosen
+// one is, renormalised weights are taken from e^(l - max l), which cannot vanish
 constexpr float kTinyLogit = -80.0f;
 
 struct GateArgs {
@@ -51,6 +63,47 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+__device__ __forceinline__ float clamp_bias(float b) {
+  return fmaxf(fminf(b, kBiasClamp), -kBiasClamp);
+}
+
+__device__ __forceinline__ float rcp_fast(float x) {  // within 1 ulp
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// e^(a - b) for a <= b, 0 for a = -inf: the difference is split error-free
+// into hi + lo and e^(hi + lo) = e^hi (1 + lo).
+__device__ __forceinline__ float exp_diff(float a, float b) {
+  if (a == -INFINITY) return 0.0f;
+  const float hi = __fsub_rn(a, b);
+  const float bb = __fsub_rn(hi, a);
+  const float lo = __fsub_rn(__fsub_rn(a, __fsub_rn(hi, bb)), __fadd_rn(b, bb));
+  const float e = expf(hi);
+  return hi > -FLT_MAX ? __fmaf_rn(e, lo, e) : 0.0f;
+}
+
+__device__ __forceinline__ float sigmoid32(float x) {
+  // (far below zero 1 + e^-x overflows; the score is e^x there)
+  return x < kTinyLogit ? expf(x) : __frcp_rn(__fadd_rn(1.0f, expf(-x)));
+}
+
+// Compensated butterfly sum; every lane ends with the same value.
+__device__ __forceinline__ float warp_sum_compensated(float x) {
+  float s = x, c = 0.0f;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    const float os = __shfl_xor_sync(kFull, s, off);
+    const float oc = __shfl_xor_sync(kFull, c, off);
+    const float n = __fadd_rn(s, os), bb = __fsub_rn(n, s);
+    const float e = __fadd_rn(__fsub_rn(s, __fsub_rn(n, bb)), __fsub_rn(os, bb));
+    s = n;
+    c = __fadd_rn(__fadd_rn(c, oc), e);
+  }
+  return __fadd_rn(s, c);
+}
+
 // Arg-max over the warp of the values whose bit is set in mask (element i of
 // this lane is id lane + 32 i): the largest value, ties to the lower id.
 template <int VPL>
@@ -75,7 +128,157 @@ __device__ __forceinline__ void warp_argmax(const double (&v)[VPL], uint32_t mas
   }
 }
 
+// The k chosen experts of one row in fp64, lane j < k returning the j-th: the
+// definition step by step.  Lane L holds experts L, L + 32, ...
 template <typename L, int VPL>
+__device__ __noinline__ int select_exact(const L *row, int E, const float *bias, const GateArgs &a) {
+  const int lane = threadIdx.x & 31;
+  const int gsz = E / a.n_groups;
+  float l[VPL];
+  double c[VPL];
+  uint32_t avail = 0, on = 0;  // experts, and those not masked
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane + 32 * i;
+    l[i] = -INFINITY;
+    if (e < E) {
+      l[i] = usable(load_logit(row + e));
+      avail |= 1u << i;
+      if (l[i] > -INFINITY) on |= 1u << i;
+    }
+    m = fmaxf(m, l[i]);
+  }
+  double z = 0.0;
+  if (a.score_fn == MOE_SCORE_SOFTMAX) {
+    m = warp_max(m);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if ((on >> i) & 1u) z += exp((double)l[i] - (double)m);
+    z = warp_sum(z);
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    c[i] = -INFINITY;
+    if ((on >> i) & 1u) {
+      c[i] = a.score_fn == MOE_SCORE_SOFTMAX ? exp((double)l[i] - (double)m) / z
+                                             : 1.0 / (1.0 + exp(-(double)l[i]));
+      if (bias) c[i] += clamp_bias(__ldg(bias + lane + 32 * i));
+    }
+  }
+  if (a.n_groups > 1) {
+    double mine = -INFINITY;
+    for (int g = 0; g < a.n_groups; ++g) {
+      uint32_t mask = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (((on >> i) & 1u) && (lane + 32 * i) / gsz == g) mask |= 1u << i;
+      for (int r = 0; r < a.group_topn; ++r) {
+        double bv;
+        int bid;
+        warp_argmax<VPL>(c, mask, lane, bv, bid);
+        if (bid == INT_MAX) break;
+        if (lane == g) mine = r == 0 ? bv : mine + bv;
+        if ((bid & 31) == lane) mask &= ~(1u << (bid >> 5));
+      }
+    }
+    double gs[1] = {mine};
+    uint32_t free_ = lane < a.n_groups ? 1u : 0u, kept = 0;
+    for (int r = 0; r < a.topk_groups; ++r) {
+      double bv;
+      int bg;
+      warp_argmax<1>(gs, free_, lane, bv, bg);
+      kept |= 1u << bg;
+      if (bg == lane) free_ = 0;
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (((avail >> i) & 1u) && !((kept >> ((lane + 32 * i) / gsz)) & 1u)) avail &= ~(1u << i);
+  }
+  int my_id = 0;
+  for (int j = 0; j < a.k; ++j) {
+    double bv;
+    int bid;
+    warp_argmax<VPL>(c, avail, lane, bv, bid);
+    if ((bid & 31) == lane) avail &= ~(1u << (bid >> 5));
+    if (lane == j) my_id = bid;
+  }
+  return my_id;
+}
+
+// ------------------------------------------------------------ fp32 selection
+// Float to an unsigned integer of the same order, and back.
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+// Descending sort of V (a power of two) keys: Batcher's odd-even merge network.
+template <int V>
+__device__ __forceinline__ void sort_keys(uint32_t (&k)[V]) {
+#pragma unroll
+  for (int p = 1; p < V; p <<= 1)
+#pragma unroll
+    for (int q = p; q >= 1; q >>= 1)
+#pragma unroll
+      for (int j = q % p; j + q < V; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < V && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const uint32_t hi = max(k[i + j], k[i + j + q]);
+            k[i + j + q] = min(k[i + j], k[i + j + q]);
+            k[i + j] = hi;
+          }
+}
+
+template <int V>
+__device__ __forceinline__ void pop(uint32_t (&k)[V], bool yes) {
+#pragma unroll
+  for (int i = 0; i + 1 < V; ++i) k[i] = yes ? k[i + 1] : k[i];
+  if (yes) k[V - 1] = 0;
+}
+
+// V logits from p (16-byte pieces where the launch says that they line up).
+template <int V, bool VEC>
+__device__ __forceinline__ void load_row(const float *p, int n, float (&l)[V]) {
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (n > 0) f = __ldg(reinterpret_cast<const float4 *>(p + i));
+      l[i] = f.x;
+      l[i + 1] = f.y;
+      l[i + 2] = f.z;
+      l[i + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) l[i] = i < n ? __ldg(p + i) : -INFINITY;
+  }
+}
+template <int V, bool VEC>
+__device__ __forceinline__ void load_row(const __nv_bfloat16 *p, int n, float (&l)[V]) {
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      uint2 u = make_uint2(0xFF80FF80u, 0xFF80FF80u);
+      if (n > 0) u = __ldg(reinterpret_cast<const uint2 *>(p + i));
+      l[i] = __uint_as_float(u.x << 16);
+      l[i + 1] = __uint_as_float(u.x & 0xFFFF0000u);
+      l[i + 2] = __uint_as_float(u.y << 16);
+      l[i + 3] = __uint_as_float(u.y & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) l[i] = i < n ? load_logit(p + i) : -INFINITY;
+  }
+}
+
+// VPL: experts per lane of select_exact, ceil(E / 32) rounded up.
+template <typename L, int V, int VPL, bool VEC>
 __global__ void __launch_bounds__(256) gate_kernel(const L *__restrict__ logits, int64_t ld,
                                                    int64_t T, int E,
                                                    const float *__restrict__ bias, GateArgs a,
@@ -86,113 +289,169 @@ __global__ void __launch_bounds__(256) gate_kernel(const L *__restrict__ logits,
   const int lane = threadIdx.x & 31;
   const int64_t warp0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-  const int gsz = E / a.n_groups;
+  const int gsz = E / a.n_groups, p = 32 / a.n_groups;
+  const int grp = lane / p, q = lane - grp * p;
+  const bool has = grp < a.n_groups && q * V < gsz;  // this lane holds experts
+  const int e0 = has ? grp * gsz + q * V : 0;
+  const int n = has ? min(V, gsz - q * V) : 0;
+  const bool softmax = a.score_fn == MOE_SCORE_SOFTMAX;
+  // without bias and groups the scores' order is the logits'
+  const bool by_logit = bias == nullptr && a.n_groups == 1;
+  const bool need_z = softmax && (!by_logit || !a.renormalize);
+  float b[V];
+  if (bias != nullptr) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) b[i] = i < n ? clamp_bias(__ldg(bias + e0 + i)) : 0.0f;
+  }
+  // Error bounds of a key's score c: kScoreErr of the row's largest s (fast
+  // exponential, reciprocal or sum), and of |c| the bits given to the position
+  // and the rounding of the addition.
+  const float key_err = by_logit ? (V - 1) * 0x1p-23f : V * 0x1p-23f;
+  const float score_err = by_logit ? 0.0f : softmax ? 1.2e-6f : 3e-7f;
+
   for (int64_t t = warp0; t < T; t += nwarps) {
-    float l[VPL];
-    double c[VPL];
-    uint32_t avail = 0, on = 0;  // experts, and those not masked
+    const L *row = logits + t * ld;
+    float l[V];
+    load_row<V, VEC>(row + e0, n, l);
+    float m = -INFINITY, zinv = 1.0f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = lane + 32 * i;
-      l[i] = -INFINITY;
-      if (e < E) {
-        l[i] = usable(load_logit(logits + t * ld + e));
-        avail |= 1u << i;
-        if (l[i] > -INFINITY) on |= 1u << i;
-      }
-    }
-    float m = -INFINITY;
-    double z = 0.0;
-    if (a.score_fn == MOE_SCORE_SOFTMAX) {
+    for (int i = 0; i < V; ++i) l[i] = usable(l[i]);
+    uint32_t key[V];
+    float c[V];
+    if (need_z) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) m = fmaxf(m, l[i]);
+      for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
       m = warp_max(m);
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if ((on >> i) & 1u) z += exp((double)l[i] - (double)m);
-      z = warp_sum(z);
-    }
-    double s[VPL];
+      for (int i = 0; i < V; ++i) c[i] = exp_diff(l[i], m);
+      float part[V];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      s[i] = 0.0;
-      c[i] = -INFINITY;
-      if ((on >> i) & 1u) {
-        s[i] = a.score_fn == MOE_SCORE_SOFTMAX ? exp((double)l[i] - (double)m) / z
-                                               : 1.0 / (1.0 + exp(-(double)l[i]));
-        double b = 0.0;
-        if (bias) b = fmaxf(fminf(__ldg(bias + lane + 32 * i), kBiasClamp), -kBiasClamp);
-        c[i] = s[i] + b;
-      }
+      for (int i = 0; i < V; ++i) part[i] = c[i];
+#pragma unroll
+      for (int s = V / 2; s > 0; s >>= 1)
+#pragma unroll
+        for (int i = 0; i < s; ++i) part[i] += part[i + s];
+      float z = part[0];
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(kFull, z, off);
+      zinv = z > 0.0f ? __fdiv_rn(1.0f, z) : 0.0f;
     }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float x = l[i];
+      if (!by_logit) {
+        x = softmax ? c[i] * zinv : rcp_fast(1.0f + __expf(-l[i]));
+        if (bias != nullptr) x += b[i];
+      }
+      // a masked expert's key lies below every score's, that of no expert is 0
+      const uint32_t k = l[i] > -INFINITY ? ordered(x + 0.0f) & ~(uint32_t)(V - 1) : (uint32_t)V;
+      key[i] = i < n ? k | (uint32_t)(V - 1 - i) : 0u;
+    }
+    sort_keys<V>(key);
+    bool sure = true;
+    const float s_err = score_err * (softmax ? zinv : 1.0f);
+
     if (a.n_groups > 1) {
-      double mine = -INFINITY;
+      // the group's group_topn largest scores, one round each
+      uint32_t k2[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) k2[i] = key[i];
+      float gs = 0.0f, size = 0.0f;
+      bool any = false;
+      const uint32_t members = (p == 32 ? kFull : ((1u << p) - 1u)) << (grp * p & 31);
+      for (int r = 0; r < a.group_topn; ++r) {
+        uint32_t h = k2[0];
+        if ((p & (p - 1)) == 0) {
+          for (int off = p >> 1; off > 0; off >>= 1) h = max(h, __shfl_xor_sync(kFull, h, off));
+        } else {
+          const uint32_t mine = h;
+          for (int j = 1; j < p; ++j) {
+            const int src = q + j < p ? lane + j : lane + j - p;
+            h = max(h, __shfl_sync(kFull, mine, src & 31));
+          }
+        }
+        const uint32_t same = __ballot_sync(kFull, k2[0] == h) & members;
+        if (h >= 2u * V) {
+          const float x = unordered(h & ~(uint32_t)(V - 1));
+          gs += x;
+          size += fabsf(x);
+          any = true;
+        }
+        pop<V>(k2, lane == __ffs(same) - 1);
+      }
+      const bool valid = grp < a.n_groups;
+      if (!any) gs = -INFINITY;
+      int rank = 0;
       for (int g = 0; g < a.n_groups; ++g) {
-        uint32_t mask = 0;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (((on >> i) & 1u) && (lane + 32 * i) / gsz == g) mask |= 1u << i;
-        for (int r = 0; r < a.group_topn; ++r) {
-          double bv;
-          int bid;
-          warp_argmax<VPL>(c, mask, lane, bv, bid);
-          if (bid == INT_MAX) break;
-          if (lane == g) mine = r == 0 ? bv : mine + bv;
-          if ((bid & 31) == lane) mask &= ~(1u << (bid >> 5));
-        }
+        const float o = __shfl_sync(kFull, gs, g * p);
+        if (o > gs || (o == gs && g < grp)) ++rank;
       }
-      double gs[1] = {mine};
-      uint32_t free_ = lane < a.n_groups ? 1u : 0u, kept = 0;
-      for (int r = 0; r < a.topk_groups; ++r) {
-        double bv;
-        int bg;
-        warp_argmax<1>(gs, free_, lane, bv, bg);
-        kept |= 1u << bg;
-        if (bg == lane) free_ = 0;
+      const bool keep = valid && rank < a.topk_groups;
+      const float err = a.group_topn * s_err + (key_err + a.group_topn * 0x1p-23f) * size;
+      // the kept groups' least possible score against the others' largest
+      const uint32_t least = __reduce_min_sync(kFull, keep ? ordered(any ? gs - err : gs) : 0xFFFFFFFFu);
+      const uint32_t most =
+          __reduce_max_sync(kFull, valid && !keep ? ordered(any ? gs + err : gs) : 0u);
+      // (groups without an unmasked expert are exact ties, taken by id)
+      if (a.topk_groups < a.n_groups && least <= most && most != ordered(-INFINITY)) sure = false;
+      if (!keep) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = 0;
       }
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (((avail >> i) & 1u) && !((kept >> ((lane + 32 * i) / gsz)) & 1u)) avail &= ~(1u << i);
     }
-    int my_id = 0;
+
+    uint32_t my_key = 0;
+    int my_src = 0;
     for (int j = 0; j < a.k; ++j) {
-      double bv;
-      int bid;
-      warp_argmax<VPL>(c, avail, lane, bv, bid);
-      if ((bid & 31) == lane) avail &= ~(1u << (bid >> 5));
-      if (lane == j) my_id = bid;
-    }
-    // the selected experts' scores, from the lanes that hold them
-    double my_s = 0.0;
-    float my_l = -INFINITY;
-    for (int j = 0; j < a.k; ++j) {
-      const int id = __shfl_sync(kFull, my_id, j);
-      double sv = 0.0;
-      float lv = 0.0f;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (i == (id >> 5)) {
-          sv = s[i];
-          lv = l[i];
-        }
-      sv = __shfl_sync(kFull, sv, id & 31);
-      lv = __shfl_sync(kFull, lv, id & 31);
+      // equal scores of several lanes: the lowest lane holds the lowest id
+      const uint32_t head = key[0] & ~(uint32_t)(V - 1);
+      const uint32_t top = __reduce_max_sync(kFull, head);
+      const int src = __ffs(__ballot_sync(kFull, head == top)) - 1;
+      const uint32_t won = __shfl_sync(kFull, key[0], src);
       if (lane == j) {
-        my_s = sv;
-        my_l = lv;
+        my_key = won;
+        my_src = src;
+      }
+      pop<V>(key, lane == src);
+    }
+    const uint32_t rest = __reduce_max_sync(kFull, key[0]);  // the best one left out
+    int my_id = __shfl_sync(kFull, e0, my_src) + (V - 1 - (int)(my_key & (V - 1)));
+    float my_l = -INFINITY;
+    if (lane < a.k) my_l = usable(load_logit(row + my_id));
+    // bf16 logits keep all their bits in a key: their order is exact
+    if (!(by_logit && sizeof(L) == 2)) {
+      const float my_b = bias != nullptr && lane < a.k ? __ldg(bias + my_id) : 0.0f;
+      uint32_t next = __shfl_down_sync(kFull, my_key, 1);
+      const float next_l = __shfl_down_sync(kFull, my_l, 1), next_b = __shfl_down_sync(kFull, my_b, 1);
+      if (lane == a.k - 1) next = rest;
+      if (lane < a.k && next >= 2u * V) {
+        const float x = unordered(my_key & ~(uint32_t)(V - 1));
+        const float y = unordered(next & ~(uint32_t)(V - 1));
+        const bool apart = x - (s_err + key_err * fabsf(x)) > y + (s_err + key_err * fabsf(y));
+        const bool tie = lane < a.k - 1 && my_l == next_l && my_b == next_b;
+        if (!apart && !tie) sure = false;
       }
     }
+    if (!__all_sync(kFull, sure)) {
+      my_id = select_exact<L, VPL>(row, E, bias, a);
+      if (lane < a.k) my_l = usable(load_logit(row + my_id));
+    }
+
+    // weights, in fp32 with compensated differences and sums
+    float v = 0.0f;
     if (a.renormalize) {
-      const float ml = warp_max(my_l);
-      // (softmax: the selected experts may all be far below the row's largest)
-      const bool rel = a.score_fn == MOE_SCORE_SOFTMAX || ml < kTinyLogit;
-      const double num = rel ? (my_l > -INFINITY ? exp((double)my_l - (double)ml) : 0.0) : my_s;
-      const double den = warp_sum(lane < a.k ? num : 0.0);
-      my_s = den > 0.0 ? num / den : 0.0;
+      const float ml = warp_max(lane < a.k ? my_l : -INFINITY);
+      // (softmax: the chosen experts may all be far below the row's largest)
+      const bool rel = softmax || ml < kTinyLogit;
+      const float num = lane >= a.k ? 0.0f : rel ? exp_diff(my_l, ml) : sigmoid32(my_l);
+      const float den = warp_sum_compensated(num);
+      if (den > 0.0f) v = __fdiv_rn(num, den);
+    } else if (lane < a.k) {
+      v = softmax ? exp_diff(my_l, m) * zinv : sigmoid32(my_l);
     }
     if (lane < a.k) {
       ids[t * a.k + lane] = my_id;
-      w[t * a.k + lane] = (float)((double)a.scale * my_s);
+      w[t * a.k + lane] = a.scale * v;
     }
   }
 }
@@ -203,6 +462,8 @@ __global__ void __launch_bounds__(256) gate_kernel(const L *__restrict__ logits,
 //   sigmoid, renorm    dl_e = scale (g_e - sum g v) v_e (1 - s_e)    selected e
 //   softmax            dl_e = s_e (scale g_e [selected] - scale sum g s)  all e
 //   softmax, renorm    dl_e = scale (g_e - sum g v) v_e              selected e
+// A row is first written whole (zeros, or -s_e scale sum g s), then lane j < k
+// overwrites the j-th chosen expert's entry.
 template <typename L, int VPL>
 __global__ void __launch_bounds__(256)
     gate_backward_kernel(const L *__restrict__ logits, int64_t ld, int64_t T, int E,
@@ -213,8 +474,10 @@ __global__ void __launch_bounds__(256)
   const int lane = threadIdx.x & 31;
   const int64_t warp0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-  const bool dense = a.score_fn == MOE_SCORE_SOFTMAX && !a.renormalize;
+  const bool softmax = a.score_fn == MOE_SCORE_SOFTMAX;
+  const bool dense = softmax && !a.renormalize;
   for (int64_t t = warp0; t < T; t += nwarps) {
+    L *out = grad_logits + t * E;
     int id = -1;
     float g = 0.0f, my_l = -INFINITY;
     if (lane < a.k) {
@@ -223,66 +486,60 @@ __global__ void __launch_bounds__(256)
         moe::report_error(status, MOE_ERR_DEVICE_INDEX, (int32_t)(t * a.k + lane), moe::K_GATE);
         id = -1;
       } else {
-        g = __ldg(grad_w + t * a.k + lane);
+        g = a.scale * __ldg(grad_w + t * a.k + lane);
         my_l = usable(load_logit(logits + t * ld + id));
       }
     }
     const bool live = my_l > -INFINITY;
-    double mine = 0.0;  // this lane's assignment: its share of dl
-    double p[VPL];      // dense: every expert's score
-    double dot = 0.0;
+    float mine = 0.0f;  // this lane's entry
     if (dense) {
-      float m = -INFINITY;
+      float x[VPL], m = -INFINITY, z = 0.0f;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
         const int e = lane + 32 * i;
-        p[i] = e < E ? usable(load_logit(logits + t * ld + e)) : -INFINITY;
-        m = fmaxf(m, (float)p[i]);
+        x[i] = e < E ? usable(load_logit(logits + t * ld + e)) : -INFINITY;
+        m = fmaxf(m, x[i]);
       }
       m = warp_max(m);
-      double z = 0.0;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        p[i] = p[i] > -INFINITY ? exp(p[i] - (double)m) : 0.0;
-        z += p[i];
+        x[i] = exp_diff(x[i], m);
+        z += x[i];
       }
-      z = warp_sum(z);
+      z = warp_sum_compensated(z);
+      const float zinv = z > 0.0f ? __fdiv_rn(1.0f, z) : 0.0f;
+      const float p = live ? exp_diff(my_l, m) * zinv : 0.0f;
+      const float dot = warp_sum_compensated(g * p);
+      mine = p * (g - dot);
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) p[i] = z > 0.0 ? p[i] / z : 0.0;
-      dot = warp_sum(live ? (double)g * (exp((double)my_l - (double)m) / z) : 0.0);
-      mine = (double)a.scale * g;
+      for (int i = 0; i < VPL; ++i) {
+        const int e = lane + 32 * i;
+        if (e < E) store_grad(out + e, -(x[i] * zinv) * dot);
+      }
     } else {
-      const double s = a.score_fn == MOE_SCORE_SIGMOID && live ? 1.0 / (1.0 + exp(-(double)my_l)) : 0.0;
+      float num = 0.0f, q = 1.0f;  // q = 1 - s
+      if (!softmax && live) {
+        num = sigmoid32(my_l);
+        q = sigmoid32(-my_l);
+      }
       if (a.renormalize) {
         const float ml = warp_max(my_l);
-        const bool rel = a.score_fn == MOE_SCORE_SOFTMAX || ml < kTinyLogit;
-        const double num = !live ? 0.0 : rel ? exp((double)my_l - (double)ml) : s;
-        const double den = warp_sum(num);
-        const double v = den > 0.0 ? num / den : 0.0;
-        dot = warp_sum((double)g * v);
-        mine = (double)a.scale * (g - dot) * v * (1.0 - s);
+        if (softmax || ml < kTinyLogit) num = live ? exp_diff(my_l, ml) : 0.0f;
+        const float den = warp_sum_compensated(num);
+        const float v = den > 0.0f ? __fdiv_rn(num, den) : 0.0f;
+        const float dot = warp_sum_compensated(g * v);
+        mine = (g - dot) * v * q;
       } else {
-        mine = (double)a.scale * g * s * (1.0 - s);
+        mine = g * num * q;
+      }
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const int e = lane + 32 * i;
+        if (e < E) store_grad(out + e, 0.0f);
       }
     }
-    double out[VPL];
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) out[i] = 0.0;
-    for (int j = 0; j < a.k; ++j) {
-      const int e = __shfl_sync(kFull, id, j);
-      const double v = __shfl_sync(kFull, mine, j);
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (e == lane + 32 * i) out[i] = v;
-    }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = lane + 32 * i;
-      if (e < E) {
-        if (dense) out[i] = p[i] * (out[i] - (double)a.scale * dot);
-        store_grad(grad_logits + t * E + e, (float)out[i]);
-      }
-    }
+    __syncwarp();  // the row's stores come before the overwriting ones
+    if (id >= 0) store_grad(out + id, mine);
   }
 }
 
@@ -293,15 +550,18 @@ __global__ void __launch_bounds__(512) gate_update_bias_kernel(const int32_t *__
                                                                float *bias_out) {
   moe::pdl_wait();
   moe::pdl_trigger();
-  __shared__ unsigned long long total;
+  __shared__ long long part[16];
   const int e = threadIdx.x;
-  if (e == 0) total = 0;
-  __syncthreads();
   const long long n = e < E ? counts[e] : 0;
-  if (e < E) atomicAdd(&total, (unsigned long long)n);  // integers: the order does not matter
+  long long total = n;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(kFull, total, off);
+  if ((e & 31) == 0) part[e >> 5] = total;
   __syncthreads();
   if (e < E) {
-    const long long d = (long long)total - (long long)E * n;
+    total = 0;
+    for (int i = 0; i < 16; ++i) total += part[i];
+    const long long d = total - (long long)E * n;
     bias_out[e] = bias[e] + (d > 0 ? rate : d < 0 ? -rate : 0.0f);
   }
 }
@@ -337,26 +597,43 @@ unsigned gate_grid(int64_t T) {
   return (unsigned)(blocks > cap ? cap : blocks);
 }
 
-// Calls f with the experts a lane holds (1, 2, 4, 8 or 16) as a type.
+// Calls f with the smallest of 1, 2, 4, 8, 16, 32 that is at least n, as a type.
 template <int N>
-struct Vpl {
+struct Int {
   static constexpr int value = N;
 };
 template <typename F>
-moe_status by_experts(int E, F &&f) {
-  if (E <= 32) return f(Vpl<1>{});
-  if (E <= 64) return f(Vpl<2>{});
-  if (E <= 128) return f(Vpl<4>{});
-  if (E <= 256) return f(Vpl<8>{});
-  return f(Vpl<16>{});
+moe_status by_size(int n, F &&f) {
+  if (n <= 1) return f(Int<1>{});
+  if (n <= 2) return f(Int<2>{});
+  if (n <= 4) return f(Int<4>{});
+  if (n <= 8) return f(Int<8>{});
+  if (n <= 16) return f(Int<16>{});
+  return f(Int<32>{});
 }
 
 template <typename L>
 moe_status launch_gate(const void *logits, int64_t ld, int64_t T, int E, const float *bias,
                        GateArgs a, int32_t *ids, float *w, cudaStream_t st) {
-  return by_experts(E, [&](auto v) {
-    return moe_host::launch_pdl(gate_kernel<L, decltype(v)::value>, dim3(gate_grid(T)), dim3(256), 0,
-                                st, static_cast<const L *>(logits), ld, T, E, bias, a, ids, w);
+  const L *l = static_cast<const L *>(logits);
+  const int gsz = E / a.n_groups, p = 32 / a.n_groups;
+  return by_size((gsz + p - 1) / p, [&](auto v) {
+    constexpr int V = decltype(v)::value;
+    // experts per lane over the whole row: at most V, at least V / 2 where the
+    // groups fill the lanes, less where they do not
+    constexpr int VPL = V > 16 ? 16 : V;
+    auto run = [&](auto kernel) {
+      return moe_host::launch_pdl(kernel, dim3(gate_grid(T)), dim3(256), 0, st, l, ld, T, E, bias, a,
+                                  ids, w);
+    };
+    if constexpr (V >= 4) {
+      // four logits a load: every lane's experts start on a multiple of four
+      // in memory and none has a part of its V
+      if (gsz % V == 0 && ld % 4 == 0 &&
+          reinterpret_cast<uintptr_t>(logits) % (4 * sizeof(L)) == 0)
+        return run(gate_kernel<L, V, VPL, true>);
+    }
+    return run(gate_kernel<L, V, VPL, false>);
   });
 }
 
@@ -364,8 +641,9 @@ template <typename L>
 moe_status launch_backward(const void *logits, int64_t ld, int64_t T, int E, const int32_t *ids,
                            const float *g, GateArgs a, void *out, int32_t *status,
                            cudaStream_t st) {
-  return by_experts(E, [&](auto v) {
-    return moe_host::launch_pdl(gate_backward_kernel<L, decltype(v)::value>, dim3(gate_grid(T)),
+  return by_size((E + 31) / 32, [&](auto v) {
+    constexpr int VPL = decltype(v)::value > 16 ? 16 : decltype(v)::value;
+    return moe_host::launch_pdl(gate_backward_kernel<L, VPL>, dim3(gate_grid(T)),
                                 dim3(256), 0, st, static_cast<const L *>(logits), ld, T, E, ids, g,
                                 a, static_cast<L *>(out), status);
   });
