@@ -22,7 +22,6 @@
 #include <cuda_bf16.h>
 
 #include <cfloat>
-#include <climits>
 
 #include "common.cuh"
 
@@ -49,7 +48,7 @@ __device__ __forceinline__ void store_grad(__nv_bfloat16 *p, float v) { *p = __f
 
 // A logit as the scores see it: -inf for -inf and NaN (a masked expert), and
 // at most FLT_MAX.
-__device__ __forceinline__ float usable(float x) { return x > -INFINITY ? fminf(x, FLT_MAX) : -INFINITY; }
+__device__ __forceinline__ float usable(float x) { return fminf(fmaxf(x, -INFINITY), FLT_MAX); }
 
 __device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
@@ -72,6 +71,11 @@ __device__ __forceinline__ float rcp_fast(float x) {  // within 1 ulp
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+__device__ __forceinline__ float exp2_fast(float x) {  // within 2 ulp, tiny results 0
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 
 // e^(a - b) for a <= b, 0 for a = -inf: the difference is split error-free
 // into hi + lo and e^(hi + lo) = e^hi (1 + lo).
@@ -86,7 +90,20 @@ __device__ __forceinline__ float exp_diff(float a, float b) {
 
 __device__ __forceinline__ float sigmoid32(float x) {
   // (far below zero 1 + e^-x overflows; the score is e^x there)
-  return x < kTinyLogit ? expf(x) : __frcp_rn(__fadd_rn(1.0f, expf(-x)));
+  const float e = expf(x < kTinyLogit ? x : -x);
+  return x < kTinyLogit ? e : rcp_fast(__fadd_rn(1.0f, e));
+}
+
+// Sum over lanes 0..15 (the others hold 0), in those lanes: four roundings.
+__device__ __forceinline__ float sum16(float x) {
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) x += __shfl_xor_sync(kFull, x, off);
+  return x;
+}
+__device__ __forceinline__ float max16(float x) {
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, off));
+  return x;
 }
 
 // Compensated butterfly sum; every lane ends with the same value.
@@ -104,109 +121,6 @@ __device__ __forceinline__ float warp_sum_compensated(float x) {
   return __fadd_rn(s, c);
 }
 
-// Arg-max over the warp of the values whose bit is set in mask (element i of
-// this lane is id lane + 32 i): the largest value, ties to the lower id.
-template <int VPL>
-__device__ __forceinline__ void warp_argmax(const double (&v)[VPL], uint32_t mask, int lane,
-                                            double &bv, int &bid) {
-  bv = 0.0;
-  bid = INT_MAX;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i)
-    if (((mask >> i) & 1u) && (bid == INT_MAX || v[i] > bv)) {
-      bv = v[i];
-      bid = lane + 32 * i;
-    }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    const double ov = __shfl_xor_sync(kFull, bv, off);
-    const int oid = __shfl_xor_sync(kFull, bid, off);
-    if (oid != INT_MAX && (bid == INT_MAX || ov > bv || (ov == bv && oid < bid))) {
-      bv = ov;
-      bid = oid;
-    }
-  }
-}
-
-// The k chosen experts of one row in fp64, lane j < k returning the j-th: the
-// definition step by step.  Lane L holds experts L, L + 32, ...
-template <typename L, int VPL>
-__device__ __noinline__ int select_exact(const L *row, int E, const float *bias, const GateArgs &a) {
-  const int lane = threadIdx.x & 31;
-  const int gsz = E / a.n_groups;
-  float l[VPL];
-  double c[VPL];
-  uint32_t avail = 0, on = 0;  // experts, and those not masked
-  float m = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane + 32 * i;
-    l[i] = -INFINITY;
-    if (e < E) {
-      l[i] = usable(load_logit(row + e));
-      avail |= 1u << i;
-      if (l[i] > -INFINITY) on |= 1u << i;
-    }
-    m = fmaxf(m, l[i]);
-  }
-  double z = 0.0;
-  if (a.score_fn == MOE_SCORE_SOFTMAX) {
-    m = warp_max(m);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if ((on >> i) & 1u) z += exp((double)l[i] - (double)m);
-    z = warp_sum(z);
-  }
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    c[i] = -INFINITY;
-    if ((on >> i) & 1u) {
-      c[i] = a.score_fn == MOE_SCORE_SOFTMAX ? exp((double)l[i] - (double)m) / z
-                                             : 1.0 / (1.0 + exp(-(double)l[i]));
-      if (bias) c[i] += clamp_bias(__ldg(bias + lane + 32 * i));
-    }
-  }
-  if (a.n_groups > 1) {
-    double mine = -INFINITY;
-    for (int g = 0; g < a.n_groups; ++g) {
-      uint32_t mask = 0;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (((on >> i) & 1u) && (lane + 32 * i) / gsz == g) mask |= 1u << i;
-      for (int r = 0; r < a.group_topn; ++r) {
-        double bv;
-        int bid;
-        warp_argmax<VPL>(c, mask, lane, bv, bid);
-        if (bid == INT_MAX) break;
-        if (lane == g) mine = r == 0 ? bv : mine + bv;
-        if ((bid & 31) == lane) mask &= ~(1u << (bid >> 5));
-      }
-    }
-    double gs[1] = {mine};
-    uint32_t free_ = lane < a.n_groups ? 1u : 0u, kept = 0;
-    for (int r = 0; r < a.topk_groups; ++r) {
-      double bv;
-      int bg;
-      warp_argmax<1>(gs, free_, lane, bv, bg);
-      kept |= 1u << bg;
-      if (bg == lane) free_ = 0;
-    }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (((avail >> i) & 1u) && !((kept >> ((lane + 32 * i) / gsz)) & 1u)) avail &= ~(1u << i);
-  }
-  int my_id = 0;
-  for (int j = 0; j < a.k; ++j) {
-    double bv;
-    int bid;
-    warp_argmax<VPL>(c, avail, lane, bv, bid);
-    if ((bid & 31) == lane) avail &= ~(1u << (bid >> 5));
-    if (lane == j) my_id = bid;
-  }
-  return my_id;
-}
-
-// ------------------------------------------------------------ fp32 selection
 // Float to an unsigned integer of the same order, and back.
 __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t u = __float_as_uint(x);
@@ -215,7 +129,131 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 __device__ __forceinline__ float unordered(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
+__device__ __forceinline__ uint64_t ordered(double x) {
+  const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);
+  return u ^ ((uint64_t)((int64_t)u >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double unordered(uint64_t k) {
+  return __longlong_as_double((int64_t)(k >> 63 ? k ^ 0x8000000000000000ull : ~k));
+}
 
+// What lane `lane` holds: experts [e0, e0 + n) of group grp, as part q of p.
+template <int V>
+struct Share {
+  int p, grp, q, e0, n;
+  uint32_t members;  // the lanes of this lane's group
+  __device__ __forceinline__ Share(int E, int n_groups, int lane) {
+    const int gsz = E / n_groups;
+    p = 32 / n_groups;
+    grp = lane / p;
+    q = lane - grp * p;
+    const bool has = grp < n_groups && q * V < gsz;
+    e0 = has ? grp * gsz + q * V : 0;
+    n = has ? min(V, gsz - q * V) : 0;
+    members = (p == 32 ? kFull : ((1u << p) - 1u)) << (grp * p & 31);
+  }
+  // The largest x among the lanes of this lane's group.
+  template <typename K>
+  __device__ __forceinline__ K group_max(K x, int lane) const {
+    K best = x;
+    if ((p & (p - 1)) == 0) {
+      for (int off = p >> 1; off > 0; off >>= 1) {
+        const K o = __shfl_xor_sync(kFull, best, off);
+        best = o > best ? o : best;
+      }
+    } else {
+      for (int j = 1; j < p; ++j) {
+        const K o = __shfl_sync(kFull, x, (q + j < p ? lane + j : lane + j - p) & 31);
+        best = o > best ? o : best;
+      }
+    }
+    return best;
+  }
+};
+
+// The k chosen experts of one row, lane j < k returning the j-th: the scores
+// in fp64 (whose order as integers is theirs), the definition step by step.
+template <typename L, int V>
+__device__ __noinline__ int select_exact(const L *row, int E, const float *bias, const GateArgs &a) {
+  const int lane = threadIdx.x & 31;
+  const Share<V> sh(E, a.n_groups, lane);
+  uint64_t key[V];  // 0: none, 1: masked
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (i < sh.n) m = fmaxf(m, usable(load_logit(row + sh.e0 + i)));
+  double z = 0.0;
+  const bool softmax = a.score_fn == MOE_SCORE_SOFTMAX;
+  if (softmax) {
+    m = warp_max(m);
+    for (int i = 0; i < sh.n; ++i) {
+      const float l = usable(load_logit(row + sh.e0 + i));
+      if (l > -INFINITY) z += exp((double)l - (double)m);
+    }
+    z = warp_sum(z);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    key[i] = 0;
+    if (i < sh.n) {
+      key[i] = 1;
+      const float l = usable(load_logit(row + sh.e0 + i));
+      if (l > -INFINITY) {
+        double c = softmax ? exp((double)l - (double)m) / z : 1.0 / (1.0 + exp(-(double)l));
+        if (bias) c += clamp_bias(__ldg(bias + sh.e0 + i));
+        key[i] = ordered(c);
+      }
+    }
+  }
+  // the first of this lane's largest keys, those in `used` left out
+  auto head = [&](uint32_t used, int &at) {
+    uint64_t best = 0;
+    at = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (!((used >> i) & 1u) && key[i] > best) {
+        best = key[i];
+        at = i;
+      }
+    return best;
+  };
+  int at;
+  if (a.n_groups > 1) {
+    uint32_t used = 0;
+    double gs = -INFINITY;
+    for (int r = 0; r < a.group_topn; ++r) {
+      const uint64_t mine = head(used, at);
+      const uint64_t best = sh.group_max(mine, lane);
+      if (best > 1) gs = r == 0 ? unordered(best) : gs + unordered(best);
+      if (__ffs(__ballot_sync(kFull, mine == best) & sh.members) - 1 == lane) used |= 1u << at;
+    }
+    const uint64_t gk = ordered(gs);
+    int rank = 0;
+    for (int g = 0; g < a.n_groups; ++g) {
+      const uint64_t o = __shfl_sync(kFull, gk, g * sh.p);
+      if (o > gk || (o == gk && g < sh.grp)) ++rank;
+    }
+    if (rank >= a.topk_groups || sh.grp >= a.n_groups) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = 0;
+    }
+  }
+  uint32_t used = 0;
+  int my_id = 0;
+  for (int j = 0; j < a.k; ++j) {
+    const uint64_t mine = head(used, at);
+    const uint32_t hi = (uint32_t)(mine >> 32), lo = (uint32_t)mine;
+    const uint32_t top = __reduce_max_sync(kFull, hi);
+    const uint32_t low = __reduce_max_sync(kFull, hi == top ? lo : 0u);
+    const int src = __ffs(__ballot_sync(kFull, hi == top && lo == low)) - 1;
+    const int id = __shfl_sync(kFull, sh.e0 + at, src);
+    if (lane == j) my_id = id;
+    if (lane == src) used |= 1u << at;
+  }
+  return my_id;
+}
+
+// ------------------------------------------------------------ fp32 selection
 // Descending sort of V (a power of two) keys: Batcher's odd-even merge network.
 template <int V>
 __device__ __forceinline__ void sort_keys(uint32_t (&k)[V]) {
@@ -277,23 +315,18 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16 *p, int n, float (&
   }
 }
 
-// VPL: experts per lane of select_exact, ceil(E / 32) rounded up.
-template <typename L, int V, int VPL, bool VEC>
-__global__ void __launch_bounds__(256) gate_kernel(const L *__restrict__ logits, int64_t ld,
-                                                   int64_t T, int E,
-                                                   const float *__restrict__ bias, GateArgs a,
-                                                   int32_t *__restrict__ ids,
-                                                   float *__restrict__ w) {
+template <typename L, int V, bool VEC>
+__global__ void __launch_bounds__(256, V <= 8 ? 4 : 2)
+    gate_kernel(const L *__restrict__ logits, int64_t ld, int64_t T, int E,
+                const float *__restrict__ bias, GateArgs a, int32_t *__restrict__ ids,
+                float *__restrict__ w) {
   moe::pdl_wait();
   moe::pdl_trigger();
   const int lane = threadIdx.x & 31;
   const int64_t warp0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-  const int gsz = E / a.n_groups, p = 32 / a.n_groups;
-  const int grp = lane / p, q = lane - grp * p;
-  const bool has = grp < a.n_groups && q * V < gsz;  // this lane holds experts
-  const int e0 = has ? grp * gsz + q * V : 0;
-  const int n = has ? min(V, gsz - q * V) : 0;
+  const Share<V> sh(E, a.n_groups, lane);
+  const int e0 = sh.e0, n = sh.n;
   const bool softmax = a.score_fn == MOE_SCORE_SOFTMAX;
   // without bias and groups the scores' order is the logits'
   const bool by_logit = bias == nullptr && a.n_groups == 1;
@@ -340,7 +373,7 @@ __global__ void __launch_bounds__(256) gate_kernel(const L *__restrict__ logits,
     for (int i = 0; i < V; ++i) {
       float x = l[i];
       if (!by_logit) {
-        x = softmax ? c[i] * zinv : rcp_fast(1.0f + __expf(-l[i]));
+        x = softmax ? c[i] * zinv : rcp_fast(1.0f + exp2_fast(l[i] * -1.442695041f));
         if (bias != nullptr) x += b[i];
       }
       // a masked expert's key lies below every score's, that of no expert is 0
@@ -358,19 +391,9 @@ __global__ void __launch_bounds__(256) gate_kernel(const L *__restrict__ logits,
       for (int i = 0; i < V; ++i) k2[i] = key[i];
       float gs = 0.0f, size = 0.0f;
       bool any = false;
-      const uint32_t members = (p == 32 ? kFull : ((1u << p) - 1u)) << (grp * p & 31);
       for (int r = 0; r < a.group_topn; ++r) {
-        uint32_t h = k2[0];
-        if ((p & (p - 1)) == 0) {
-          for (int off = p >> 1; off > 0; off >>= 1) h = max(h, __shfl_xor_sync(kFull, h, off));
-        } else {
-          const uint32_t mine = h;
-          for (int j = 1; j < p; ++j) {
-            const int src = q + j < p ? lane + j : lane + j - p;
-            h = max(h, __shfl_sync(kFull, mine, src & 31));
-          }
-        }
-        const uint32_t same = __ballot_sync(kFull, k2[0] == h) & members;
+        const uint32_t h = sh.group_max(k2[0], lane);
+        const uint32_t same = __ballot_sync(kFull, k2[0] == h) & sh.members;
         if (h >= 2u * V) {
           const float x = unordered(h & ~(uint32_t)(V - 1));
           gs += x;
@@ -379,12 +402,12 @@ __global__ void __launch_bounds__(256) gate_kernel(const L *__restrict__ logits,
         }
         pop<V>(k2, lane == __ffs(same) - 1);
       }
-      const bool valid = grp < a.n_groups;
+      const bool valid = sh.grp < a.n_groups;
       if (!any) gs = -INFINITY;
       int rank = 0;
       for (int g = 0; g < a.n_groups; ++g) {
-        const float o = __shfl_sync(kFull, gs, g * p);
-        if (o > gs || (o == gs && g < grp)) ++rank;
+        const float o = __shfl_sync(kFull, gs, g * sh.p);
+        if (o > gs || (o == gs && g < sh.grp)) ++rank;
       }
       const bool keep = valid && rank < a.topk_groups;
       const float err = a.group_topn * s_err + (key_err + a.group_topn * 0x1p-23f) * size;
@@ -433,21 +456,25 @@ __global__ void __launch_bounds__(256) gate_kernel(const L *__restrict__ logits,
       }
     }
     if (!__all_sync(kFull, sure)) {
-      my_id = select_exact<L, VPL>(row, E, bias, a);
+      my_id = select_exact<L, V>(row, E, bias, a);
       if (lane < a.k) my_l = usable(load_logit(row + my_id));
     }
 
-    // weights, in fp32 with compensated differences and sums
+    // weights (lanes past k hold -inf and add nothing)
     float v = 0.0f;
+    if (softmax) {
+      // renormalised, the chosen experts may all be far below the row's largest
+      if (a.renormalize) m = max16(my_l);
+      v = exp_diff(my_l, m);
+    } else {
+      v = sigmoid32(my_l);
+      if (a.renormalize && !__any_sync(kFull, my_l >= kTinyLogit)) v = exp_diff(my_l, max16(my_l));
+    }
     if (a.renormalize) {
-      const float ml = warp_max(lane < a.k ? my_l : -INFINITY);
-      // (softmax: the chosen experts may all be far below the row's largest)
-      const bool rel = softmax || ml < kTinyLogit;
-      const float num = lane >= a.k ? 0.0f : rel ? exp_diff(my_l, ml) : sigmoid32(my_l);
-      const float den = warp_sum_compensated(num);
-      if (den > 0.0f) v = __fdiv_rn(num, den);
-    } else if (lane < a.k) {
-      v = softmax ? exp_diff(my_l, m) * zinv : sigmoid32(my_l);
+      const float den = sum16(v);
+      v = den > 0.0f ? v * rcp_fast(den) : 0.0f;
+    } else if (softmax) {
+      v *= zinv;
     }
     if (lane < a.k) {
       ids[t * a.k + lane] = my_id;
@@ -591,9 +618,11 @@ GateArgs args_of(const moe_gate_cfg *c) {
                   c->group_topn, c->renormalize, c->scale};
 }
 
-unsigned gate_grid(int64_t T) {
+// Blocks of 8 warps, a token each at a time: at most as many as are resident
+// together (per_sm of each SM), so that all warps take as many tokens.
+unsigned gate_grid(int64_t T, int per_sm) {
   int64_t blocks = (T + 7) / 8;
-  const int64_t cap = (int64_t)moe_host::sm_count() * 16;
+  const int64_t cap = (int64_t)moe_host::sm_count() * per_sm;
   return (unsigned)(blocks > cap ? cap : blocks);
 }
 
@@ -619,11 +648,9 @@ moe_status launch_gate(const void *logits, int64_t ld, int64_t T, int E, const f
   const int gsz = E / a.n_groups, p = 32 / a.n_groups;
   return by_size((gsz + p - 1) / p, [&](auto v) {
     constexpr int V = decltype(v)::value;
-    // experts per lane over the whole row: at most V, at least V / 2 where the
-    // groups fill the lanes, less where they do not
-    constexpr int VPL = V > 16 ? 16 : V;
     auto run = [&](auto kernel) {
-      return moe_host::launch_pdl(kernel, dim3(gate_grid(T)), dim3(256), 0, st, l, ld, T, E, bias, a,
+      return moe_host::launch_pdl(kernel, dim3(gate_grid(T, V <= 8 ? 4 : 2)), dim3(256), 0, st, l,
+                                  ld, T, E, bias, a,
                                   ids, w);
     };
     if constexpr (V >= 4) {
@@ -631,9 +658,9 @@ moe_status launch_gate(const void *logits, int64_t ld, int64_t T, int E, const f
       // in memory and none has a part of its V
       if (gsz % V == 0 && ld % 4 == 0 &&
           reinterpret_cast<uintptr_t>(logits) % (4 * sizeof(L)) == 0)
-        return run(gate_kernel<L, V, VPL, true>);
+        return run(gate_kernel<L, V, true>);
     }
-    return run(gate_kernel<L, V, VPL, false>);
+    return run(gate_kernel<L, V, false>);
   });
 }
 
@@ -643,7 +670,7 @@ moe_status launch_backward(const void *logits, int64_t ld, int64_t T, int E, con
                            cudaStream_t st) {
   return by_size((E + 31) / 32, [&](auto v) {
     constexpr int VPL = decltype(v)::value > 16 ? 16 : decltype(v)::value;
-    return moe_host::launch_pdl(gate_backward_kernel<L, VPL>, dim3(gate_grid(T)),
+    return moe_host::launch_pdl(gate_backward_kernel<L, VPL>, dim3(gate_grid(T, 8)),
                                 dim3(256), 0, st, static_cast<const L *>(logits), ld, T, E, ids, g,
                                 a, static_cast<L *>(out), status);
   });
