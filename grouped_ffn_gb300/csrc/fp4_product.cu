@@ -10,12 +10,13 @@
 // a segment of a few rows moves few bytes and wastes little of the tensor
 // core.  A segment of n rows is cut into ceil(n / 112) tiles of equal size.
 //
-// Per CTA (one per SM, 224 threads), a ring of 4 stages of 256 elements of K:
+// Per CTA (one per SM, 256 threads), a ring of 4 stages of 256 elements of K:
 //   warp 0     weights (one bulk copy) and rows (TMA boxes of 16 rows)
 //   warp 1     copies the stage's scales into TMEM (tcgen05.cp) and issues 8
 //              block-scaled MMAs of K = 64 (4 steps x 2 weight halves)
 //   warps 2-5  epilogue: TMEM lane = weight row, column = row of x
-//   warp 6     the rows' scales into the layout that tcgen05.cp reads
+//   warp 7     the rows' scales as they lie in memory (cp.async)
+//   warp 6     turns them into the layout that tcgen05.cp reads, in place
 // TMEM: two accumulators of 2 x 112 columns, 48 columns of scales.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -35,7 +36,7 @@ constexpr int kMaxRows = 112;  // rows of x in a tile
 constexpr int kBoxRows = 16;
 constexpr int kStages = 4;
 constexpr int kMaxSegs = 1024;
-constexpr int kThreads = 224;
+constexpr int kThreads = 256;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kAccCols = 2 * kMaxRows;
 constexpr int kScaleCol = 2 * kAccCols;  // 32 columns of weight scales, 16 of row scales
@@ -48,6 +49,7 @@ static_assert(kStageBytes % 1024 == 0 && kXOff % 1024 == 0, "swizzle atoms are 1
 struct __align__(8) Bars {
   uint64_t full[kStages];
   uint64_t empty[kStages];
+  uint64_t raw[kStages];
   uint64_t tfull[2];
   uint64_t tempty[2];
   uint64_t drain;
@@ -55,7 +57,9 @@ struct __align__(8) Bars {
 constexpr size_t kBarsOff = (size_t)kStages * kStageBytes;
 constexpr size_t kMiscOff = kBarsOff + sizeof(Bars);
 constexpr size_t kSegOff = kMiscOff + 24;
-constexpr size_t kSmemBytes = kSegOff + (size_t)(4 * kMaxSegs + 1) * 4 + 1024;
+constexpr size_t kOutOff = (kSegOff + (size_t)(3 * kMaxSegs + 2) * 4 + 15) / 16 * 16;
+constexpr int kOutWarpBytes = 16 * 64;  // an epilogue warp's 16 rows of 32 bf16
+constexpr size_t kSmemBytes = kOutOff + 4 * kOutWarpBytes + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of one SM");
 
 struct Params {
@@ -79,8 +83,30 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
       : "memory");
 }
 
+// BYTES (8 or 16) from global to shared memory; arrive_copied signals `bar`
+// once this thread's copies so far have landed.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES)
+               : "memory");
+}
+__device__ __forceinline__ void arrive_copied(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 __device__ __forceinline__ void fence_proxy_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// One lane of a whole warp.  TMA, tcgen05.cp and tcgen05.mma take their operands
+// from uniform registers: behind elect.sync the compiler knows that one thread
+// runs and issues them at once, behind a comparison of the lane it loops over
+// the active threads for each (8 MMAs and 12 copies: 1501 cycles against 584).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
+  return p != 0;
 }
 
 // 512 bytes of scales (32 rows of 16 bytes) to 4 TMEM columns, repeated in
@@ -121,15 +147,33 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
-__device__ __forceinline__ void store_out(float *p, float v) { *p = v; }
-__device__ __forceinline__ void store_out(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+// 16 TMEM lanes x 16 columns as four 8 x 8 pieces: lane L of the warp gets
+// lane L / 4 (r[0..1], r[4..5]) and L / 4 + 8 (r[2..3], r[6..7]), columns
+// 2 (L % 4) and the next (r[4..7]: 8 further on).
+__device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr));
+}
+
+// Four 8 x 8 bf16 pieces, transposed on the way: row i of a piece (its lane
+// 8 piece + i names the address) takes column i of the fragment.
+__device__ __forceinline__ void stmatrix_t(uint32_t saddr, uint32_t a, uint32_t b, uint32_t c,
+                                           uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared::cta.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                   saddr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
 
 // silu(g) u.  bf16 results: the fast exponential and division are far below
 // the rounding of the result; fp32 results take the accurate ones.
-__device__ __forceinline__ float swiglu(float g, float u, float *) {
+__device__ __forceinline__ float swiglu_accurate(float g, float u) {
   return g / (1.0f + expf(-g)) * u;
 }
-__device__ __forceinline__ float swiglu(float g, float u, __nv_bfloat16 *) {
+__device__ __forceinline__ float swiglu_fast(float g, float u) {
   return __fdividef(g, 1.0f + __expf(-g)) * u;
 }
 
@@ -142,7 +186,7 @@ struct Tile {
 // Tiles in order (segment, weight tile, row tile): CTAs side by side read the
 // same weight tile.  CTA b takes tiles b, b + grid, ...
 struct Walk {
-  const int32_t *pre, *lo, *hi, *ex;
+  const int32_t *pre, *off, *ex;
   int S, nbn;
   int64_t t, total;
 
@@ -159,13 +203,13 @@ struct Walk {
     }
     const int mt = pre[a + 1] - pre[a];
     const int r = (int)(t - (int64_t)pre[a] * nbn);
-    const int rows = hi[a] - lo[a];
+    const int rows = off[a + 1] - off[a];
     const int per = ((rows + mt - 1) / mt + 15) & ~15;  // <= 112, and (mt - 1) * per < rows
     Tile x;
     x.e = ex[a];
     x.nb = r / mt;
     const int m = r - x.nb * mt;
-    x.row0 = lo[a] + m * per;
+    x.row0 = off[a] + m * per;
     x.n = min(per, rows - m * per);
     return x;
   }
@@ -181,10 +225,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kMiscOff);
   volatile int32_t *abort_flag = reinterpret_cast<int32_t *>(smem + kMiscOff + 4);
   volatile int32_t *epi_ok = reinterpret_cast<int32_t *>(smem + kMiscOff + 8);
-  int32_t *lo = reinterpret_cast<int32_t *>(smem + kSegOff);
-  int32_t *hi = lo + kMaxSegs;
-  int32_t *ex = hi + kMaxSegs;
-  int32_t *pre = ex + kMaxSegs;  // [S + 1] row tiles before segment s
+  int32_t *off = reinterpret_cast<int32_t *>(smem + kSegOff);  // [S + 1] first rows
+  int32_t *pre = off + kMaxSegs + 1;                           // [S + 1] row tiles before s
+  int32_t *ex = pre + kMaxSegs + 1;                            // [S]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int32_t kid = moe::K_FP4_PRODUCT;
   constexpr int kScaleBytes = fp4::Fmt<FMT>::kScaleBytes;
@@ -195,6 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bars->full[i], 2);  // the producer and the rows' scales
       mbar_init(&bars->empty[i], 1);
+      mbar_init(&bars->raw[i], 32);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->tfull[i], 1);
@@ -225,8 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       else
         mt = (int)((b - a + kMaxRows - 1) / kMaxRows);
     }
-    lo[s] = (int)a;
-    hi[s] = (int)b;
+    off[s] = (int)a;
+    if (s == p.S - 1) off[p.S] = (int)b;
     ex[s] = e;
     pre[s] = mt;
   }
@@ -236,12 +280,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  Walk walk{pre, lo, hi, ex, p.S, p.nbn, (int64_t)blockIdx.x,
+  Walk walk{pre, off, ex, p.S, p.nbn, (int64_t)blockIdx.x,
             none ? 0 : (int64_t)pre[p.S] * p.nbn};
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
+    if (elect_one()) {
       prefetch_tmap(&tmap_x);
       const uint64_t pol = policy_evict_first();
       int stage = 0;
@@ -281,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    if (elect_one()) {
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
@@ -338,48 +382,70 @@ __global__ void __launch_bounds__(kThreads, 1)
       umma_commit(&bars->drain);
       mbar_wait_drain(&bars->drain, 0);
     }
-  } else if (warp == 6) {
-    // ------------------------------------------- the rows' scales, per stage
+  } else if (warp == 7) {
+    // ------------------------------- the rows' scales of a stage, row by row
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (; walk.valid() && ok; walk.next()) {
       const Tile ti = walk.tile();
+      const uint8_t *src = p.sf + (ti.row0 + lane) * p.sf_ld;
       for (int kb = 0; kb < p.nkb; ++kb) {
-        // rows lane, lane + 32, ...: this step's scale bytes of each
-        uint32_t v[4][kGroups];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = lane + 32 * j;
-#pragma unroll
-          for (int g = 0; g < kGroups; ++g) v[j][g] = 0;
-          if (r < ti.n) {
-            const uint32_t *src = reinterpret_cast<const uint32_t *>(
-                p.sf + (ti.row0 + r) * p.sf_ld + kb * kScaleBytes);
-            if constexpr (FMT == 1) {
-              const uint4 u = __ldg(reinterpret_cast<const uint4 *>(src));
-              v[j][0] = u.x;
-              v[j][1] = u.y;
-              v[j][2] = u.z;
-              v[j][3] = u.w;
-            } else {
-              const uint2 u = __ldg(reinterpret_cast<const uint2 *>(src));
-              v[j][0] = u.x;
-              v[j][1] = u.y;
-            }
-          }
-        }
         int got = 0;
         if (lane == 0)
           got = mbar_wait(&bars->empty[stage], phase ^ 1u, abort_flag, p.status, kid) ? 1 : 0;
-        if (!__shfl_sync(0xffffffffu, got, 0)) {
-          ok = false;
-          break;
+        ok = __shfl_sync(0xffffffffu, got, 0) != 0;
+        if (!ok) break;
+        // (scales past the tile's rows belong to columns that nobody reads)
+        uint8_t *dst = smem + (size_t)stage * kStageBytes + kXsOff + lane * kScaleBytes;
+        for (int j = 0; lane + 32 * j < ti.n; ++j)
+          copy_async<kScaleBytes>(dst + j * 32 * kScaleBytes,
+                                  src + (int64_t)(32 * j) * p.sf_ld + kb * kScaleBytes);
+        arrive_copied(&bars->raw[stage]);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
         }
-        uint8_t *dst = smem + (size_t)stage * kStageBytes + kXsOff + lane * 16;
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // before the CTA exits
+  } else if (warp == 6) {
+    // ---------------------------- ... into 512-byte groups of 4 bytes a row
+    // This is a warp of its own: its proxy fence would wait for loads in
+    // flight, a microsecond a stage.
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (; walk.valid() && ok; walk.next()) {
+      for (int kb = 0; kb < p.nkb; ++kb) {
+        int got = 0;
+        if (lane == 0)
+          got = mbar_wait(&bars->raw[stage], phase, abort_flag, p.status, kid) ? 1 : 0;
+        ok = __shfl_sync(0xffffffffu, got, 0) != 0;
+        if (!ok) break;
+        if (lane != 0) mbar_try_wait(&bars->raw[stage], phase);  // complete: acquires the copies
+        uint8_t *xs = smem + (size_t)stage * kStageBytes + kXsOff;
+        uint32_t v[4][kGroups];  // rows lane, lane + 32, ...
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint8_t *src = xs + (lane + 32 * j) * kScaleBytes;
+          if constexpr (FMT == 1) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(src);
+            v[j][0] = x.x;
+            v[j][1] = x.y;
+            v[j][2] = x.z;
+            v[j][3] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2 *>(src);
+            v[j][0] = x.x;
+            v[j][1] = x.y;
+          }
+        }
+        __syncwarp();  // all rows are read before the groups overwrite them
 #pragma unroll
         for (int g = 0; g < kGroups; ++g)
-          *reinterpret_cast<uint4 *>(dst + g * 512) = make_uint4(v[0][g], v[1][g], v[2][g], v[3][g]);
+          *reinterpret_cast<uint4 *>(xs + g * 512 + lane * 16) =
+              make_uint4(v[0][g], v[1][g], v[2][g], v[3][g]);
         fence_proxy_async_shared();  // tcgen05.cp reads them through the async proxy
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->full[stage]);
@@ -403,24 +469,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const float alpha = p.alpha ? __ldg(p.alpha + ti.e) : 1.0f;
       const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kAccCols);
-      const int col0 = ti.nb * (SWIGLU ? 128 : 256) + q * 32 + lane;
-      Y *out = static_cast<Y *>(p.out) + ti.row0 * p.out_n + col0;
+      const int colw = ti.nb * (SWIGLU ? 128 : 256) + q * 32;  // the warp's first column
+      if constexpr (sizeof(Y) == 4) {
+        // fp32: a lane's weight row is a column of out, 128 bytes a store
+        const int col0 = colw + lane;
+        Y *out = static_cast<Y *>(p.out) + ti.row0 * p.out_n + col0;
 #pragma unroll 1
-      for (int c = 0; c < ti.n; c += 16) {
-        uint32_t a[16], b[16];
-        tmem_ld16(tbase + c, a);
-        tmem_ld16(tbase + kMaxRows + c, b);
-        tmem_wait_ld();
+        for (int c = 0; c < ti.n; c += 16) {
+          uint32_t a[16], b[16];
+          tmem_ld16(tbase + c, a);
+          tmem_ld16(tbase + kMaxRows + c, b);
+          tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          if (c + i >= ti.n) break;
-          const float va = __uint_as_float(a[i]) * alpha, vb = __uint_as_float(b[i]) * alpha;
-          Y *o = out + (int64_t)(c + i) * p.out_n;
-          if (SWIGLU) {
-            if (col0 < p.out_n) store_out(o, swiglu(va, vb, (Y *)nullptr));
-          } else {
-            if (col0 < p.out_n) store_out(o, va);
-            if (col0 + 128 < p.out_n) store_out(o + 128, vb);
+          for (int i = 0; i < 16; ++i) {
+            if (c + i >= ti.n) break;
+            const float va = __uint_as_float(a[i]) * alpha, vb = __uint_as_float(b[i]) * alpha;
+            Y *o = out + (int64_t)(c + i) * p.out_n;
+            if (SWIGLU) {
+              if (col0 < p.out_n) *o = swiglu_accurate(va, vb);
+            } else {
+              if (col0 < p.out_n) *o = va;
+              if (col0 + 128 < p.out_n) o[128] = vb;
+            }
+          }
+        }
+      } else {
+        // bf16: 32 weight rows x 16 rows of x at a time, transposed through
+        // the warp's kilobyte of shared memory (row t in 64 bytes, 16-byte
+        // chunk c at c ^ (t / 2 % 4)), out in 16-byte stores
+        uint8_t *buf = smem + kOutOff + q * kOutWarpBytes;
+        const int piece = lane >> 3, st_row = (lane & 7) + (piece >> 1) * 8;
+        const uint32_t st = smem_u32(buf) + st_row * 64;
+        const int st_sw = (st_row >> 1) & 3;
+        Y *out = static_cast<Y *>(p.out) + ti.row0 * p.out_n;
+#pragma unroll 1
+        for (int c = 0; c < ti.n; c += 16) {
+          uint32_t v[2][2][8];  // [weight half][16 lanes][8]
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              tmem_ld_16x16(tbase + ((uint32_t)(16 * r) << 16) + h * kMaxRows + c, v[h][r]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int h = 0; h < (SWIGLU ? 1 : 2); ++h) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              uint32_t pk[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float x = __uint_as_float(v[h][r][2 * i]) * alpha;
+                float y = __uint_as_float(v[h][r][2 * i + 1]) * alpha;
+                if (SWIGLU) {
+                  x = swiglu_fast(x, __uint_as_float(v[1][r][2 * i]) * alpha);
+                  y = swiglu_fast(y, __uint_as_float(v[1][r][2 * i + 1]) * alpha);
+                }
+                pk[i] = pack_bf16x2(x, y);
+              }
+              stmatrix_t(st + (((2 * r + (piece & 1)) ^ st_sw) << 4), pk[0], pk[1], pk[2], pk[3]);
+            }
+            __syncwarp();
+            const int col = colw + h * 128 + (lane & 3) * 8;
+#pragma unroll
+            for (int it = 0; it < 2; ++it) {
+              const int t = it * 8 + (lane >> 2);
+              const uint4 x = *reinterpret_cast<const uint4 *>(
+                  buf + t * 64 + (((lane & 3) ^ ((t >> 1) & 3)) << 4));
+              if (c + t < ti.n && col < p.out_n)
+                *reinterpret_cast<uint4 *>(out + (int64_t)(c + t) * p.out_n + col) = x;
+            }
+            __syncwarp();
           }
         }
       }
