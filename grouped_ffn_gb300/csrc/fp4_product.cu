@@ -15,8 +15,9 @@
 //   warp 1     copies the stage's scales into TMEM (tcgen05.cp) and issues 8
 //              block-scaled MMAs of K = 64 (4 steps x 2 weight halves)
 //   warps 2-5  epilogue: TMEM lane = weight row, column = row of x
-//   warp 7     the rows' scales as they lie in memory (cp.async)
-//   warp 6     turns them into the layout that tcgen05.cp reads, in place
+//   warp 7     the rows' scales into the layout that tcgen05.cp reads, loaded
+//              four stages ahead in registers
+//   warp 6     orders those stores before the tensor core's reads
 // TMEM: two accumulators of 2 x 112 columns, 48 columns of scales.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -81,17 +82,6 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
       " [%0], [%1], %2, [%3], %4;" ::"r"(smem_u32(dst)),
       "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
       : "memory");
-}
-
-// BYTES (8 or 16) from global to shared memory; arrive_copied signals `bar`
-// once this thread's copies so far have landed.
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void *dst, const void *src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES)
-               : "memory");
-}
-__device__ __forceinline__ void arrive_copied(uint64_t *bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 __device__ __forceinline__ void fence_proxy_async_shared() {
@@ -238,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bars->full[i], 2);  // the producer and the rows' scales
       mbar_init(&bars->empty[i], 1);
-      mbar_init(&bars->raw[i], 32);
+      mbar_init(&bars->raw[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->tfull[i], 1);
@@ -383,72 +373,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_drain(&bars->drain, 0);
     }
   } else if (warp == 7) {
-    // ------------------------------- the rows' scales of a stage, row by row
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (; walk.valid() && ok; walk.next()) {
-      const Tile ti = walk.tile();
-      const uint8_t *src = p.sf + (ti.row0 + lane) * p.sf_ld;
-      for (int kb = 0; kb < p.nkb; ++kb) {
-        int got = 0;
-        if (lane == 0)
-          got = mbar_wait(&bars->empty[stage], phase ^ 1u, abort_flag, p.status, kid) ? 1 : 0;
-        ok = __shfl_sync(0xffffffffu, got, 0) != 0;
-        if (!ok) break;
-        // (scales past the tile's rows belong to columns that nobody reads)
-        uint8_t *dst = smem + (size_t)stage * kStageBytes + kXsOff + lane * kScaleBytes;
-        for (int j = 0; lane + 32 * j < ti.n; ++j)
-          copy_async<kScaleBytes>(dst + j * 32 * kScaleBytes,
-                                  src + (int64_t)(32 * j) * p.sf_ld + kb * kScaleBytes);
-        arrive_copied(&bars->raw[stage]);
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");  // before the CTA exits
-  } else if (warp == 6) {
-    // ---------------------------- ... into 512-byte groups of 4 bytes a row
-    // This is a warp of its own: its proxy fence would wait for loads in
-    // flight, a microsecond a stage.
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (; walk.valid() && ok; walk.next()) {
-      for (int kb = 0; kb < p.nkb; ++kb) {
-        int got = 0;
-        if (lane == 0)
-          got = mbar_wait(&bars->raw[stage], phase, abort_flag, p.status, kid) ? 1 : 0;
-        ok = __shfl_sync(0xffffffffu, got, 0) != 0;
-        if (!ok) break;
-        if (lane != 0) mbar_try_wait(&bars->raw[stage], phase);  // complete: acquires the copies
-        uint8_t *xs = smem + (size_t)stage * kStageBytes + kXsOff;
-        uint32_t v[4][kGroups];  // rows lane, lane + 32, ...
+    // ------------------------------------------- the rows' scales, per stage
+    uint32_t v[kStages][4][kGroups];
+    Tile ti{};
+    int kb = 0;
+    bool more = walk.valid();
+    if (more) ti = walk.tile();
+    const int64_t n_tiles = more ? (walk.total - walk.t + gridDim.x - 1) / gridDim.x : 0;
+    auto load = [&](uint32_t (&u)[4][kGroups]) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint8_t *src = xs + (lane + 32 * j) * kScaleBytes;
+      for (int j = 0; j < 4; ++j) {  // rows lane, lane + 32, ...
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) u[j][g] = 0;
+        const int r = lane + 32 * j;
+        if (more && r < ti.n) {
+          const uint8_t *src = p.sf + (ti.row0 + r) * p.sf_ld + kb * kScaleBytes;
           if constexpr (FMT == 1) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(src);
-            v[j][0] = x.x;
-            v[j][1] = x.y;
-            v[j][2] = x.z;
-            v[j][3] = x.w;
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(src));
+            u[j][0] = x.x;
+            u[j][1] = x.y;
+            u[j][2] = x.z;
+            u[j][3] = x.w;
           } else {
-            const uint2 x = *reinterpret_cast<const uint2 *>(src);
-            v[j][0] = x.x;
-            v[j][1] = x.y;
+            const uint2 x = __ldg(reinterpret_cast<const uint2 *>(src));
+            u[j][0] = x.x;
+            u[j][1] = x.y;
           }
         }
-        __syncwarp();  // all rows are read before the groups overwrite them
+      }
+      if (more && ++kb == p.nkb) {
+        kb = 0;
+        walk.next();
+        more = walk.valid();
+        if (more) ti = walk.tile();
+      }
+    };
+#pragma unroll
+    for (int d = 0; d < kStages; ++d) load(v[d]);
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int64_t left = n_tiles * p.nkb; left > 0 && ok; left -= kStages, phase ^= 1u) {
+#pragma unroll
+      for (int d = 0; d < kStages; ++d) {
+        if (d >= left || !ok) break;
+        int got = 0;
+        if (lane == 0)
+          got = mbar_wait(&bars->empty[d], phase ^ 1u, abort_flag, p.status, kid) ? 1 : 0;
+        ok = __shfl_sync(0xffffffffu, got, 0) != 0;
+        if (!ok) break;
+        uint8_t *dst = smem + (size_t)d * kStageBytes + kXsOff + lane * 16;
 #pragma unroll
         for (int g = 0; g < kGroups; ++g)
-          *reinterpret_cast<uint4 *>(xs + g * 512 + lane * 16) =
-              make_uint4(v[0][g], v[1][g], v[2][g], v[3][g]);
-        fence_proxy_async_shared();  // tcgen05.cp reads them through the async proxy
+          *reinterpret_cast<uint4 *>(dst + g * 512) =
+              make_uint4(v[d][0][g], v[d][1][g], v[d][2][g], v[d][3][g]);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->full[stage]);
+        if (lane == 0) mbar_arrive(&bars->raw[d]);
+        load(v[d]);
+      }
+    }
+  } else if (warp == 6) {
+    // The proxy fence between those stores and tcgen05.cp, in a warp of its
+    // own: it would also wait for warp 7's loads in flight.
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      const int64_t n_tiles =
+          walk.valid() ? (walk.total - walk.t + gridDim.x - 1) / gridDim.x : 0;
+      for (int64_t left = n_tiles * p.nkb; left > 0; --left) {
+        if (!mbar_wait(&bars->raw[stage], phase, abort_flag, p.status, kid)) break;
+        fence_proxy_async_shared();
+        mbar_arrive(&bars->full[stage]);
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1u;
