@@ -33,35 +33,40 @@ namespace {
 
 using namespace umma;
 
-constexpr int kMaxRows = 112;  // rows of x in a tile
+constexpr int kSlotRows = 112;  // rows of x that one accumulator slot holds
 constexpr int kBoxRows = 16;
-constexpr int kStages = 4;
 constexpr int kMaxSegs = 1024;
-constexpr int kThreads = 256;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kAccCols = 2 * kMaxRows;
-constexpr int kScaleCol = 2 * kAccCols;  // 32 columns of weight scales, 16 of row scales
+constexpr int kSlotCols = 2 * kSlotRows;
+constexpr int kScaleCol = 2 * kSlotCols;  // 32 columns of weight scales, up to 32 of row scales
+constexpr int kOutWarpBytes = 16 * 64;    // an epilogue warp's 16 rows of 32 bf16
 
-constexpr int kXOff = fp4::kTileCodes + 4096;   // rows' codes within a stage
-constexpr int kXsOff = kXOff + kMaxRows * 128;  // rows' scales: 4 groups of 512 bytes
-constexpr int kStageBytes = kXsOff + 4 * 512;
-static_assert(kStageBytes % 1024 == 0 && kXOff % 1024 == 0, "swizzle atoms are 1024 bytes");
-
-struct __align__(8) Bars {
-  uint64_t full[kStages];
-  uint64_t empty[kStages];
-  uint64_t raw[kStages];
-  uint64_t tfull[2];
-  uint64_t tempty[2];
-  uint64_t drain;
+// Shared memory of tiles of up to ROWS rows (112 or 224).
+template <int ROWS>
+struct Cfg {
+  static constexpr int kStages = ROWS == 112 ? 4 : 3;
+  static constexpr int kBlocks = (ROWS + 127) / 128;  // 128-row blocks of row scales
+  static constexpr int kEpiWarps = ROWS == 112 ? 4 : 8;
+  static constexpr int kThreads = 128 + 32 * kEpiWarps;
+  static constexpr int kXOff = fp4::kTileCodes + 4096;  // rows' codes within a stage
+  static constexpr int kXsOff = kXOff + ROWS * 128;     // rows' scales, 4 groups a block
+  static constexpr int kStageBytes = kXsOff + kBlocks * 4 * 512;
+  struct __align__(8) Bars {
+    uint64_t full[kStages];
+    uint64_t empty[kStages];
+    uint64_t raw[kStages];
+    uint64_t tfull[2];
+    uint64_t tempty[2];
+    uint64_t drain;
+  };
+  static constexpr size_t kBarsOff = (size_t)kStages * kStageBytes;
+  static constexpr size_t kMiscOff = kBarsOff + sizeof(Bars);
+  static constexpr size_t kSegOff = kMiscOff + 24;
+  static constexpr size_t kOutOff = (kSegOff + (size_t)(3 * kMaxSegs + 2) * 4 + 15) / 16 * 16;
+  static constexpr size_t kSmemBytes = kOutOff + kEpiWarps * kOutWarpBytes + 1024;
+  static_assert(kStageBytes % 1024 == 0 && kXOff % 1024 == 0, "swizzle atoms are 1024 bytes");
+  static_assert(kSmemBytes <= 232448, "shared memory of one SM");
 };
-constexpr size_t kBarsOff = (size_t)kStages * kStageBytes;
-constexpr size_t kMiscOff = kBarsOff + sizeof(Bars);
-constexpr size_t kSegOff = kMiscOff + 24;
-constexpr size_t kOutOff = (kSegOff + (size_t)(3 * kMaxSegs + 2) * 4 + 15) / 16 * 16;
-constexpr int kOutWarpBytes = 16 * 64;  // an epilogue warp's 16 rows of 32 bf16
-constexpr size_t kSmemBytes = kOutOff + 4 * kOutWarpBytes + 1024;
-static_assert(kSmemBytes <= 232448, "shared memory of one SM");
 
 struct Params {
   const int32_t *seg_offsets, *seg_expert;
@@ -194,7 +199,7 @@ struct Walk {
     const int mt = pre[a + 1] - pre[a];
     const int r = (int)(t - (int64_t)pre[a] * nbn);
     const int rows = off[a + 1] - off[a];
-    const int per = ((rows + mt - 1) / mt + 15) & ~15;  // <= 112, and (mt - 1) * per < rows
+    const int per = ((rows + mt - 1) / mt + 15) & ~15;  // <= ROWS, and (mt - 1) * per < rows
     Tile x;
     x.e = ex[a];
     x.nb = r / mt;
@@ -205,17 +210,22 @@ struct Walk {
   }
 };
 
-template <int FMT, bool SWIGLU, typename Y>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int FMT, bool SWIGLU, typename Y, int ROWS>
+__global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap tmap_x, const Params p) {
+  using C = Cfg<ROWS>;
+  using Bars = typename C::Bars;
+  constexpr int kStages = C::kStages, kStageBytes = C::kStageBytes, kXOff = C::kXOff,
+                kXsOff = C::kXsOff, kThreads = C::kThreads, kBlocks = C::kBlocks,
+                kEpiThreads = 32 * C::kEpiWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  Bars *bars = reinterpret_cast<Bars *>(smem + kBarsOff);
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kMiscOff);
-  volatile int32_t *abort_flag = reinterpret_cast<int32_t *>(smem + kMiscOff + 4);
-  volatile int32_t *epi_ok = reinterpret_cast<int32_t *>(smem + kMiscOff + 8);
-  int32_t *off = reinterpret_cast<int32_t *>(smem + kSegOff);  // [S + 1] first rows
+  Bars *bars = reinterpret_cast<Bars *>(smem + C::kBarsOff);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kMiscOff);
+  volatile int32_t *abort_flag = reinterpret_cast<int32_t *>(smem + C::kMiscOff + 4);
+  volatile int32_t *epi_ok = reinterpret_cast<int32_t *>(smem + C::kMiscOff + 8);
+  int32_t *off = reinterpret_cast<int32_t *>(smem + C::kSegOff);  // [S + 1] first rows
   int32_t *pre = off + kMaxSegs + 1;                           // [S + 1] row tiles before s
   int32_t *ex = pre + kMaxSegs + 1;                            // [S]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -232,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->tfull[i], 1);
-      mbar_init(&bars->tempty[i], 128);
+      mbar_init(&bars->tempty[i], kEpiThreads);
     }
     mbar_init(&bars->drain, 1);
     *abort_flag = 0;
@@ -257,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (a < 0 || b > p.n_rows || e < 0 || e >= p.E)
         moe::report_error(p.status, MOE_ERR_DEVICE_INDEX, s, kid);
       else
-        mt = (int)((b - a + kMaxRows - 1) / kMaxRows);
+        mt = (int)((b - a + ROWS - 1) / ROWS);
     }
     off[s] = (int)a;
     if (s == p.S - 1) off[p.S] = (int)b;
@@ -317,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     if (elect_one()) {
       int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
+      uint32_t phase = 0, pe = 0;  // bit i: slot i's phase
       bool ok = true;
       for (; walk.valid() && ok; walk.next()) {
         const Tile ti = walk.tile();
@@ -326,9 +336,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         // E4M3 (0) at 23, M = 128 at 27
         const uint32_t idesc = (1u << 7) | (1u << 10) | ((nmma >> 3) << 17) |
                                ((FMT == 0 ? 1u : 0u) << 23) | (1u << 27);
-        if (!mbar_wait(&bars->tempty[acc], acc_phase ^ 1u, abort_flag, p.status, kid)) break;
+        // a tile of more than 112 rows takes both slots
+        const bool big = ROWS > kSlotRows && ti.n > kSlotRows;
+        if (big) acc = 0;
+        const int slot = acc, rows = big ? ROWS : kSlotRows;
+        if (!mbar_wait(&bars->tempty[slot], (pe >> slot & 1u) ^ 1u, abort_flag, p.status, kid)) break;
+        pe ^= 1u << slot;
+        if (big) {
+          if (!mbar_wait(&bars->tempty[1], (pe >> 1) ^ 1u, abort_flag, p.status, kid)) break;
+          pe ^= 2u;
+        }
         tc_fence_after();
-        const uint32_t d = tmem_base + (uint32_t)(acc * kAccCols);
+        const uint32_t d = tmem_base + (uint32_t)(slot * kSlotCols);
         const uint32_t sfa = tmem_base + kScaleCol, sfb = sfa + 32;
         for (int kb = 0; kb < p.nkb; ++kb) {
           if (!mbar_wait(&bars->full[stage], phase, abort_flag, p.status, kid)) {
@@ -345,7 +364,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               copy_scales(sfa + (h * kGroups + g) * 4,
                           sw + fp4::kTileCodes + (h * kGroups + g) * 512);
 #pragma unroll
-          for (int g = 0; g < kGroups; ++g) copy_scales(sfb + g * 4, sw + kXsOff + g * 512);
+          for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+              copy_scales(sfb + (g * kBlocks + b) * 4, sw + kXsOff + (g * kBlocks + b) * 512);
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
             // NV: a group a step; MX: two steps share a group's 4 bytes
@@ -354,9 +376,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t idesc_s = idesc | (id << 4) | (id << 29);
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              mma_fp4<FMT>(d + h * kMaxRows, sw128_desc(sw + h * 16384 + s * 32),
+              mma_fp4<FMT>(d + h * rows, sw128_desc(sw + h * 16384 + s * 32),
                            sw128_desc(sx + s * 32), idesc_s, sfa + (h * kGroups + g) * 4,
-                           sfb + g * 4, (kb | s) != 0 ? 1u : 0u);
+                           sfb + g * kBlocks * 4, (kb | s) != 0 ? 1u : 0u);
           }
           umma_commit(&bars->empty[stage]);
           if (++stage == kStages) {
@@ -365,24 +387,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) break;
-        umma_commit(&bars->tfull[acc]);
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
+        umma_commit(&bars->tfull[slot]);
+        acc = big ? 0 : acc ^ 1;
       }
       umma_commit(&bars->drain);
       mbar_wait_drain(&bars->drain, 0);
     }
   } else if (warp == 7) {
     // ------------------------------------------- the rows' scales, per stage
-    uint32_t v[kStages][4][kGroups];
+    constexpr int kPer = 4 * kBlocks;  // rows of a lane
+    uint32_t v[kStages][kPer][kGroups];
     Tile ti{};
     int kb = 0;
     bool more = walk.valid();
     if (more) ti = walk.tile();
     const int64_t n_tiles = more ? (walk.total - walk.t + gridDim.x - 1) / gridDim.x : 0;
-    auto load = [&](uint32_t (&u)[4][kGroups]) {
+    auto load = [&](uint32_t (&u)[kPer][kGroups]) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {  // rows lane, lane + 32, ...
+      for (int j = 0; j < kPer; ++j) {  // rows lane, lane + 32, ...
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) u[j][g] = 0;
         const int r = lane + 32 * j;
@@ -424,8 +446,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t *dst = smem + (size_t)d * kStageBytes + kXsOff + lane * 16;
 #pragma unroll
         for (int g = 0; g < kGroups; ++g)
-          *reinterpret_cast<uint4 *>(dst + g * 512) =
-              make_uint4(v[d][0][g], v[d][1][g], v[d][2][g], v[d][3][g]);
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b)
+            *reinterpret_cast<uint4 *>(dst + (g * kBlocks + b) * 512) = make_uint4(
+                v[d][4 * b][g], v[d][4 * b + 1][g], v[d][4 * b + 2][g], v[d][4 * b + 3][g]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->raw[d]);
         load(v[d]);
@@ -450,29 +474,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // -------------------------------------------------- epilogue warps 2..5
-    const int q = warp & 3;  // TMEM lane quadrant this warp may access
+    // ------------------------------------------- epilogue warps 2..5 (8..11)
+    const int q = warp & 3;          // TMEM lane quadrant this warp may access
+    const int part = warp >= 8;      // which of the quadrant's warps
+    constexpr int kStep = 16 * (C::kEpiWarps / 4);  // they take 16 rows in turn
     int acc = 0;
-    uint32_t acc_phase = 0;
+    uint32_t pf = 0;  // bit i: slot i's phase
     for (; walk.valid(); walk.next()) {
       const Tile ti = walk.tile();
+      const bool big = ROWS > kSlotRows && ti.n > kSlotRows;
+      if (big) acc = 0;
+      const int slot = acc, rows = big ? ROWS : kSlotRows;
       if (warp == 2 && lane == 0)
-        epi_ok[acc] = mbar_wait(&bars->tfull[acc], acc_phase, abort_flag, p.status, kid) ? 1 : 0;
-      epilogue_bar();
-      if (!epi_ok[acc]) break;
+        epi_ok[slot] = mbar_wait(&bars->tfull[slot], pf >> slot & 1u, abort_flag, p.status, kid) ? 1 : 0;
+      asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory");
+      if (!epi_ok[slot]) break;
+      pf ^= 1u << slot;
       tc_fence_after();
       const float alpha = p.alpha ? __ldg(p.alpha + ti.e) : 1.0f;
-      const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kAccCols);
+      const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(slot * kSlotCols);
       const int colw = ti.nb * (SWIGLU ? 128 : 256) + q * 32;  // the warp's first column
       if constexpr (sizeof(Y) == 4) {
         // fp32: a lane's weight row is a column of out, 128 bytes a store
         const int col0 = colw + lane;
         Y *out = static_cast<Y *>(p.out) + ti.row0 * p.out_n + col0;
 #pragma unroll 1
-        for (int c = 0; c < ti.n; c += 16) {
+        for (int c = 16 * part; c < ti.n; c += kStep) {
           uint32_t a[16], b[16];
           tmem_ld16(tbase + c, a);
-          tmem_ld16(tbase + kMaxRows + c, b);
+          tmem_ld16(tbase + rows + c, b);
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -491,19 +521,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         // bf16: 32 weight rows x 16 rows of x at a time, transposed through
         // the warp's kilobyte of shared memory (row t in 64 bytes, 16-byte
         // chunk c at c ^ (t / 2 % 4)), out in 16-byte stores
-        uint8_t *buf = smem + kOutOff + q * kOutWarpBytes;
+        uint8_t *buf = smem + C::kOutOff + (4 * part + q) * kOutWarpBytes;
         const int piece = lane >> 3, st_row = (lane & 7) + (piece >> 1) * 8;
         const uint32_t st = smem_u32(buf) + st_row * 64;
         const int st_sw = (st_row >> 1) & 3;
         Y *out = static_cast<Y *>(p.out) + ti.row0 * p.out_n;
 #pragma unroll 1
-        for (int c = 0; c < ti.n; c += 16) {
+        for (int c = 16 * part; c < ti.n; c += kStep) {
           uint32_t v[2][2][8];  // [weight half][16 lanes][8]
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-              tmem_ld_16x16(tbase + ((uint32_t)(16 * r) << 16) + h * kMaxRows + c, v[h][r]);
+              tmem_ld_16x16(tbase + ((uint32_t)(16 * r) << 16) + h * rows + c, v[h][r]);
           tmem_wait_ld();
 #pragma unroll
           for (int h = 0; h < (SWIGLU ? 1 : 2); ++h) {
@@ -537,9 +567,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc_fence_before();
-      mbar_arrive(&bars->tempty[acc]);
-      acc ^= 1;
-      if (acc == 0) acc_phase ^= 1u;
+      mbar_arrive(&bars->tempty[slot]);
+      if (big) mbar_arrive(&bars->tempty[1]);
+      acc = big ? 0 : acc ^ 1;
     }
   }
   __syncthreads();
@@ -550,6 +580,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ host
+// Above this many rows a segment on average, tiles of up to 224 rows.
+constexpr int kBigRows = 64;
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -564,30 +597,33 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-template <int FMT, bool SWIGLU, typename Y>
-moe_status launch(const CUtensorMap &m, const Params &p, int64_t max_tiles, cudaStream_t st) {
+template <int FMT, bool SWIGLU, typename Y, int ROWS>
+moe_status launch(const CUtensorMap &m, const Params &p, cudaStream_t st) {
   constexpr int kMaxDevices = 64;
   static bool done[kMaxDevices] = {false};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
   if (dev < 0 || dev >= kMaxDevices || !done[dev]) {
-    if (cudaFuncSetAttribute(product_kernel<FMT, SWIGLU, Y>,
+    if (cudaFuncSetAttribute(product_kernel<FMT, SWIGLU, Y, ROWS>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)kSmemBytes) != cudaSuccess)
+                             (int)Cfg<ROWS>::kSmemBytes) != cudaSuccess)
       return MOE_ERR_CUDA;
     if (dev >= 0 && dev < kMaxDevices) done[dev] = true;
   }
   int64_t grid = moe_host::sm_count();
+  const int64_t max_tiles = ((p.n_rows + ROWS - 1) / ROWS + p.S) * p.nbn;
   if (max_tiles < grid) grid = max_tiles;
-  return moe_host::launch_pdl(product_kernel<FMT, SWIGLU, Y>, dim3((unsigned)grid), dim3(kThreads),
-                              kSmemBytes, st, m, p);
+  return moe_host::launch_pdl(product_kernel<FMT, SWIGLU, Y, ROWS>, dim3((unsigned)grid),
+                              dim3(Cfg<ROWS>::kThreads), Cfg<ROWS>::kSmemBytes, st, m, p);
 }
 
 template <int FMT, bool SWIGLU>
-moe_status launch_type(const CUtensorMap &m, const Params &p, int64_t max_tiles, int32_t out_type,
-                       cudaStream_t st) {
-  return out_type == MOE_F32 ? launch<FMT, SWIGLU, float>(m, p, max_tiles, st)
-                             : launch<FMT, SWIGLU, __nv_bfloat16>(m, p, max_tiles, st);
+moe_status launch_type(const CUtensorMap &m, const Params &p, int32_t out_type, cudaStream_t st) {
+  const bool big = p.n_rows > (int64_t)p.S * kBigRows;
+  if (out_type == MOE_F32)
+    return big ? launch<FMT, SWIGLU, float, 224>(m, p, st) : launch<FMT, SWIGLU, float, 112>(m, p, st);
+  return big ? launch<FMT, SWIGLU, __nv_bfloat16, 224>(m, p, st)
+             : launch<FMT, SWIGLU, __nv_bfloat16, 112>(m, p, st);
 }
 
 }  // namespace
@@ -610,7 +646,7 @@ extern "C" moe_status moe_grouped_product_fp4(const uint8_t *codes, const uint8_
   Params p{};
   p.nkb = (K + fp4::kStepElems - 1) / fp4::kStepElems;
   p.nbn = swi ? (N / 2 + 127) / 128 : (N + 255) / 256;
-  const int64_t max_tiles = ((n_rows + kMaxRows - 1) / kMaxRows + S) * p.nbn;
+  const int64_t max_tiles = ((n_rows + kSlotRows - 1) / kSlotRows + S) * p.nbn;
   if (max_tiles >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
   if (!seg_offsets || !seg_expert || !w_packed) return MOE_ERR_INVALID_ARG;
   if (moe_status s = moe_host::check_ws(ws, ws_bytes, moe::kStatusBytes)) return s;
@@ -645,8 +681,8 @@ extern "C" moe_status moe_grouped_product_fp4(const uint8_t *codes, const uint8_
   p.out_n = swi ? N / 2 : N;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (fmt == MOE_FP4_MX)
-    return swi ? launch_type<0, true>(m, p, max_tiles, out_type, st)
-               : launch_type<0, false>(m, p, max_tiles, out_type, st);
-  return swi ? launch_type<1, true>(m, p, max_tiles, out_type, st)
-             : launch_type<1, false>(m, p, max_tiles, out_type, st);
+    return swi ? launch_type<0, true>(m, p, out_type, st)
+               : launch_type<0, false>(m, p, out_type, st);
+  return swi ? launch_type<1, true>(m, p, out_type, st)
+             : launch_type<1, false>(m, p, out_type, st);
 }

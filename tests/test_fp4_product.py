@@ -163,6 +163,22 @@ def test_product(case, fmt, out_t):
     assert torch.equal(again[lo:hi], out[lo:hi])
 
 
+LONG = [  # many rows a segment: tiles of more than 112 rows, mixed with small ones
+    ((300, 0, 113, 112, 224, 225, 1, 700), 3, 4, 264, 288, False, True),
+    ((129, 448, 16, 97, 336), 0, 2, 272, 512, True, True),
+    ((1000, 240), 0, 3, 1040, 160, False, False),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out_t", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("case", LONG)
+def test_long_segments(case, fmt, out_t):
+    test_product(case, fmt, out_t)
+    test_exact_sums(case, fmt)
+
+
 @pytest.mark.gpu
 def test_nan_stays_in_its_row():
     m = moe()
