@@ -19,7 +19,40 @@
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kVec = 16;  // elements per thread: one NV block, half an MX block
+constexpr int kVec = 32;  // elements a thread quantizes: one MX block, two NV blocks
+
+// Pieces of rows, flat over (row, piece): thread i of a chunk of rows finds its
+// row by a multiplication (a 64-bit division costs more than the rest of a
+// piece).  Exact for i < 2^31; longer inputs take several chunks (grid.y).
+struct Pieces {
+  int64_t rows, chunk;  // all rows, rows a chunk
+  uint32_t per_row, mul, shift;
+
+  static Pieces of(int64_t rows, int per_row) {
+    Pieces p;
+    p.rows = rows;
+    p.per_row = (uint32_t)per_row;
+    p.chunk = ((int64_t)1 << 30) / per_row;
+    if (p.chunk > rows) p.chunk = rows;
+    // per_row in (2^(L-1), 2^L]: q = i * ceil(2^(31+L) / per_row) >> (31+L),
+    // off by less than i * 2^-31 / per_row < 1 / per_row
+    uint32_t L = 0;
+    while (((uint64_t)1 << L) < (uint64_t)per_row) ++L;
+    p.mul = (uint32_t)((((uint64_t)1 << (31 + L)) + per_row - 1) / per_row);
+    p.shift = 31 + L;
+    return p;
+  }
+  unsigned chunks() const { return (unsigned)((rows + chunk - 1) / chunk); }
+  __device__ __forceinline__ uint32_t total() const {  // of this chunk
+    const int64_t left = rows - blockIdx.y * chunk;
+    return (uint32_t)(left < chunk ? left : chunk) * per_row;
+  }
+  __device__ __forceinline__ void at(uint32_t i, int64_t &row, int &piece) const {
+    const uint32_t q = (uint32_t)((uint64_t)i * mul >> shift);
+    row = blockIdx.y * chunk + q;
+    piece = (int)(i - q * per_row);
+  }
+};
 
 __device__ __forceinline__ float pow2f(int e) {  // e in [-127, 127]
   return e > -127 ? __int_as_float((127 + e) << 23) : __int_as_float(1 << 22);
@@ -47,51 +80,43 @@ __device__ __forceinline__ float e4m3_value(uint32_t code) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3)));
 }
 
-// 16 elements of a row and the largest magnitude among them, as fp32 bits.
-struct Elems {
-  float v[kVec];
-  __device__ __forceinline__ void load(const float *p) {
-    const float4 *q = reinterpret_cast<const float4 *>(p);
+// N consecutive elements of a row.
+template <int N>
+__device__ __forceinline__ void load_elems(const float *p, float (&v)[N]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 f = __ldcs(q + i);
-      v[4 * i] = f.x;
-      v[4 * i + 1] = f.y;
-      v[4 * i + 2] = f.z;
-      v[4 * i + 3] = f.w;
+  for (int i = 0; i < N / 4; ++i) {
+    const float4 f = __ldcs(reinterpret_cast<const float4 *>(p) + i);
+    v[4 * i] = f.x;
+    v[4 * i + 1] = f.y;
+    v[4 * i + 2] = f.z;
+    v[4 * i + 3] = f.w;
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_elems(const __nv_bfloat16 *p, float (&v)[N]) {
+  uint4 u[N / 8];
+#pragma unroll
+  for (int i = 0; i < N / 8; ++i) u[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+#pragma unroll
+  for (int i = 0; i < N / 8; ++i) {
+    const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      v[8 * i + 2 * c] = __uint_as_float(w[c] << 16);
+      v[8 * i + 2 * c + 1] = __uint_as_float(w[c] & 0xFFFF0000u);
     }
   }
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
-    const uint4 *q = reinterpret_cast<const uint4 *>(p);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 u = moe::ld_stream_u4(q + i);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        v[8 * i + 2 * c] = __uint_as_float(w[c] << 16);
-        v[8 * i + 2 * c + 1] = __uint_as_float(w[c] & 0xFFFF0000u);
-      }
-    }
-  }
-  __device__ __forceinline__ uint32_t amax_bits() const {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    return m;
-  }
-};
+}
 
-// Codes (8 bytes) and the scale byte of one thread's 16 elements; m is the
-// block's largest magnitude.
-template <int FMT, bool WIDE>
-__device__ __forceinline__ uint2 quantize16(const Elems &x, uint32_t m, int scale_exp,
-                                            uint32_t &scale) {
-  float y[kVec];
-  if (m >= 0x7F800000u) {  // an infinity or NaN: the whole block reads back as NaN
-    scale = fp4::Fmt<FMT>::kScaleBad;
-    return make_uint2(0, 0);
-  }
+// Codes (N / 8 words) and the scale byte of a block of N elements.
+template <int FMT, bool WIDE, int N>
+__device__ __forceinline__ uint32_t quantize_block(const float *x, int scale_exp, uint32_t *w) {
+  uint32_t m = 0;  // the largest magnitude, as fp32 bits
+#pragma unroll
+  for (int i = 0; i < N; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  uint32_t scale;
+  float y[N];
+  bool zero = false;
   if (FMT == 0) {
     // the smallest e in [-127, 127] with amax <= 6 * 2^e: amax = M 2^q gives
     // q - 2, plus one when M > 1.5
@@ -99,64 +124,70 @@ __device__ __forceinline__ uint2 quantize16(const Elems &x, uint32_t m, int scal
     scale = (uint32_t)(e + 127);
     const float inv = pow2f(-e);
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) y[i] = x.v[i] * inv;
+    for (int i = 0; i < N; ++i) y[i] = x[i] * inv;
   } else {
     const float down = pow2f(-scale_exp);
     const float a = __uint_as_float(m) * down;
     const float sixth = WIDE ? div_to_odd(a, 6.0f) : __fdiv_rn(a, 6.0f);
     scale = __nv_cvt_float_to_fp8(sixth, __NV_SATFINITE, __NV_E4M3);
-    if (scale == 0) return make_uint2(0, 0);
+    zero = scale == 0;
     const float s = e4m3_value(scale);
     if (WIDE) {
 #pragma unroll
-      for (int i = 0; i < kVec; ++i)
-        y[i] = copysignf(div_to_odd(fabsf(x.v[i]) * down, s), x.v[i]);
+      for (int i = 0; i < N; ++i) y[i] = copysignf(div_to_odd(fabsf(x[i]) * down, s), x[i]);
     } else {
       // a multiple of 2^-18 nearest to x / s: codes' borders are such
       // multiples, and any other quotient is further from them than the
       // reciprocal's error and this rounding together (|y| > 6 saturates)
       const float inv = __frcp_rn(s) * down;
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) y[i] = __fadd_rn(__fmaf_rn(x.v[i], inv, 48.0f), -48.0f);
+      for (int i = 0; i < N; ++i) y[i] = __fadd_rn(__fmaf_rn(x[i], inv, 48.0f), -48.0f);
     }
   }
-  uint32_t w[2] = {0, 0};
 #pragma unroll
-  for (int i = 0; i < kVec / 2; ++i)
-    w[i / 4] |= e2m1x2(y[2 * i], y[2 * i + 1]) << (8 * (i % 4));
-  return make_uint2(w[0], w[1]);
+  for (int i = 0; i < N / 8; ++i) {
+    w[i] = 0;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      w[i] |= e2m1x2(y[8 * i + 2 * c], y[8 * i + 2 * c + 1]) << (8 * c);
+  }
+  const bool bad = m >= 0x7F800000u;  // an infinity or NaN: the block reads back as NaN
+  if (bad) scale = fp4::Fmt<FMT>::kScaleBad;
+  if (bad || zero) {
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) w[i] = 0;
+  }
+  return scale;
 }
 
 // Rows of x to codes and scales.  k == 0: row t to row t.  k > 0: row t once
 // to each of its k dispatched rows dest_row[t*k + j] (-1: dropped).
-// One thread per 16 elements, flat over (row, piece).
+// One thread per 32 elements, a 16-byte store of codes for each destination.
 template <typename X, int FMT>
 __global__ void __launch_bounds__(kThreads)
-    quantize_kernel(const X *__restrict__ x, int64_t ldx, int64_t T, int K, int k,
+    quantize_kernel(const X *__restrict__ x, int64_t ldx, Pieces pieces, int K, int k,
                     const int32_t *__restrict__ dest_row, int64_t n_rows, int scale_exp,
                     uint8_t *__restrict__ codes, uint8_t *__restrict__ sf, int sf_ld,
                     int32_t *status) {
   moe::pdl_wait();
   moe::pdl_trigger();
-  const int per_row = K / kVec;  // even: the two halves of an MX block sit in neighbouring lanes
-  const int64_t total = T * per_row;
-  const int64_t stride = (int64_t)gridDim.x * kThreads;
+  constexpr bool WIDE = sizeof(X) == 4;
+  const uint32_t total = pieces.total(), stride = gridDim.x * kThreads;
   const int nsf = K / fp4::Fmt<FMT>::kBlock;
-  for (int64_t i0 = (int64_t)blockIdx.x * kThreads; i0 < total; i0 += stride) {
-    const int64_t i = i0 + threadIdx.x;
-    const bool on = i < total;
-    const int64_t t = on ? i / per_row : 0;
-    const int piece = on ? (int)(i - t * per_row) : 0;
-    Elems e;
-    uint32_t m = 0;
-    if (on) {
-      e.load(x + t * ldx + (int64_t)piece * kVec);
-      m = e.amax_bits();
+  for (uint32_t i = blockIdx.x * kThreads + threadIdx.x; i < total; i += stride) {
+    int64_t t;
+    int piece;
+    pieces.at(i, t, piece);
+    float v[kVec];
+    load_elems<kVec>(x + t * ldx + (int64_t)piece * kVec, v);
+    uint32_t w[4], scale;
+    if constexpr (FMT == 0) {
+      scale = quantize_block<FMT, WIDE, 32>(v, scale_exp, w);
+    } else {
+      scale = quantize_block<FMT, WIDE, 16>(v, scale_exp, w);
+      scale |= quantize_block<FMT, WIDE, 16>(v + 16, scale_exp, w + 2) << 8;
     }
-    if (FMT == 0) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    if (!on) continue;
-    uint32_t scale;
-    const uint2 q = quantize16<FMT, sizeof(X) == 4>(e, m, scale_exp, scale);
+    const uint4 q = make_uint4(w[0], w[1], w[2], w[3]);
     const int n_dst = k == 0 ? 1 : k;
     for (int j = 0; j < n_dst; ++j) {
       int64_t r = t;
@@ -168,32 +199,15 @@ __global__ void __launch_bounds__(kThreads)
           continue;
         }
       }
-      *reinterpret_cast<uint2 *>(codes + r * (K / 2) + piece * 8) = q;
+      *reinterpret_cast<uint4 *>(codes + r * (K / 2) + piece * 16) = q;
       uint8_t *srow = sf + r * sf_ld;
-      if (FMT == 1) srow[piece] = (uint8_t)scale;
-      if (FMT == 0 && !(piece & 1)) srow[piece >> 1] = (uint8_t)scale;
-      if (piece == per_row - 1)
+      if (FMT == 1)
+        reinterpret_cast<uint16_t *>(srow)[piece] = (uint16_t)scale;
+      else
+        srow[piece] = (uint8_t)scale;
+      if (piece == (int)pieces.per_row - 1)
         for (int c = nsf; c < sf_ld; ++c) srow[c] = 0;
     }
-  }
-}
-
-__device__ __forceinline__ void store16(float *p, const float (&v)[kVec]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    __stcs(reinterpret_cast<float4 *>(p) + i,
-           make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
-}
-__device__ __forceinline__ void store16(__nv_bfloat16 *p, const float (&v)[kVec]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t w[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * i + 2 * c], v[8 * i + 2 * c + 1]);
-      w[c] = *reinterpret_cast<uint32_t *>(&b);
-    }
-    __stcs(reinterpret_cast<uint4 *>(p) + i, make_uint4(w[0], w[1], w[2], w[3]));
   }
 }
 
@@ -205,31 +219,57 @@ __device__ __forceinline__ float2 e2m1x2_value(uint32_t code) {
   return __half22float2(*reinterpret_cast<__half2 *>(&h));
 }
 
+// A 16-byte store a piece (8 bf16 or 4 fp32 values, 4 or 2 bytes of codes), so
+// that a warp's stores cover whole lines; kDeqUnroll pieces in flight a thread.
+constexpr int kDeqUnroll = 4;
+
 template <typename Y, int FMT>
 __global__ void __launch_bounds__(kThreads)
     dequant_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ sf, int sf_ld,
-                   int64_t n_rows, int K, int scale_exp, Y *__restrict__ out) {
+                   Pieces pieces, int K, int scale_exp, Y *__restrict__ out) {
   moe::pdl_wait();
   moe::pdl_trigger();
-  const int per_row = K / kVec;
-  const int64_t total = n_rows * per_row;
-  const int64_t stride = (int64_t)gridDim.x * kThreads;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += stride) {
-    const int64_t r = i / per_row;
-    const int piece = (int)(i - r * per_row);
-    const uint2 q = __ldcs(reinterpret_cast<const uint2 *>(codes + r * (K / 2) + piece * 8));
-    const uint32_t c = __ldg(sf + r * sf_ld + (FMT == 1 ? piece : piece >> 1));
-    const float s = FMT == 1  ? e4m3_value(c) * pow2f(scale_exp)
-                    : c == 255 ? __int_as_float(0x7FFFFFFF)
-                               : pow2f((int)c - 127);
-    float v[kVec];
+  constexpr int N = 16 / sizeof(Y);  // elements a piece
+  const uint32_t total = pieces.total(), stride = gridDim.x * kThreads;
+  for (uint32_t i0 = blockIdx.x * kThreads + threadIdx.x; i0 < total; i0 += stride * kDeqUnroll) {
+    uint32_t q[kDeqUnroll], c[kDeqUnroll];
+    Y *dst[kDeqUnroll];
 #pragma unroll
-    for (int b = 0; b < 8; ++b) {
-      const float2 f = e2m1x2_value((b < 4 ? q.x >> (8 * b) : q.y >> (8 * b - 32)) & 0xFFu);
-      v[2 * b] = f.x * s;
-      v[2 * b + 1] = f.y * s;
+    for (int u = 0; u < kDeqUnroll; ++u) {
+      const uint32_t i = i0 + u * stride;
+      dst[u] = nullptr;
+      q[u] = c[u] = 0;
+      if (i < total) {
+        int64_t r;
+        int piece;
+        pieces.at(i, r, piece);
+        const uint8_t *src = codes + r * (K / 2) + piece * (N / 2);
+        q[u] = N == 8 ? __ldcs(reinterpret_cast<const uint32_t *>(src))
+                      : __ldcs(reinterpret_cast<const uint16_t *>(src));
+        c[u] = __ldg(sf + r * sf_ld + piece / (fp4::Fmt<FMT>::kBlock / N));
+        dst[u] = out + r * K + piece * N;
+      }
     }
-    store16(out + r * K + piece * kVec, v);
+#pragma unroll
+    for (int u = 0; u < kDeqUnroll; ++u) {
+      if (dst[u] == nullptr) continue;
+      const float s = FMT == 1       ? e4m3_value(c[u]) * pow2f(scale_exp)
+                      : c[u] == 255 ? __int_as_float(0x7FFFFFFF)
+                                     : pow2f((int)c[u] - 127);
+      uint32_t o[4];
+#pragma unroll
+      for (int b = 0; b < N / 2; ++b) {
+        const float2 f = e2m1x2_value(q[u] >> (8 * b) & 0xFFu);
+        if constexpr (N == 8) {
+          __nv_bfloat162 p = __floats2bfloat162_rn(f.x * s, f.y * s);
+          o[b] = *reinterpret_cast<uint32_t *>(&p);
+        } else {
+          o[2 * b] = __float_as_uint(f.x * s);
+          o[2 * b + 1] = __float_as_uint(f.y * s);
+        }
+      }
+      __stcs(reinterpret_cast<uint4 *>(dst[u]), make_uint4(o[0], o[1], o[2], o[3]));
+    }
   }
 }
 
@@ -293,28 +333,31 @@ moe_status check_shape(int64_t rows, int32_t K, int32_t fmt, int32_t scale_exp) 
   return MOE_OK;
 }
 
-unsigned flat_grid(int64_t threads) {
-  int64_t blocks = (threads + kThreads - 1) / kThreads;
-  const int64_t lim = (int64_t)moe_host::sm_count() * 32;
-  return (unsigned)(blocks > lim ? lim : blocks);
+// Blocks for the pieces of a chunk, unroll of them a thread and turn.
+dim3 pieces_grid(const Pieces &p, int unroll) {
+  const int64_t per = (int64_t)kThreads * unroll;
+  int64_t blocks = (p.chunk * p.per_row + per - 1) / per;
+  const int64_t lim = (int64_t)moe_host::sm_count() * 16;
+  return dim3((unsigned)(blocks > lim ? lim : blocks), p.chunks());
 }
 
 template <typename X, int FMT>
 moe_status launch_quantize(const void *x, int64_t ldx, int64_t T, int32_t K, int32_t k,
                            const int32_t *dest_row, int64_t n_rows, int32_t scale_exp,
                            uint8_t *codes, uint8_t *sf, int32_t *status, cudaStream_t st) {
-  return moe_host::launch_pdl(quantize_kernel<X, FMT>, dim3(flat_grid(T * (K / kVec))),
-                              dim3(kThreads), 0, st, static_cast<const X *>(x), ldx, T, (int)K,
-                              (int)k, dest_row, n_rows, (int)scale_exp, codes, sf,
+  const Pieces p = Pieces::of(T, K / kVec);
+  return moe_host::launch_pdl(quantize_kernel<X, FMT>, pieces_grid(p, 1), dim3(kThreads), 0, st,
+                              static_cast<const X *>(x), ldx, p, (int)K, (int)k, dest_row, n_rows, (int)scale_exp, codes, sf,
                               (int)moe_fp4_scale_ld(K, FMT), status);
 }
 
 template <typename Y, int FMT>
 moe_status launch_dequant(const uint8_t *codes, const uint8_t *sf, int64_t n_rows, int32_t K,
                           int32_t scale_exp, void *out, cudaStream_t st) {
-  return moe_host::launch_pdl(dequant_kernel<Y, FMT>, dim3(flat_grid(n_rows * (K / kVec))),
-                              dim3(kThreads), 0, st, codes, sf, (int)moe_fp4_scale_ld(K, FMT),
-                              n_rows, (int)K, (int)scale_exp, static_cast<Y *>(out));
+  const Pieces p = Pieces::of(n_rows, K / (16 / (int)sizeof(Y)));
+  return moe_host::launch_pdl(dequant_kernel<Y, FMT>, pieces_grid(p, kDeqUnroll), dim3(kThreads), 0,
+                              st, codes, sf, (int)moe_fp4_scale_ld(K, FMT), p, (int)K,
+                              (int)scale_exp, static_cast<Y *>(out));
 }
 
 }  // namespace
