@@ -10,6 +10,7 @@ count, through torch; the library itself allocates nothing.
 
 from __future__ import annotations
 
+import math
 from typing import Optional
 
 import torch
@@ -31,7 +32,9 @@ class MoELayer:
                  replica_refine: bool = False, gather: bool = False,
                  masked_cap: Optional[int] = None,
                  fp8_dispatch: bool = False, fuse_shared: bool = True,
-                 ffn_schedule: Optional[moe.FfnSchedule] = None):
+                 ffn_schedule: Optional[moe.FfnSchedule] = None,
+                 gate: Optional[moe.GateCfg] = None, gate_bias: Optional[torch.Tensor] = None,
+                 fp4: Optional[int] = None, fp4_scale_exp: tuple = (-6, -6)):
         """replica_relax=(c_num, c_den) chooses each assignment's replica by
         locality-preferred water-filling with load bounds C = c_num/c_den
         (moe_route_replicas); None keeps the fixed replica rule.
@@ -51,7 +54,19 @@ class MoELayer:
         otherwise it is a second launch.  The results are the same bits.
         ffn_schedule (packed weights, contiguous layout) sets the grouped
         FFN's tile schedule; None is the library's default.  Every schedule
-        gives the same bits."""
+        gives the same bits.
+        gate=cfg routes with moe_gate and that configuration (score_fn,
+        n_groups, topk_groups and group_topn above are then unused);
+        gate_bias fp32 [E] is its balance bias, kept as self.gate_bias and
+        moved by update_gate_bias().
+        fp4=MOE_FP4_MX or MOE_FP4_NV runs the experts in FP4: the weights are
+        quantized and packed once, here; token rows are quantized on their
+        way into the dispatched rows (moe_permute_fp4), and both GEMMs are
+        grouped FP4 products with the hidden rows quantized in between.
+        fp4_scale_exp: NV's tensor scale exponents of token rows and of
+        hidden rows (full precision for blocks whose largest magnitude lies
+        in [2^(e-3), 2^(e+11)]).  A shared expert needs the routed experts'
+        width and runs as one more segment.  Contiguous layout only."""
         if (gather or masked_cap is not None) and not packed:
             raise ValueError("gather and fixed-capacity modes stream packed weights")
         if gather and (masked_cap is not None or fp8_dispatch):
@@ -60,6 +75,18 @@ class MoELayer:
             raise ValueError("fixed-capacity layout: cap >= 1, fixed replica rule")
         if ffn_schedule is not None and (not packed or gather or masked_cap is not None):
             raise ValueError("ffn_schedule applies to the packed contiguous FFN")
+        if fp4 is not None:
+            if gather or masked_cap is not None or fp8_dispatch or ffn_schedule is not None:
+                raise ValueError("fp4 experts: contiguous layout, no gather, FP8 dispatch or schedule")
+            if fp4 not in (moe.MOE_FP4_MX, moe.MOE_FP4_NV):
+                raise ValueError("fp4: MOE_FP4_MX or MOE_FP4_NV")
+            if shared_w_gate_up is not None and tuple(shared_w_gate_up.shape[1:]) != (2 * I, H):
+                raise ValueError("fp4 experts: the shared expert needs the routed experts' width")
+        if gate is not None and gate.k != k:
+            raise ValueError("gate.k must be k")
+        if gate_bias is not None and gate is None:
+            raise ValueError("gate_bias belongs to a gate")
+        self.gate, self.gate_bias, self.fp4 = gate, gate_bias, fp4
         self.ffn_schedule = ffn_schedule
         self.gather = gather
         self.masked_cap = masked_cap
@@ -69,9 +96,15 @@ class MoELayer:
         self.packed = packed
         self.fuse_shared = bool(
             fuse_shared and shared_w_gate_up is not None and packed and not gather
-            and masked_cap is None and not fp8_dispatch
+            and fp4 is None and masked_cap is None and not fp8_dispatch
             and tuple(shared_w_gate_up.shape[1:]) == (2 * I, H))
-        if self.fuse_shared:
+        self.fp4_shared = fp4 is not None and shared_w_gate_up is not None
+        if fp4 is not None:
+            self._init_fp4(w_gate_up, w_down, shared_w_gate_up, shared_w_down, fp4_scale_exp,
+                           max_tokens, device)
+            w_gate_up = w_down = shared_w_gate_up = shared_w_down = None
+            self.shared_I = I if self.fp4_shared else 0
+        elif self.fuse_shared:
             # one packed tensor holds the routed experts and, as expert E,
             # the shared one, so that one launch serves both
             gu = torch.empty((E + 1, 2 * I, H), dtype=w_gate_up.dtype, device=w_gate_up.device)
@@ -101,17 +134,19 @@ class MoELayer:
         # dispatched rows: T*k in the contiguous layout (+ T for a fused
         # shared expert), S*cap in the fixed one
         rows = A if masked_cap is None else S * masked_cap
-        if self.fuse_shared:
+        if self.fuse_shared or self.fp4_shared:
             rows = A + max_tokens
         self.slot = torch.empty(A, **i32)
         self.seg_counts = torch.empty(S, **i32)
-        self.seg_offsets = torch.empty(S + 1, **i32)
+        # (with one more entry for a shared expert's segment of an FP4 layer)
+        self._seg_offsets_all = torch.empty(S + 2, **i32)
+        self.seg_offsets = self._seg_offsets_all[:S + 1]
         self.dest_row = torch.empty(A, **i32)
         self.src_assign = torch.empty(rows, **i32)
         self.rank_counts = torch.empty(R, **i32)
         self.masked_m = torch.zeros(S, **i32)
         self.n_dropped = torch.zeros(1, **i32)
-        self.x_perm = torch.empty(0 if gather else rows, H, **bf)
+        self.x_perm = torch.empty(0 if gather or fp4 is not None else rows, H, **bf)
         if fp8_dispatch:
             self.xq = torch.empty(rows, H, dtype=torch.uint8, device=dev)
             self.x_scale = torch.empty(rows, H // 128, dtype=torch.float32, device=dev)
@@ -133,7 +168,7 @@ class MoELayer:
         self.replica_refine = replica_refine
         self.inter_node = torch.zeros(1, **i32)
         self.messages = torch.zeros(2, **i32)
-        if self.fuse_shared:
+        if self.fuse_shared or fp4 is not None:
             pass
         elif shared_w_gate_up is not None:
             self.shared_I = shared_w_gate_up.shape[1] // 2
@@ -155,7 +190,7 @@ class MoELayer:
         # without replicas, packed weights, the contiguous layout
         small = max_tokens * k * H * 2 <= self.PREFETCH_MAX_DISPATCH
         self.prefetch_bytes = self.PREFETCH_BYTES if (
-            small and packed and not gather and masked_cap is None and replica_relax is None
+            small and fp4 is None and packed and not gather and masked_cap is None and replica_relax is None
             and placement.n_slots == placement.n_experts) else 0
         self._ev_route = torch.cuda.Event()
         # the layout scan takes up to 1024 assignments in one CTA, which then
@@ -165,6 +200,85 @@ class MoELayer:
             (4 if replica_relax is not None else 0) + (1 if replica_refine else 0) - \
             (1 if gather else 0) + \
             (1 if fp8_dispatch else 0) + (1 if self.prefetch_bytes else 0) - (1 if one_tile else 0)
+        if fp4 is not None:
+            # two products and the hidden rows' quantization for the FFN
+            self.launches_per_step += 2 + (1 if self.fp4_shared else 0)
+
+    @staticmethod
+    def _quantize_experts(w, fmt):
+        """FP4 codes and scales [E, N, ..] of bf16 weights [E, N, K] and the
+        tensor scale exponent of each expert (NV: the smallest power of two
+        that keeps every block scale in range)."""
+        E, N, K = w.shape
+        codes = torch.empty(E, N, K // 2, dtype=torch.uint8, device=w.device)
+        sf = torch.empty(E, N, moe.moe_fp4_scale_ld(K, fmt), dtype=torch.uint8, device=w.device)
+        exps = []
+        for e in range(E):
+            x = 0
+            if fmt == moe.MOE_FP4_NV:
+                top = float(w[e].abs().max()) / (448.0 * 6.0)
+                x = max(-100, min(100, math.frexp(top)[1])) if top > 0.0 else 0
+            moe.moe_quantize_fp4(w[e], fmt, x, codes[e], sf[e])
+            exps.append(x)
+        return codes, sf, exps
+
+    def _init_fp4(self, w_gate_up, w_down, shared_gu, shared_dn, scale_exp, max_tokens, device):
+        fmt, dev = self.fp4, torch.device(device)
+        self.x_exp, self.h_exp = scale_exp if fmt == moe.MOE_FP4_NV else (0, 0)
+
+        def experts(w, shared, epilogue, row_exp):
+            w = w if shared is None else torch.cat((w, shared))
+            codes, sf, exps = self._quantize_experts(w, fmt)
+            alpha = torch.tensor([2.0 ** (x + row_exp) for x in exps], dtype=torch.float32)
+            return moe.pack_weights_fp4(codes, sf, fmt, epilogue), alpha.to(dev)
+
+        self.w_gate_up_fp4, self.alpha_gate_up = experts(w_gate_up, shared_gu, moe.MOE_EPI_SWIGLU,
+                                                         self.x_exp)
+        self.w_down_fp4, self.alpha_down = experts(w_down, shared_dn, moe.MOE_EPI_NONE, self.h_exp)
+        rows = max_tokens * self.k + (max_tokens if self.fp4_shared else 0)
+        self.x_codes, self.x_sf = moe.new_fp4(rows, self.H, fmt, dev)
+        self.h_codes, self.h_sf = moe.new_fp4(rows, self.I, fmt, dev)
+        se = self.placement.slot_expert
+        self._fp4_experts = torch.cat((se, se.new_tensor([self.E]))) if self.fp4_shared else se
+
+    def _ffn_fp4(self, x, T, A, stream, mark):
+        """Dispatch and both expert GEMMs in FP4; y_perm is written."""
+        fmt, rows = self.fp4, A + (T if self.fp4_shared else 0)
+        offs = self.seg_offsets
+        moe.moe_permute_fp4(x, self.k, self.dest_row[:A], fmt, self.x_exp, self.x_codes[:A],
+                            self.x_sf[:A], self.ws, stream)
+        if self.fp4_shared:
+            # rows [A, A + T) carry every token for the shared expert
+            moe.moe_quantize_fp4(x, fmt, self.x_exp, self.x_codes[A:rows], self.x_sf[A:rows], stream)
+            with torch.cuda.stream(stream or torch.cuda.current_stream()):
+                self._seg_offsets_all[-1:].fill_(rows)
+            offs = self._seg_offsets_all
+        mark("permute")
+        h = self.h[:rows]
+        moe.moe_grouped_product_fp4(self.x_codes[:rows], self.x_sf[:rows], offs, self._fp4_experts,
+                                    self.w_gate_up_fp4, self.alpha_gate_up, h, self.ws, stream)
+        moe.moe_quantize_fp4(h, fmt, self.h_exp, self.h_codes[:rows], self.h_sf[:rows], stream)
+        moe.moe_grouped_product_fp4(self.h_codes[:rows], self.h_sf[:rows], offs, self._fp4_experts,
+                                    self.w_down_fp4, self.alpha_down, self.y_perm[:rows], self.ws,
+                                    stream)
+
+    def update_gate_bias(self, rate: float, stream=None):
+        """Move the gate's balance bias against the last step's expert loads
+        (moe_gate_update_bias; placements without replicas)."""
+        if self.gate_bias is None or self.placement.n_slots != self.E:
+            raise ValueError("update_gate_bias needs a gate_bias and one slot an expert")
+        with torch.cuda.stream(stream or torch.cuda.current_stream()):
+            # slots are sorted by rank: loads in the experts' order
+            loads = self.seg_counts[self.placement.rep_slots.long()]
+            moe.moe_gate_update_bias(loads, self.gate_bias, rate, self.gate_bias)
+
+    def gate_backward(self, logits, grad_w, grad_logits, stream=None):
+        """Gradient of the last step's logits for a gradient grad_w [T, k] of
+        its weights (moe_gate_backward, the chosen experts held fixed)."""
+        if self.gate is None:
+            raise ValueError("gate_backward needs a gate")
+        moe.moe_gate_backward(logits, self.topk_ids[:logits.shape[0]], grad_w, self.gate,
+                              grad_logits, self.ws, stream)
 
     @staticmethod
     def _pack(w_gate_up, w_down):
@@ -199,7 +313,10 @@ class MoELayer:
             raise ValueError("more tokens than the layer was sized for")
         A = T * self.k
         ids, w = self.topk_ids[:T], self.topk_w[:T]
-        moe.moe_route(logits, self.cfg, ids, w, self.ws, stream)
+        if self.gate is not None:
+            moe.moe_gate(logits, self.gate_bias, self.gate, ids, w, stream)
+        else:
+            moe.moe_route(logits, self.cfg, ids, w, self.ws, stream)
         self._fork_prefetch(ids, stream)
         mark("route")
         if self.masked_cap is not None:
@@ -219,7 +336,9 @@ class MoELayer:
                                            self.src_assign[:A], self.rank_counts, self.ws, stream)
         mark("layout")
         self._fork_balance(stream)
-        if self.gather:
+        if self.fp4 is not None:
+            self._ffn_fp4(x, T, A, stream, mark)
+        elif self.gather:
             mark("permute")
             moe.moe_grouped_ffn_gather(x, self.k, self.src_assign[:A], self.seg_offsets,
                                        self.placement.slot_expert, self.w_gate_up, self.w_down,
@@ -245,7 +364,8 @@ class MoELayer:
             self._ffn(self.x_perm[:A], self.seg_offsets, self.placement.slot_expert,
                       self.w_gate_up, self.w_down, self.h[:A], self.y_perm[:A], self.ws, stream)
         mark("grouped_ffn")
-        shared = self.shared_output(T) if self.fuse_shared else self._shared(x, T, stream, mark)
+        shared = self.shared_output(T) if self.fuse_shared or self.fp4 is not None \
+            else self._shared(x, T, stream, mark)
         moe.moe_combine(self.y_perm[:A], self.dest_row[:A], w, y, self.ws, shared, stream)
         mark("combine")
         self._join_balance(stream, mark)
@@ -279,7 +399,7 @@ class MoELayer:
     def shared_output(self, T: int):
         """The shared expert's output rows [T, H] of the last step, or None
         when the layer has no shared expert."""
-        if self.fuse_shared:
+        if self.fuse_shared or self.fp4_shared:
             A = T * self.k
             return self.y_perm[A:A + T]
         return self.shared_y[:T] if self.shared_I else None
