@@ -9,7 +9,7 @@
 // One warp per token.  GB300 issues fp64 at a small fraction of the fp32 rate
 // and the choice needs more than fp32 only where two scores nearly meet, so
 // the warp chooses in fp32 with a bound on every score's error, and chooses
-// again in fp64 (select_exact) when a gap that decides something is within the
+// again in fp64 (exact_token) when a gap that decides something is within the
 // bounds: about one token in a thousand of a spread-out router.
 //
 // Layout: a group takes p = floor(32 / n_groups) neighbouring lanes and each
@@ -171,10 +171,31 @@ struct Share {
   }
 };
 
-// The k chosen experts of one row, lane j < k returning the j-th: the scores
-// in fp64 (whose order as integers is theirs), the definition step by step.
+// The weight of this lane's chosen expert with logit l (lanes past k hold -inf);
+// m and zinv: the row's largest logit and 1 / sum e^(l - m) (softmax scores).
+__device__ __forceinline__ float chosen_weight(const GateArgs &a, float l, float m, float zinv) {
+  float v;
+  if (a.score_fn == MOE_SCORE_SOFTMAX) {
+    // renormalised, the chosen experts may all be far below the row's largest
+    if (a.renormalize) m = max16(l);
+    v = exp_diff(l, m);
+    if (!a.renormalize) v *= zinv;
+  } else {
+    v = sigmoid32(l);
+    if (a.renormalize && !__any_sync(kFull, l >= kTinyLogit)) v = exp_diff(l, max16(l));
+  }
+  if (a.renormalize) {
+    const float den = sum16(v);
+    v = den > 0.0f ? v * rcp_fast(den) : 0.0f;
+  }
+  return a.scale * v;
+}
+
+// One row again: the scores in fp64 (whose order as integers is theirs), the
+// definition step by step; lane j < k writes the j-th choice.
 template <typename L, int V>
-__device__ __noinline__ int select_exact(const L *row, int E, const float *bias, const GateArgs &a) {
+__device__ __noinline__ void exact_token(const L *row, int E, const float *bias, const GateArgs &a,
+                                         int32_t *ids, float *w) {
   const int lane = threadIdx.x & 31;
   const Share<V> sh(E, a.n_groups, lane);
   uint64_t key[V];  // 0: none, 1: masked
@@ -250,7 +271,12 @@ __device__ __noinline__ int select_exact(const L *row, int E, const float *bias,
     if (lane == j) my_id = id;
     if (lane == src) used |= 1u << at;
   }
-  return my_id;
+  const float my_l = lane < a.k ? usable(load_logit(row + my_id)) : -INFINITY;
+  const float v = chosen_weight(a, my_l, m, z > 0.0 ? (float)(1.0 / z) : 0.0f);
+  if (lane < a.k) {
+    ids[lane] = my_id;
+    w[lane] = v;
+  }
 }
 
 // ------------------------------------------------------------ fp32 selection
@@ -342,143 +368,167 @@ __global__ void __launch_bounds__(256, V <= 8 ? 4 : 2)
   const float key_err = by_logit ? (V - 1) * 0x1p-23f : V * 0x1p-23f;
   const float score_err = by_logit ? 0.0f : softmax ? 1.2e-6f : 3e-7f;
 
-  for (int64_t t = warp0; t < T; t += nwarps) {
-    const L *row = logits + t * ld;
-    float l[V];
-    load_row<V, VEC>(row + e0, n, l);
-    float m = -INFINITY, zinv = 1.0f;
+  // Rows in doubt that the candidates do not settle are noted and come again
+  // after 32 rows, out of this loop.
+  for (int64_t first = warp0; first < T; first += 32 * nwarps) {
+    uint32_t doubtful = 0;
+    int64_t t = first;
+    for (int it = 0; it < 32 && t < T; ++it, t += nwarps) {
+      const L *row = logits + t * ld;
+      float l[V];
+      load_row<V, VEC>(row + e0, n, l);
+      float m = -INFINITY, zinv = 1.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) l[i] = usable(l[i]);
-    uint32_t key[V];
-    float c[V];
-    if (need_z) {
+      for (int i = 0; i < V; ++i) l[i] = usable(l[i]);
+      uint32_t key[V];
+      float c[V];
+      if (need_z) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
-      m = warp_max(m);
+        for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
+        m = warp_max(m);
 #pragma unroll
-      for (int i = 0; i < V; ++i) c[i] = exp_diff(l[i], m);
-      float part[V];
+        for (int i = 0; i < V; ++i) c[i] = exp_diff(l[i], m);
+        float part[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) part[i] = c[i];
+        for (int i = 0; i < V; ++i) part[i] = c[i];
 #pragma unroll
-      for (int s = V / 2; s > 0; s >>= 1)
+        for (int s = V / 2; s > 0; s >>= 1)
 #pragma unroll
-        for (int i = 0; i < s; ++i) part[i] += part[i + s];
-      float z = part[0];
+          for (int i = 0; i < s; ++i) part[i] += part[i + s];
+        float z = part[0];
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(kFull, z, off);
-      zinv = z > 0.0f ? __fdiv_rn(1.0f, z) : 0.0f;
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float x = l[i];
-      if (!by_logit) {
-        x = softmax ? c[i] * zinv : rcp_fast(1.0f + exp2_fast(l[i] * -1.442695041f));
-        if (bias != nullptr) x += b[i];
+        for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(kFull, z, off);
+        zinv = z > 0.0f ? __fdiv_rn(1.0f, z) : 0.0f;
       }
-      // a masked expert's key lies below every score's, that of no expert is 0
-      const uint32_t k = l[i] > -INFINITY ? ordered(x + 0.0f) & ~(uint32_t)(V - 1) : (uint32_t)V;
-      key[i] = i < n ? k | (uint32_t)(V - 1 - i) : 0u;
-    }
-    sort_keys<V>(key);
-    bool sure = true;
-    const float s_err = score_err * (softmax ? zinv : 1.0f);
-
-    if (a.n_groups > 1) {
-      // the group's group_topn largest scores, one round each
-      uint32_t k2[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) k2[i] = key[i];
-      float gs = 0.0f, size = 0.0f;
-      bool any = false;
-      for (int r = 0; r < a.group_topn; ++r) {
-        const uint32_t h = sh.group_max(k2[0], lane);
-        const uint32_t same = __ballot_sync(kFull, k2[0] == h) & sh.members;
-        if (h >= 2u * V) {
-          const float x = unordered(h & ~(uint32_t)(V - 1));
-          gs += x;
-          size += fabsf(x);
-          any = true;
+      for (int i = 0; i < V; ++i) {
+        float x = l[i];
+        if (!by_logit) {
+          x = softmax ? c[i] * zinv : rcp_fast(1.0f + exp2_fast(l[i] * -1.442695041f));
+          if (bias != nullptr) x += b[i];
         }
-        pop<V>(k2, lane == __ffs(same) - 1);
+        // a masked expert's key lies below every score's, that of no expert is 0
+        const uint32_t k = l[i] > -INFINITY ? ordered(x + 0.0f) & ~(uint32_t)(V - 1) : (uint32_t)V;
+        key[i] = i < n ? k | (uint32_t)(V - 1 - i) : 0u;
       }
-      const bool valid = sh.grp < a.n_groups;
-      if (!any) gs = -INFINITY;
-      int rank = 0;
-      for (int g = 0; g < a.n_groups; ++g) {
-        const float o = __shfl_sync(kFull, gs, g * sh.p);
-        if (o > gs || (o == gs && g < sh.grp)) ++rank;
-      }
-      const bool keep = valid && rank < a.topk_groups;
-      const float err = a.group_topn * s_err + (key_err + a.group_topn * 0x1p-23f) * size;
-      // the kept groups' least possible score against the others' largest
-      const uint32_t least = __reduce_min_sync(kFull, keep ? ordered(any ? gs - err : gs) : 0xFFFFFFFFu);
-      const uint32_t most =
-          __reduce_max_sync(kFull, valid && !keep ? ordered(any ? gs + err : gs) : 0u);
-      // (groups without an unmasked expert are exact ties, taken by id)
-      if (a.topk_groups < a.n_groups && least <= most && most != ordered(-INFINITY)) sure = false;
-      if (!keep) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = 0;
-      }
-    }
+      sort_keys<V>(key);
+      bool sure = true;
+      const float s_err = score_err * (softmax ? zinv : 1.0f);
 
-    uint32_t my_key = 0;
-    int my_src = 0;
-    for (int j = 0; j < a.k; ++j) {
-      // equal scores of several lanes: the lowest lane holds the lowest id
-      const uint32_t head = key[0] & ~(uint32_t)(V - 1);
-      const uint32_t top = __reduce_max_sync(kFull, head);
-      const int src = __ffs(__ballot_sync(kFull, head == top)) - 1;
-      const uint32_t won = __shfl_sync(kFull, key[0], src);
-      if (lane == j) {
-        my_key = won;
-        my_src = src;
+      if (a.n_groups > 1) {
+        // the group's group_topn largest scores, one round each
+        uint32_t k2[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) k2[i] = key[i];
+        float gs = 0.0f, size = 0.0f;
+        bool any = false;
+        for (int r = 0; r < a.group_topn; ++r) {
+          const uint32_t h = sh.group_max(k2[0], lane);
+          const uint32_t same = __ballot_sync(kFull, k2[0] == h) & sh.members;
+          if (h >= 2u * V) {
+            const float x = unordered(h & ~(uint32_t)(V - 1));
+            gs += x;
+            size += fabsf(x);
+            any = true;
+          }
+          pop<V>(k2, lane == __ffs(same) - 1);
+        }
+        const bool valid = sh.grp < a.n_groups;
+        if (!any) gs = -INFINITY;
+        int rank = 0;
+        for (int g = 0; g < a.n_groups; ++g) {
+          const float o = __shfl_sync(kFull, gs, g * sh.p);
+          if (o > gs || (o == gs && g < sh.grp)) ++rank;
+        }
+        const bool keep = valid && rank < a.topk_groups;
+        const float err = a.group_topn * s_err + (key_err + a.group_topn * 0x1p-23f) * size;
+        // the kept groups' least possible score against the others' largest
+        const uint32_t least = __reduce_min_sync(kFull, keep ? ordered(any ? gs - err : gs) : 0xFFFFFFFFu);
+        const uint32_t most =
+            __reduce_max_sync(kFull, valid && !keep ? ordered(any ? gs + err : gs) : 0u);
+        // (groups without an unmasked expert are exact ties, taken by id)
+        if (a.topk_groups < a.n_groups && least <= most && most != ordered(-INFINITY)) sure = false;
+        if (!keep) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) key[i] = 0;
+        }
       }
-      pop<V>(key, lane == src);
-    }
-    const uint32_t rest = __reduce_max_sync(kFull, key[0]);  // the best one left out
-    int my_id = __shfl_sync(kFull, e0, my_src) + (V - 1 - (int)(my_key & (V - 1)));
-    float my_l = -INFINITY;
-    if (lane < a.k) my_l = usable(load_logit(row + my_id));
-    // bf16 logits keep all their bits in a key: their order is exact
-    if (!(by_logit && sizeof(L) == 2)) {
-      const float my_b = bias != nullptr && lane < a.k ? __ldg(bias + my_id) : 0.0f;
-      uint32_t next = __shfl_down_sync(kFull, my_key, 1);
-      const float next_l = __shfl_down_sync(kFull, my_l, 1), next_b = __shfl_down_sync(kFull, my_b, 1);
-      if (lane == a.k - 1) next = rest;
-      if (lane < a.k && next >= 2u * V) {
+
+      uint32_t my_key = 0;
+      int my_src = 0;
+      auto take = [&](int j) {  // lane j receives the best key left
+        // equal scores of several lanes: the lowest lane holds the lowest id
+        const uint32_t head = key[0] & ~(uint32_t)(V - 1);
+        const uint32_t top = __reduce_max_sync(kFull, head);
+        const int src = __ffs(__ballot_sync(kFull, head == top)) - 1;
+        const uint32_t won = __shfl_sync(kFull, key[0], src);
+        if (lane == j) {
+          my_key = won;
+          my_src = src;
+        }
+        pop<V>(key, lane == src);
+      };
+      // Lane j < n: its key and the one after it may be the other way round
+      // (a call of the whole warp).
+      auto in_doubt = [&](int n) {
+        uint32_t next = __shfl_down_sync(kFull, my_key, 1);
+        const uint32_t rest = __reduce_max_sync(kFull, key[0]);  // the best one left out
+        if (lane == n - 1) next = rest;
         const float x = unordered(my_key & ~(uint32_t)(V - 1));
         const float y = unordered(next & ~(uint32_t)(V - 1));
-        const bool apart = x - (s_err + key_err * fabsf(x)) > y + (s_err + key_err * fabsf(y));
-        const bool tie = lane < a.k - 1 && my_l == next_l && my_b == next_b;
-        if (!apart && !tie) sure = false;
+        const bool apart = x - y > 2.0f * s_err + key_err * (fabsf(x) + fabsf(y));
+        return lane < n && next >= 2u * V && !apart;
+      };
+      for (int j = 0; j < a.k; ++j) take(j);
+      bool doubt = false;
+      // bf16 logits keep all their bits in a key: their order is exact
+      if (!(by_logit && sizeof(L) == 2)) doubt = __any_sync(kFull, in_doubt(a.k));
+      int n_cand = a.k;
+      if (doubt && (bias == nullptr || !softmax)) {
+        // four more candidates; a clear gap after them leaves the rest out
+        n_cand = min(a.k + 4, 32);
+        for (int j = a.k; j < n_cand; ++j) take(j);
+        const bool open = in_doubt(n_cand);  // (every lane takes part)
+        if (__any_sync(kFull, open && lane == n_cand - 1)) sure = false;
+      } else if (doubt) {
+        sure = false;  // a softmax's score takes the whole row again
+      }
+      int my_id = __shfl_sync(kFull, e0, my_src) + (V - 1 - (int)(my_key & (V - 1)));
+      float my_l = lane < n_cand && my_key != 0 ? usable(load_logit(row + my_id)) : -INFINITY;
+      if (doubt && sure) {
+        // one candidate a lane: the logits in order (scores rise with them)
+        // without a bias, else the scores in fp64; ties by id
+        double c = my_l;
+        if (bias != nullptr && my_l > -INFINITY)
+          c = 1.0 / (1.0 + exp(-(double)my_l)) + clamp_bias(__ldg(bias + my_id));
+        const int id = lane < n_cand && my_key != 0 ? my_id : 0x7FFFFFFF;
+        int rank = 0;
+        for (int j = 0; j < n_cand; ++j) {
+          const double oc = __shfl_sync(kFull, c, j);
+          const int oid = __shfl_sync(kFull, id, j);
+          if (oc > c || (oc == c && oid < id)) ++rank;
+        }
+        const float l0 = my_l;
+        for (int j = 0; j < n_cand; ++j) {
+          const int r = __shfl_sync(kFull, rank, j), oid = __shfl_sync(kFull, id, j);
+          const float ol = __shfl_sync(kFull, l0, j);
+          if (lane == r) {
+            my_id = oid;
+            my_l = ol;
+          }
+        }
+      }
+      if (lane >= a.k) my_l = -INFINITY;
+      if (!__all_sync(kFull, sure)) doubtful |= 1u << it;
+      const float v = chosen_weight(a, my_l, m, zinv);
+      if (lane < a.k) {
+        ids[t * a.k + lane] = my_id;
+        w[t * a.k + lane] = v;
       }
     }
-    if (!__all_sync(kFull, sure)) {
-      my_id = select_exact<L, V>(row, E, bias, a);
-      if (lane < a.k) my_l = usable(load_logit(row + my_id));
-    }
-
-    // weights (lanes past k hold -inf and add nothing)
-    float v = 0.0f;
-    if (softmax) {
-      // renormalised, the chosen experts may all be far below the row's largest
-      if (a.renormalize) m = max16(my_l);
-      v = exp_diff(my_l, m);
-    } else {
-      v = sigmoid32(my_l);
-      if (a.renormalize && !__any_sync(kFull, my_l >= kTinyLogit)) v = exp_diff(my_l, max16(my_l));
-    }
-    if (a.renormalize) {
-      const float den = sum16(v);
-      v = den > 0.0f ? v * rcp_fast(den) : 0.0f;
-    } else if (softmax) {
-      v *= zinv;
-    }
-    if (lane < a.k) {
-      ids[t * a.k + lane] = my_id;
-      w[t * a.k + lane] = a.scale * v;
+    for (; doubtful != 0; doubtful &= doubtful - 1) {
+      const int64_t u = first + (__ffs(doubtful) - 1) * nwarps;
+      exact_token<L, V>(logits + u * ld, E, bias, a, ids + u * a.k, w + u * a.k);
     }
   }
 }
