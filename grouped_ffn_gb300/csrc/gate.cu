@@ -191,6 +191,72 @@ __device__ __forceinline__ float chosen_weight(const GateArgs &a, float l, float
   return a.scale * v;
 }
 
+// ------------------------------------------------------------ two-float scores
+// A value as the unevaluated sum h + l of two floats: about 48 bits at the
+// fp32 rate (the fp64 exponential and division made a row cost 12 us).
+struct Two {
+  float h, l;
+};
+
+// e^(hi + lo) for -60 <= hi <= 0, |lo| <= ulp(hi): n = rint(hi / ln 2), r = hi +
+// lo - n ln 2 in two floats (ln 2 in three: 16 bits, so that n times it is exact,
+// 24 and 24), then Taylor's series, degrees 12 to 7 in fp32 and 6 to 0 in two
+// floats.  Relative error below 2^-45.
+__device__ __forceinline__ Two exp_two(float hi, float lo) {
+  const float n = rintf(hi * 1.4426950409f);
+  const float r1 = __fmaf_rn(-n, 0x1.62e4p-1f, hi);  // exact
+  const float p = __fmul_rn(n, 0x1.7f7d1cp-20f), pe = __fmaf_rn(n, 0x1.7f7d1cp-20f, -p);
+  float rh = __fsub_rn(r1, p);
+  const float bb = __fsub_rn(rh, r1);
+  const float e = __fsub_rn(__fsub_rn(r1, __fsub_rn(rh, bb)), __fadd_rn(p, bb));
+  float rl = __fadd_rn(e, __fsub_rn(lo, __fmaf_rn(n, 0x1.ef357ap-45f, pe)));
+  const float t = __fadd_rn(rh, rl);
+  rl = __fsub_rn(rl, __fsub_rn(t, rh));
+  rh = t;
+  float q = 1.0f / 479001600.0f;
+  q = __fmaf_rn(q, rh, 1.0f / 39916800.0f);
+  q = __fmaf_rn(q, rh, 1.0f / 3628800.0f);
+  q = __fmaf_rn(q, rh, 1.0f / 362880.0f);
+  q = __fmaf_rn(q, rh, 1.0f / 40320.0f);
+  q = __fmaf_rn(q, rh, 1.0f / 5040.0f);
+  // 1/6!, ..., 1/0! as two floats each
+  const float ch[7] = {0x1.6c16c2p-10f, 0x1.111112p-7f, 0x1.555556p-5f, 0x1.555556p-3f, 0.5f, 1.0f, 1.0f};
+  const float cl[7] = {-0x1.27d27ep-35f, -0x1.ddddep-32f, -0x1.555556p-30f, -0x1.555556p-28f, 0.0f, 0.0f, 0.0f};
+  Two a{q, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 7; ++i) {  // a = c + r a
+    const float ph = __fmul_rn(rh, a.h);
+    float pl = __fmaf_rn(rh, a.h, -ph);
+    pl = __fmaf_rn(rh, a.l, pl);
+    pl = __fmaf_rn(rl, a.h, pl);
+    const float sum = __fadd_rn(ch[i], ph);
+    a.l = __fadd_rn(__fsub_rn(ph, __fsub_rn(sum, ch[i])), __fadd_rn(pl, cl[i]));
+    a.h = sum;
+  }
+  const float scale = __int_as_float((127 + (int)n) << 23);
+  return Two{a.h * scale, a.l * scale};
+}
+
+// Scores to about 45 bits; far from zero, where two floats would leave their
+// range, in fp64.
+__device__ __noinline__ double exp_64(float hi, float lo) {
+  if (hi < -60.0f) return exp((double)hi + (double)lo);
+  const Two e = exp_two(hi, lo);
+  return (double)e.h + (double)e.l;
+}
+__device__ __noinline__ double sigmoid_64(float x) {
+  if (fabsf(x) > 60.0f) return 1.0 / (1.0 + exp(-(double)x));
+  const Two e = exp_two(-fabsf(x), 0.0f);
+  const float dh = __fadd_rn(1.0f, e.h);
+  const float dl = __fadd_rn(__fsub_rn(e.h, __fsub_rn(dh, 1.0f)), e.l);
+  const float r = __frcp_rn(dh);
+  const float rl = __fmul_rn(r, __fmaf_rn(-dl, r, __fmaf_rn(-dh, r, 1.0f)));  // 1 / d = r + rl
+  if (x >= 0.0f) return (double)r + (double)rl;
+  const float ph = __fmul_rn(e.h, r);
+  const float pl = __fmaf_rn(e.l, r, __fmaf_rn(e.h, rl, __fmaf_rn(e.h, r, -ph)));
+  return (double)ph + (double)pl;
+}
+
 // One row again: the scores in fp64 (whose order as integers is theirs), the
 // definition step by step; lane j < k writes the j-th choice.
 template <typename L, int V>
@@ -205,14 +271,18 @@ __device__ __noinline__ void exact_token(const L *row, int E, const float *bias,
     if (i < sh.n) m = fmaxf(m, usable(load_logit(row + sh.e0 + i)));
   double z = 0.0;
   const bool softmax = a.score_fn == MOE_SCORE_SOFTMAX;
+  auto exp_of = [&](float l) {  // e^(l - m)
+    if (l == -INFINITY) return 0.0;
+    const float d = __fsub_rn(l, m), bb = __fsub_rn(d, l);
+    if (d < -800.0f) return 0.0;
+    return exp_64(d, __fsub_rn(__fsub_rn(l, __fsub_rn(d, bb)), __fadd_rn(m, bb)));
+  };
   if (softmax) {
     m = warp_max(m);
-    for (int i = 0; i < sh.n; ++i) {
-      const float l = usable(load_logit(row + sh.e0 + i));
-      if (l > -INFINITY) z += exp((double)l - (double)m);
-    }
+    for (int i = 0; i < sh.n; ++i) z += exp_of(usable(load_logit(row + sh.e0 + i)));
     z = warp_sum(z);
   }
+  const double zinv = z > 0.0 ? 1.0 / z : 0.0;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     key[i] = 0;
@@ -220,7 +290,7 @@ __device__ __noinline__ void exact_token(const L *row, int E, const float *bias,
       key[i] = 1;
       const float l = usable(load_logit(row + sh.e0 + i));
       if (l > -INFINITY) {
-        double c = softmax ? exp((double)l - (double)m) / z : 1.0 / (1.0 + exp(-(double)l));
+        double c = softmax ? exp_of(l) * zinv : sigmoid_64(l);
         if (bias) c += clamp_bias(__ldg(bias + sh.e0 + i));
         key[i] = ordered(c);
       }
@@ -272,7 +342,7 @@ __device__ __noinline__ void exact_token(const L *row, int E, const float *bias,
     if (lane == src) used |= 1u << at;
   }
   const float my_l = lane < a.k ? usable(load_logit(row + my_id)) : -INFINITY;
-  const float v = chosen_weight(a, my_l, m, z > 0.0 ? (float)(1.0 / z) : 0.0f);
+  const float v = chosen_weight(a, my_l, m, (float)zinv);
   if (lane < a.k) {
     ids[lane] = my_id;
     w[lane] = v;
@@ -500,7 +570,7 @@ __global__ void __launch_bounds__(256, V <= 8 ? 4 : 2)
         // without a bias, else the scores in fp64; ties by id
         double c = my_l;
         if (bias != nullptr && my_l > -INFINITY)
-          c = 1.0 / (1.0 + exp(-(double)my_l)) + clamp_bias(__ldg(bias + my_id));
+          c = sigmoid_64(my_l) + clamp_bias(__ldg(bias + my_id));
         const int id = lane < n_cand && my_key != 0 ? my_id : 0x7FFFFFFF;
         int rank = 0;
         for (int j = 0; j < n_cand; ++j) {
