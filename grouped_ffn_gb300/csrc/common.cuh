@@ -32,6 +32,9 @@ constexpr size_t kStatusBytes = MOE_WS_STATUS_BYTES;
 // Status-block word [16]: the grouped FFN's count of finished CTAs; the
 // last CTA of a launch clears it and the per-segment readiness counters.
 constexpr int kFfnExitWord = 16;
+// Words [20, 22): the FP4 product's count of tiles taken and of finished CTAs,
+// cleared by the last CTA of a launch.
+constexpr int kFp4CounterWord = 20;
 
 // Workspace map (bytes): [0, 256) status block; [256, 256 + 4 * 1024) the
 // grouped FFN's per-segment readiness counters; [4352, 4608) the layout's

@@ -17,7 +17,7 @@
 //   warps 2-5  epilogue: TMEM lane = weight row, column = row of x
 //   warp 7     the rows' scales into the layout that tcgen05.cp reads, loaded
 //              four stages ahead in registers
-//   warp 6     orders those stores before the tensor core's reads
+//   warp 6     takes tiles from a counter (workspace) and hands them to the others
 // TMEM: two accumulators of 2 x 112 columns, 48 columns of scales.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -54,14 +54,15 @@ struct Cfg {
   struct __align__(8) Bars {
     uint64_t full[kStages];
     uint64_t empty[kStages];
-    uint64_t raw[kStages];
     uint64_t tfull[2];
     uint64_t tempty[2];
+    uint64_t sfull[4];
+    uint64_t sempty[4];
     uint64_t drain;
   };
   static constexpr size_t kBarsOff = (size_t)kStages * kStageBytes;
   static constexpr size_t kMiscOff = kBarsOff + sizeof(Bars);
-  static constexpr size_t kSegOff = kMiscOff + 24;
+  static constexpr size_t kSegOff = kMiscOff + 32;
   static constexpr size_t kOutOff = (kSegOff + (size_t)(3 * kMaxSegs + 2) * 4 + 15) / 16 * 16;
   static constexpr size_t kSmemBytes = kOutOff + kEpiWarps * kOutWarpBytes + 1024;
   static_assert(kStageBytes % 1024 == 0 && kXOff % 1024 == 0, "swizzle atoms are 1024 bytes");
@@ -75,6 +76,7 @@ struct Params {
   const float *alpha;  // per expert, or NULL
   void *out;
   int32_t *status;
+  int32_t *counter;  // tiles taken beyond the first of each CTA; finished CTAs
   int64_t n_rows;
   int32_t S, E, nkb, nbn, sf_ld;
   int32_t out_n;  // columns of out
@@ -179,15 +181,12 @@ struct Tile {
 };
 
 // Tiles in order (segment, weight tile, row tile): CTAs side by side read the
-// same weight tile.  CTA b takes tiles b, b + grid, ...
-struct Walk {
+// same weight tile.
+struct Tiles {
   const int32_t *pre, *off, *ex;
   int S, nbn;
-  int64_t t, total;
 
-  __device__ __forceinline__ bool valid() const { return t < total; }
-  __device__ __forceinline__ void next() { t += gridDim.x; }
-  __device__ __forceinline__ Tile tile() const {
+  __device__ __forceinline__ Tile at(int t) const {
     int a = 0, b = S;  // the last s with pre[s] * nbn <= t: its segment has tiles
     while (b - a > 1) {
       const int c = (a + b) >> 1;
@@ -207,6 +206,38 @@ struct Walk {
     x.row0 = off[a] + m * per;
     x.n = min(per, rows - m * per);
     return x;
+  }
+};
+
+// The CTA's tiles in turn, handed out by the scheduling warp through two slots
+// (log_slots 1): tiles differ in cost by a factor of ten and more (rows in the
+// tile, weights in L2 or not), so each CTA takes the next one when it has room
+// for it.  Warp 7 reads up to kStages stages ahead: where those reach beyond the
+// next tile it takes four slots, or the epilogue, which frees the slots last,
+// would wait for a stage that warp 7 stores only once it has its next tile.
+// -1 ends.
+struct Feed {
+  uint64_t *full, *empty;
+  volatile int32_t *slots;
+  volatile int32_t *abort_flag;
+  int32_t *status;
+  uint32_t log_slots, n;
+
+  // One thread: the next tile, -1 at the end (or after an abort).
+  __device__ __forceinline__ int next() {
+    const uint32_t i = n & ((1u << log_slots) - 1u);
+    if (!mbar_wait(full + i, (n >> log_slots) & 1u, abort_flag, status, moe::K_FP4_PRODUCT))
+      return -1;
+    const int t = slots[i];
+    mbar_arrive(empty + i);
+    ++n;
+    return t;
+  }
+  // A whole warp.
+  __device__ __forceinline__ int next_warp(int lane) {
+    int t = -1;
+    if (lane == 0) t = next();
+    return __shfl_sync(0xffffffffu, t, 0);
   }
 };
 
@@ -238,11 +269,14 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bars->full[i], 2);  // the producer and the rows' scales
       mbar_init(&bars->empty[i], 1);
-      mbar_init(&bars->raw[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->tfull[i], 1);
       mbar_init(&bars->tempty[i], kEpiThreads);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bars->sfull[i], 1);
+      mbar_init(&bars->sempty[i], 3 + C::kEpiWarps);  // every warp that works on tiles
     }
     mbar_init(&bars->drain, 1);
     *abort_flag = 0;
@@ -280,8 +314,11 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  Walk walk{pre, off, ex, p.S, p.nbn, (int64_t)blockIdx.x,
-            none ? 0 : (int64_t)pre[p.S] * p.nbn};
+  const Tiles tiles{pre, off, ex, p.S, p.nbn};
+  const int total = none ? 0 : (int)((int64_t)pre[p.S] * p.nbn);
+  volatile int32_t *slots = reinterpret_cast<int32_t *>(smem + C::kMiscOff + 16);
+  const uint32_t log_slots = p.nkb >= kStages ? 1 : 2;
+  Feed feed{bars->sfull, bars->sempty, slots, abort_flag, p.status, log_slots, 0};
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -291,8 +328,8 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
       int stage = 0;
       uint32_t phase = 0, armed = 0, armed_par = 0;
       bool ok = true;
-      for (; walk.valid() && ok; walk.next()) {
-        const Tile ti = walk.tile();
+      for (int t; ok && (t = feed.next()) >= 0;) {
+        const Tile ti = tiles.at(t);
         const int boxes = (ti.n + kBoxRows - 1) / kBoxRows;
         const uint8_t *w = p.w + ((int64_t)ti.e * p.nbn + ti.nb) * p.nkb * (int64_t)kTileBytes;
         for (int kb = 0; kb < p.nkb; ++kb) {
@@ -329,8 +366,8 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
       int stage = 0, acc = 0;
       uint32_t phase = 0, pe = 0;  // bit i: slot i's phase
       bool ok = true;
-      for (; walk.valid() && ok; walk.next()) {
-        const Tile ti = walk.tile();
+      for (int t; ok && (t = feed.next()) >= 0;) {
+        const Tile ti = tiles.at(t);
         const uint32_t nmma = (uint32_t)((ti.n + 15) & ~15);
         // e2m1 operands (bits 7-9, 10-11), N / 8 at 17, scales E8M0 (1) or
         // E4M3 (0) at 23, M = 128 at 27
@@ -355,6 +392,9 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
             break;
           }
           tc_fence_after();
+          // warp 7's stores before the copies below.  (Here, not in warp 7: the
+          // fence would wait for its loads in flight.)
+          fence_proxy_async_shared();
           const uint32_t sw = smem_u32(smem + (size_t)stage * kStageBytes);
           const uint32_t sx = sw + kXOff;
 #pragma unroll
@@ -397,11 +437,11 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
     // ------------------------------------------- the rows' scales, per stage
     constexpr int kPer = 4 * kBlocks;  // rows of a lane
     uint32_t v[kStages][kPer][kGroups];
+    bool have[kStages];  // which of v hold a stage
     Tile ti{};
-    int kb = 0;
-    bool more = walk.valid();
-    if (more) ti = walk.tile();
-    const int64_t n_tiles = more ? (walk.total - walk.t + gridDim.x - 1) / gridDim.x : 0;
+    int kb = 0, t = feed.next_warp(lane);
+    bool more = t >= 0;
+    if (more) ti = tiles.at(t);
     auto load = [&](uint32_t (&u)[kPer][kGroups]) {
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {  // rows lane, lane + 32, ...
@@ -423,21 +463,26 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
           }
         }
       }
+      const bool got = more;
       if (more && ++kb == p.nkb) {
         kb = 0;
-        walk.next();
-        more = walk.valid();
-        if (more) ti = walk.tile();
+        t = feed.next_warp(lane);
+        more = t >= 0;
+        if (more) ti = tiles.at(t);
       }
+      return got;
     };
 #pragma unroll
-    for (int d = 0; d < kStages; ++d) load(v[d]);
+    for (int d = 0; d < kStages; ++d) have[d] = load(v[d]);
     uint32_t phase = 0;
     bool ok = true;
-    for (int64_t left = n_tiles * p.nkb; left > 0 && ok; left -= kStages, phase ^= 1u) {
+    for (; ok; phase ^= 1u) {
 #pragma unroll
       for (int d = 0; d < kStages; ++d) {
-        if (d >= left || !ok) break;
+        if (!ok || !have[d]) {
+          ok = false;
+          break;
+        }
         int got = 0;
         if (lane == 0)
           got = mbar_wait(&bars->empty[d], phase ^ 1u, abort_flag, p.status, kid) ? 1 : 0;
@@ -451,26 +496,22 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
             *reinterpret_cast<uint4 *>(dst + (g * kBlocks + b) * 512) = make_uint4(
                 v[d][4 * b][g], v[d][4 * b + 1][g], v[d][4 * b + 2][g], v[d][4 * b + 3][g]);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->raw[d]);
-        load(v[d]);
+        if (lane == 0) mbar_arrive(&bars->full[d]);
+        have[d] = load(v[d]);
       }
     }
   } else if (warp == 6) {
-    // The proxy fence between those stores and tcgen05.cp, in a warp of its
-    // own: it would also wait for warp 7's loads in flight.
+    // ------------------------------------------------------------ scheduler
     if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      const int64_t n_tiles =
-          walk.valid() ? (walk.total - walk.t + gridDim.x - 1) / gridDim.x : 0;
-      for (int64_t left = n_tiles * p.nkb; left > 0; --left) {
-        if (!mbar_wait(&bars->raw[stage], phase, abort_flag, p.status, kid)) break;
-        fence_proxy_async_shared();
-        mbar_arrive(&bars->full[stage]);
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+      int t = blockIdx.x;
+      for (uint32_t n = 0;; ++n) {
+        const uint32_t i = n & ((1u << log_slots) - 1u);
+        if (!mbar_wait(&bars->sempty[i], ((n >> log_slots) & 1u) ^ 1u, abort_flag, p.status, kid))
+          break;
+        slots[i] = t < total ? t : -1;
+        mbar_arrive(&bars->sfull[i]);
+        if (t >= total) break;
+        t = (int)gridDim.x + atomicAdd(p.counter, 1);
       }
     }
   } else {
@@ -480,8 +521,8 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
     constexpr int kStep = 16 * (C::kEpiWarps / 4);  // they take 16 rows in turn
     int acc = 0;
     uint32_t pf = 0;  // bit i: slot i's phase
-    for (; walk.valid(); walk.next()) {
-      const Tile ti = walk.tile();
+    for (int t; (t = feed.next_warp(lane)) >= 0;) {
+      const Tile ti = tiles.at(t);
       const bool big = ROWS > kSlotRows && ti.n > kSlotRows;
       if (big) acc = 0;
       const int slot = acc, rows = big ? ROWS : kSlotRows;
@@ -577,6 +618,15 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem_base, kTmemCols);
   }
+  // The last CTA to finish (no tile is taken any more) clears the counters for
+  // the next launch on this workspace.
+  if (threadIdx.x == 0) {
+    __threadfence();
+    if (atomicAdd(p.counter + 1, 1) == (int)gridDim.x - 1) {
+      p.counter[0] = 0;
+      p.counter[1] = 0;
+    }
+  }
 }
 
 // ------------------------------------------------------------------ host
@@ -647,7 +697,7 @@ extern "C" moe_status moe_grouped_product_fp4(const uint8_t *codes, const uint8_
   p.nkb = (K + fp4::kStepElems - 1) / fp4::kStepElems;
   p.nbn = swi ? (N / 2 + 127) / 128 : (N + 255) / 256;
   const int64_t max_tiles = ((n_rows + kSlotRows - 1) / kSlotRows + S) * p.nbn;
-  if (max_tiles >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+  if (max_tiles >= ((int64_t)1 << 31) - 65536) return MOE_ERR_UNSUPPORTED;
   if (!seg_offsets || !seg_expert || !w_packed) return MOE_ERR_INVALID_ARG;
   if (moe_status s = moe_host::check_ws(ws, ws_bytes, moe::kStatusBytes)) return s;
   if (n_rows == 0) return MOE_OK;
@@ -674,6 +724,7 @@ extern "C" moe_status moe_grouped_product_fp4(const uint8_t *codes, const uint8_
   p.alpha = alpha;
   p.out = out;
   p.status = moe_host::status_ptr(ws);
+  p.counter = p.status + moe::kFp4CounterWord;
   p.n_rows = n_rows;
   p.S = S;
   p.E = E;

@@ -688,7 +688,9 @@ moe_status moe_grouped_ffn_gather(const uint16_t *x, int64_t T, int32_t k,
  *              16-byte aligned; rows outside every segment are left unwritten.
  *  Two calls (gate/up with SwiGLU, quantize, down) make an expert's FFN.
  *  Limits: S <= 1024, K % 32 == 0, N % 8 == 0 (SwiGLU: N % 16 == 0), n_rows <
- *  2^31 - 16.  ws: at least MOE_WS_STATUS_BYTES.  Device errors:
+ *  2^31 - 16.  ws: at least MOE_WS_STATUS_BYTES; two counters in it must be
+ *  zero on entry (moe_workspace_init makes them so, every call leaves them
+ *  zero).  Device errors:
  *  MOE_ERR_DEVICE_INDEX (an expert id or a segment outside its range: the
  *  segment is skipped; offsets that decrease: nothing is computed),
  *  MOE_ERR_DEVICE_TIMEOUT. */
