@@ -165,13 +165,27 @@ __device__ __forceinline__ void stmatrix_t(uint32_t saddr, uint32_t a, uint32_t 
                : "memory");
 }
 
-// silu(g) u.  bf16 results: the fast exponential and division are far below
-// the rounding of the result; fp32 results take the accurate ones.
+// silu(g) u for fp32 results.
 __device__ __forceinline__ float swiglu_accurate(float g, float u) {
   return g / (1.0f + expf(-g)) * u;
 }
-__device__ __forceinline__ float swiglu_fast(float g, float u) {
-  return __fdividef(g, 1.0f + __expf(-g)) * u;
+
+// Two of them for bf16 results, by the approximate exponential and one
+// approximate reciprocal for both (the special function unit bounds the
+// epilogue: 1.5 operations a value instead of 2): 1 / a = b / (a b).  The
+// errors, a few fp32 steps, are far below the rounding of the result.  e^-g is
+// held below 2^62, so that the product stays finite: silu(g) is then off by
+// less than 2^-56 for any g.
+__device__ __forceinline__ void swiglu_fast2(float g0, float u0, float g1, float u1, float &y0,
+                                             float &y1) {
+  constexpr float kLog2e = 1.4426950409f;
+  float e0, e1, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(fminf(g0 * -kLog2e, 62.0f)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(fminf(g1 * -kLog2e, 62.0f)));
+  const float d0 = 1.0f + e0, d1 = 1.0f + e1;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d0 * d1));
+  y0 = g0 * u0 * (r * d1);
+  y1 = g1 * u1 * (r * d0);
 }
 
 // One tile: weight tile nb of expert e times rows [row0, row0 + n) of x.
@@ -585,10 +599,9 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
               for (int i = 0; i < 4; ++i) {
                 float x = __uint_as_float(v[h][r][2 * i]) * alpha;
                 float y = __uint_as_float(v[h][r][2 * i + 1]) * alpha;
-                if (SWIGLU) {
-                  x = swiglu_fast(x, __uint_as_float(v[1][r][2 * i]) * alpha);
-                  y = swiglu_fast(y, __uint_as_float(v[1][r][2 * i + 1]) * alpha);
-                }
+                if (SWIGLU)
+                  swiglu_fast2(x, __uint_as_float(v[1][r][2 * i]) * alpha, y,
+                               __uint_as_float(v[1][r][2 * i + 1]) * alpha, x, y);
                 pk[i] = pack_bf16x2(x, y);
               }
               stmatrix_t(st + (((2 * r + (piece & 1)) ^ st_sw) << 4), pk[0], pk[1], pk[2], pk[3]);
