@@ -6,7 +6,7 @@
 //   groups by the sum of their group_topn largest c, then the k largest c of
 //   the kept groups (ties: lower id);   w = scale s  or  scale s / sum_k s.
 //
-// One warp per token.  GB300 issues fp64 at a small fraction of the fp32 rate
+// One warp per token, or (gate_many_kernel) four lanes.  GB300 issues fp64 at a small fraction of the fp32 rate
 // and the choice needs more than fp32 only where two scores nearly meet, so
 // the warp chooses in fp32 with a bound on every score's error, and chooses
 // again in fp64 (exact_token) when a gap that decides something is within the
@@ -603,6 +603,292 @@ __global__ void __launch_bounds__(256, V <= 8 ? 4 : 2)
   }
 }
 
+// ------------------------------------------------------- many tokens at once
+// Four lanes a token, eight tokens a warp: what a warp does once a token in
+// gate_kernel (rounds, checks, weights) it does here once for eight.  Lane q
+// of a token holds experts [q P, (q + 1) P), P = 8 NB, as GL whole groups (or,
+// without groups, a quarter of the row), and goes through them in batches of
+// eight: sort the batch, keep the eight largest of it and the group's list.
+//
+// Keys are fixed-point numbers, c 2^28 + 2^31 rounded down, their low log2 P
+// bits the place in the lane: 2^-22 of |c| < 8 at P = 64, where a float key
+// would lose 2^-17 of c.  Rows with a |c| beyond kKeyRange go to exact_token,
+// as do rows in doubt.
+constexpr float kKeyRange = 7.9f;
+constexpr int kManyThreads = 256;
+
+// Descending bitonic merge of eight keys that first fall and then rise.
+__device__ __forceinline__ void merge8(uint32_t (&k)[8]) {
+#pragma unroll
+  for (int d = 4; d >= 1; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((i & d) == 0) {
+        const uint32_t hi = max(k[i], k[i + d]);
+        k[i + d] = min(k[i], k[i + d]);
+        k[i] = hi;
+      }
+}
+
+// The eight largest of two descending lists, descending.
+__device__ __forceinline__ void merge_top8(uint32_t (&a)[8], const uint32_t (&b)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] = max(a[i], b[7 - i]);
+  merge8(a);
+}
+
+__device__ __forceinline__ float quad_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(kFull, x, 1));
+  return fmaxf(x, __shfl_xor_sync(kFull, x, 2));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  x += __shfl_xor_sync(kFull, x, 1);
+  return x + __shfl_xor_sync(kFull, x, 2);
+}
+__device__ __forceinline__ uint32_t quad_max(uint32_t x) {
+  x = max(x, __shfl_xor_sync(kFull, x, 1));
+  return max(x, __shfl_xor_sync(kFull, x, 2));
+}
+__device__ __forceinline__ uint32_t quad_min(uint32_t x) {
+  x = min(x, __shfl_xor_sync(kFull, x, 1));
+  return min(x, __shfl_xor_sync(kFull, x, 2));
+}
+
+__device__ __forceinline__ void load8(const float *p, float (&l)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
+  const float4 b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+  l[0] = a.x, l[1] = a.y, l[2] = a.z, l[3] = a.w;
+  l[4] = b.x, l[5] = b.y, l[6] = b.z, l[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&l)[8]) {
+  const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    l[2 * i] = __uint_as_float(w[i] << 16);
+    l[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+template <typename L, int NB, int GL>
+__global__ void __launch_bounds__(kManyThreads, 3)
+    gate_many_kernel(const L *__restrict__ logits, int64_t ld, int64_t T,
+                     const float *__restrict__ bias, GateArgs a, int32_t *__restrict__ ids,
+                     float *__restrict__ w) {
+  constexpr int P = 8 * NB, E = 4 * P, NBG = NB / GL;
+  constexpr uint32_t kPlace = P - 1;
+  constexpr int kPad = P + 4;  // a lane's biases, off the other lanes' banks
+  __shared__ __align__(16) float bias_s[4 * kPad];
+  moe::pdl_wait();
+  moe::pdl_trigger();
+  for (int e = threadIdx.x; e < E; e += kManyThreads)
+    bias_s[e / P * kPad + e % P] = bias != nullptr ? clamp_bias(__ldg(bias + e)) : 0.0f;
+  __syncthreads();
+  const int lane = threadIdx.x & 31, q = lane & 3;
+  const uint32_t quad = 0xFu << (lane & 28);
+  const int64_t warp0 = ((int64_t)blockIdx.x * kManyThreads + threadIdx.x) >> 5;
+  const int64_t nwarps = ((int64_t)gridDim.x * kManyThreads) >> 5;
+  const bool softmax = a.score_fn == MOE_SCORE_SOFTMAX;
+  const float *my_bias = bias_s + q * kPad;
+
+  for (int64_t first = warp0 * 8; first < T; first += nwarps * 32) {
+    uint32_t doubtful = 0;  // a bit a token, eight a turn
+    int64_t t8 = first;
+    for (int turn = 0; turn < 4 && t8 < T; ++turn, t8 += nwarps * 8) {
+      const bool real = t8 + (lane >> 2) < T;
+      const int64_t t = real ? t8 + (lane >> 2) : T - 1;
+      const L *row = logits + t * ld + q * P;
+      float m = -INFINITY, zinv = 1.0f;
+      if (softmax) {
+#pragma unroll 2
+        for (int b = 0; b < NB; ++b) {
+          float l[8];
+          load8(row + 8 * b, l);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) m = fmaxf(m, usable(l[i]));
+        }
+        m = quad_max(m);
+        float z = 0.0f;
+#pragma unroll 1
+        for (int b = 0; b < NB; ++b) {
+          float l[8];
+          load8(row + 8 * b, l);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) l[i] = exp_diff(usable(l[i]), m);
+          z += ((l[0] + l[1]) + (l[2] + l[3])) + ((l[4] + l[5]) + (l[6] + l[7]));
+        }
+        z = quad_sum(z);
+        zinv = z > 0.0f ? __fdiv_rn(1.0f, z) : 0.0f;
+      }
+      bool wild = false;
+      uint32_t list[GL][8];
+#pragma unroll
+      for (int g = 0; g < GL; ++g) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) list[g][i] = 0;
+#pragma unroll 1
+        for (int b = 0; b < NBG; ++b) {
+          const int at = (g * NBG + b) * 8;
+          float l[8], bb[8];
+          load8(row + at, l);
+          *reinterpret_cast<float4 *>(bb) = *reinterpret_cast<const float4 *>(my_bias + at);
+          *reinterpret_cast<float4 *>(bb + 4) = *reinterpret_cast<const float4 *>(my_bias + at + 4);
+          uint32_t key[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float x = usable(l[i]);
+            const float s = softmax ? exp2_fast((x - m) * 1.442695041f) * zinv
+                                    : rcp_fast(1.0f + exp2_fast(x * -1.442695041f));
+            const float c = s + bb[i];
+            const bool on = x > -INFINITY;
+            wild |= on && fabsf(c) > kKeyRange;
+            const uint32_t k = (uint32_t)__float2int_rd(c * 0x1p28f) ^ 0x80000000u;
+            key[i] = (on ? k & ~kPlace : (uint32_t)P) | (kPlace - (uint32_t)(at + i));
+          }
+          sort_keys<8>(key);
+          merge_top8(list[g], key);
+        }
+      }
+      // What a key may be off by: its place and rounding, the score (see
+      // gate_kernel; a softmax's are at most zinv) and the addition.
+      const uint32_t err = P + (uint32_t)((softmax ? 1.2e-6f * zinv : 3e-7f) * 0x1p28f) + 130u;
+      bool sure = !wild;
+
+      if (a.n_groups > 1) {
+        // a group's score, halved: c as in the keys, 0 for what is masked
+        uint32_t gs[GL];
+        int rank[GL];
+#pragma unroll
+        for (int g = 0; g < GL; ++g) {
+          gs[g] = list[g][0] < 2u * P ? 0u : list[g][0] >> 1;
+          if (a.group_topn > 1 && gs[g] != 0)
+            gs[g] += list[g][1] < 2u * P ? 0x40000000u : list[g][1] >> 1;
+          rank[g] = 0;
+        }
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+          for (int h = 0; h < GL; ++h) {
+            const uint32_t o = __shfl_xor_sync(kFull, gs[h], d);
+            const int id = (q ^ d) * GL + h;
+#pragma unroll
+            for (int g = 0; g < GL; ++g)
+              if (o > gs[g] || (o == gs[g] && id < q * GL + g)) ++rank[g];
+          }
+        uint32_t least = 0xFFFFFFFFu, most = 0;
+#pragma unroll
+        for (int g = 0; g < GL; ++g) {
+          const bool keep = rank[g] < a.topk_groups;
+          if (keep)
+            least = min(least, gs[g]);
+          else
+            most = max(most, gs[g]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (!keep) list[g][i] = 0;
+        }
+        least = quad_min(least);
+        most = quad_max(most);
+        // (groups without an unmasked expert are exact ties, taken by id)
+        if (a.topk_groups < a.n_groups && most != 0 && least - most <= 2 * err + 4) sure = false;
+      }
+#pragma unroll
+      for (int g = 1; g < GL; ++g) merge_top8(list[0], list[g]);
+
+      uint32_t my_key[2] = {0, 0}, last = 0, close = 0;  // close: bit j, entries j and j + 1
+      int my_q[2] = {0, 0};
+      for (int j = 0; j <= a.k; ++j) {
+        const uint32_t head = list[0][0] & ~kPlace;
+        const uint32_t best = quad_max(head);
+        if (j > 0 && best >= 2u * P && last - best <= 2 * err) close |= 1u << (j - 1);
+        if (j == a.k) break;
+        last = best;
+        const int src = __ffs(__ballot_sync(kFull, head == best) & quad) - 1;
+        const uint32_t won = __shfl_sync(kFull, list[0][0], src);
+        if ((j & 3) == q) {
+          if (j < 4) {
+            my_key[0] = won;
+            my_q[0] = src & 3;
+          } else {
+            my_key[1] = won;
+            my_q[1] = src & 3;
+          }
+        }
+        pop<8>(list[0], lane == src);
+      }
+      // entries q and q + 4
+      int my_id[2];
+      float my_l[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        my_id[s] = my_q[s] * P + (int)(kPlace - (my_key[s] & kPlace));
+        my_l[s] = 4 * s + q < a.k ? usable(load_logit(logits + t * ld + my_id[s])) : -INFINITY;
+      }
+      if (__any_sync(kFull, close != 0)) {
+        // equal logits with equal biases are exact ties, already by id
+        float my_b[2], nl[2], nb[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          my_b[s] = bias_s[my_id[s] / P * kPad + my_id[s] % P];
+        const int next = (lane & 28) | ((q + 1) & 3);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          // entry q + 1 of the same four, or the first of the other four
+          const float l0 = __shfl_sync(kFull, my_l[s], next), l1 = __shfl_sync(kFull, my_l[1], next);
+          const float b0 = __shfl_sync(kFull, my_b[s], next), b1 = __shfl_sync(kFull, my_b[1], next);
+          nl[s] = q < 3 ? l0 : l1;
+          nb[s] = q < 3 ? b0 : b1;
+        }
+        uint32_t open = close;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int j = 4 * s + q;
+          if (j < a.k - 1 && my_l[s] == nl[s] && my_b[s] == nb[s]) open &= ~(1u << j);
+        }
+        open &= __shfl_xor_sync(kFull, open, 1);
+        open &= __shfl_xor_sync(kFull, open, 2);
+        if (open != 0) sure = false;
+      }
+      // lane 4 i speaks for token i: bits 4 i to bits i
+      uint32_t bits = __ballot_sync(kFull, !sure && real && q == 0);
+      bits = (bits | bits >> 3) & 0x03030303u;
+      bits = (bits | bits >> 6) & 0x000F000Fu;
+      bits = (bits | bits >> 12) & 0xFFu;
+      doubtful |= bits << (8 * turn);
+
+      // weights, as chosen_weight
+      float v[2];
+      float ml = 0.0f;
+      const bool tiny = a.renormalize && quad_max(fmaxf(my_l[0], my_l[1])) < kTinyLogit;
+      const bool rel = softmax || tiny;
+      if (__any_sync(kFull, rel)) ml = softmax && !a.renormalize ? m : quad_max(fmaxf(my_l[0], my_l[1]));
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (!softmax) v[s] = sigmoid32(my_l[s]);
+        if (rel) v[s] = exp_diff(my_l[s], ml);
+        if (4 * s + q >= a.k) v[s] = 0.0f;
+      }
+      float f = softmax ? zinv : 1.0f;
+      if (a.renormalize) {
+        const float den = quad_sum(v[0] + v[1]);
+        f = den > 0.0f ? rcp_fast(den) : 0.0f;
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (real && 4 * s + q < a.k) {
+          ids[t * a.k + 4 * s + q] = my_id[s];
+          w[t * a.k + 4 * s + q] = a.scale * (v[s] * f);
+        }
+    }
+    __syncwarp();  // the rows' first results are written
+    for (; doubtful != 0; doubtful &= doubtful - 1) {
+      const int i = __ffs(doubtful) - 1;
+      const int64_t u = first + (i >> 3) * nwarps * 8 + (i & 7);
+      exact_token<L, E / 32>(logits + u * ld, E, bias, a, ids + u * a.k, w + u * a.k);
+    }
+  }
+}
+
 // Gradient of the logits for a gradient g of the weights (the selection and
 // the bias carry none).  With v the renormalised weights without scale:
 //   sigmoid            dl_e = scale g_e s_e (1 - s_e)                selected e
@@ -761,9 +1047,59 @@ moe_status by_size(int n, F &&f) {
   return f(Int<32>{});
 }
 
+// gate_many_kernel's cases: a row in four equal parts of whole batches and
+// whole groups, 16-byte loads.  Fewer tokens than kManyTokens leave SMs idle
+// and take a warp each: 256 experts in 8 groups, 4096 tokens 9.8 us with a warp
+// a token against 14.9 us here, 8192 tokens 19 against 15 us, 65536 78 against
+// 39 us; 32 experts 3.7 and 5.7, 7.1 and 5.8, 27 and 13 us.
+constexpr int64_t kManyTokens = 8192;
+
+template <typename L>
+bool many_fits(const void *logits, int64_t ld, int64_t T, int E, const float *bias,
+               const GateArgs &a) {
+  const int per_lane = a.n_groups / 4;  // groups
+  return T >= kManyTokens && (E == 32 || E == 64 || E == 128 || E == 256) &&
+         (a.n_groups == 1 || a.n_groups == 4 || a.n_groups == 8) &&
+         (a.n_groups > 1 || bias != nullptr) && (per_lane == 0 || E / 32 % per_lane == 0) &&
+         a.k <= 8 && a.group_topn <= 2 && ld % 8 == 0 &&
+         reinterpret_cast<uintptr_t>(logits) % (8 * sizeof(L) > 16 ? 16 : 8 * sizeof(L)) == 0;
+}
+
+template <typename L, int NB, int GL>
+moe_status launch_many_parts(const L *l, int64_t ld, int64_t T, const float *bias, GateArgs a,
+                             int32_t *ids, float *w, cudaStream_t st) {
+  constexpr int per_block = kManyThreads / 4;
+  int64_t blocks = (T + per_block - 1) / per_block;
+  // four times as many as are resident: a block that meets a row in doubt takes
+  // longer, and others take its place (65536 tokens: 39 us, 45 with three an SM)
+  const int64_t cap = (int64_t)moe_host::sm_count() * 12;
+  if (blocks > cap) blocks = cap;
+  return moe_host::launch_pdl(gate_many_kernel<L, NB, GL>, dim3((unsigned)blocks),
+                              dim3(kManyThreads), 0, st, l, ld, T, bias, a, ids, w);
+}
+
+template <typename L>
+moe_status launch_many(const void *logits, int64_t ld, int64_t T, int E, const float *bias,
+                       GateArgs a, int32_t *ids, float *w, cudaStream_t st) {
+  const L *l = static_cast<const L *>(logits);
+  return by_size(E / 32, [&](auto v) -> moe_status {
+    constexpr int NB = decltype(v)::value;
+    if constexpr (NB <= 8) {
+      if constexpr (NB >= 2) {
+        if (a.n_groups == 8) return launch_many_parts<L, NB, 2>(l, ld, T, bias, a, ids, w, st);
+      }
+      return launch_many_parts<L, NB, 1>(l, ld, T, bias, a, ids, w, st);
+    } else {
+      return MOE_ERR_UNSUPPORTED;
+    }
+  });
+}
+
 template <typename L>
 moe_status launch_gate(const void *logits, int64_t ld, int64_t T, int E, const float *bias,
                        GateArgs a, int32_t *ids, float *w, cudaStream_t st) {
+  if (many_fits<L>(logits, ld, T, E, bias, a))
+    return launch_many<L>(logits, ld, T, E, bias, a, ids, w, st);
   const L *l = static_cast<const L *>(logits);
   const int gsz = E / a.n_groups, p = 32 / a.n_groups;
   return by_size((gsz + p - 1) / p, [&](auto v) {

@@ -276,6 +276,77 @@ def test_close_scores(fn):
             assert_admissible(ids.cpu().numpy(), l.astype(np.float64), b, fn, 8, groups, kept, 2)
 
 
+MANY = [  # sizes that take four lanes a token, and neighbours of them
+    (8200, 256, SIGMOID, 8, 8, 4, 2, 1, 2.5, True, "f32"),
+    (8192, 256, SIGMOID, 6, 8, 3, 1, 0, 1.0, False, "f32"),
+    (8201, 32, SOFTMAX, 4, 1, 1, 1, 0, 1.0, True, "bf16"),
+    (8195, 64, SIGMOID, 8, 8, 8, 2, 1, 1.0, True, "f32"),
+    (8193, 64, SOFTMAX, 5, 4, 2, 2, 1, 1.0, True, "f32"),
+    (8199, 128, SOFTMAX, 8, 4, 1, 2, 0, 2.0, False, "bf16"),
+    (8194, 128, SIGMOID, 1, 1, 1, 1, 1, 1.0, True, "bf16"),
+    (8197, 256, SOFTMAX, 7, 1, 1, 1, 1, 1.0, True, "f32"),
+    (8198, 96, SIGMOID, 4, 1, 1, 1, 1, 1.0, True, "f32"),
+    (9000, 256, SIGMOID, 16, 8, 4, 2, 1, 1.0, True, "f32"),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", MANY)
+def test_many_tokens(case):
+    """Many tokens: rows of every kind among them, compared with the definition on a sample and with
+    the same rows in small calls everywhere."""
+    T, E, fn, k, G, kept, topn, renorm, scale, has_bias, dtype = case
+
+    def edit(l, rng):
+        l[0] = -np.inf
+        l[1] = np.nan
+        l[2, 3:] = -np.inf
+        l[3, :E // 4] = -np.inf
+        l[4] = -90 + 0.01 * l[4]
+        l[5] = 0
+        l[6, 5] = np.inf
+        l[7, ::2] = np.nan
+        l[8] = 20 + l[8]
+        l[9] *= 30
+        l[-1] = l[-2]
+    t, l, rng = make(T, E, dtype, T + E, edit=edit)
+    bias = (0.1 * rng.standard_normal(E)).astype(np.float32) if has_bias else None
+    m = moe()
+    cfg = m.GateCfg(fn, k, G, kept, topn, renorm, scale)
+    dev, db = t.cuda(), None if bias is None else torch.from_numpy(bias).cuda()
+    ids, w = run_gate(dev, db, cfg)
+    sample = np.concatenate((np.arange(40), rng.integers(40, T, 200), [T - 2, T - 1]))
+    rid, rw = reference(l[sample], bias, fn, k, G, kept, topn, renorm, scale)
+    assert np.array_equal(ids.cpu().numpy()[sample], rid)
+    err = np.abs(w.cpu().numpy().astype(np.float64)[sample] - rw)
+    assert (err <= 16 * HALF32 * rw + 2.0 ** -140).all()
+    for lo in range(0, T, 2000):
+        i2, w2 = run_gate(dev[lo:lo + 2000], db, cfg)
+        assert torch.equal(ids[lo:lo + 2000], i2)
+        d = (w[lo:lo + 2000] - w2).abs()
+        assert (d <= 32 * HALF32 * w2 + 2.0 ** -140).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fn", [SOFTMAX, SIGMOID])
+def test_many_tokens_with_large_biases(fn):
+    """Scores with biases beyond the range of the fixed-point keys."""
+    T, E = 8192, 64
+    t, l, rng = make(T, E, "f32", 77)
+    bias = (rng.choice([0.0, 3.0, -7.5, 7.8, 9.0, -50.0, 1e30], E)).astype(np.float32)
+    for G, kept in ((1, 1), (4, 2)):
+        cfg = moe().GateCfg(fn, 6, G, kept, 2 if G > 1 else 1, 1, 1.0)
+        db = torch.from_numpy(bias).cuda()
+        ids, w = run_gate(t.cuda(), db, cfg)
+        i2, w2 = run_gate(t.cuda()[:4000], db, cfg)
+        assert torch.equal(ids[:4000], i2)
+        assert ((w[:4000] - w2).abs() <= 32 * HALF32 * w2 + 2.0 ** -140).all()
+        sample = rng.integers(0, T, 100)
+        rid, _ = reference(l[sample], bias, fn, 6, G, kept, 2 if G > 1 else 1, 1, 1.0)
+        # (scores under a bias of 1e30 vanish in 64 bits too, and tie by id)
+        assert np.array_equal(ids.cpu().numpy()[sample], rid)
+
+
 @pytest.mark.gpu
 def test_row_stride_and_bias_order():
     """Rows further apart than their length; a large bias decides the choice, not the weights."""
