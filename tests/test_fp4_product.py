@@ -246,3 +246,28 @@ def test_on_another_stream_and_in_a_graph():
     graph.replay()
     m.moe_grouped_product_fp4(*args, out, ws)
     assert torch.equal(out[:80], other[:80])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out_t", [torch.float32, torch.bfloat16])
+def test_offsets_past_32_bits(out_t):
+    """Results more than 4 GiB into the output: the last rows against the same rows alone."""
+    m = moe()
+    rng = np.random.default_rng(9)
+    n, N, K = 1_200_000, 2048, 64
+    wc, wsf, _ = fp4_tensor((2, N, K), MX, rng, -2, 1)
+    xc, xs, _ = fp4_tensor((300, K), MX, rng, -2, 1)
+    w = m.pack_weights_fp4(torch.from_numpy(wc).cuda(), torch.from_numpy(wsf).cuda(), MX, m.MOE_EPI_NONE)
+    codes, sf = m.new_fp4(n, K, MX)
+    codes.zero_(), sf.fill_(127)
+    codes[-300:], sf[-300:] = torch.from_numpy(xc).cuda(), torch.from_numpy(xs).cuda()
+    ws = m.new_workspace(n, 1, 2)
+    experts = torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    offs = torch.tensor([0, n - 200, n], dtype=torch.int32, device="cuda")
+    out = torch.full((n, N), 3.0, dtype=out_t, device="cuda")
+    m.moe_grouped_product_fp4(codes, sf, offs, experts, w, None, out, ws)
+    m.moe_check_device_status(ws)
+    few = torch.empty(300, N, dtype=out_t, device="cuda")
+    offs = torch.tensor([0, 100, 300], dtype=torch.int32, device="cuda")
+    m.moe_grouped_product_fp4(codes[-300:].contiguous(), sf[-300:].contiguous(), offs, experts, w, None, few, ws)
+    assert torch.equal(out[-300:], few) and few.abs().max() > 0 and not out[:-300].any()

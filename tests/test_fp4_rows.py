@@ -274,3 +274,29 @@ def test_pack_layout(E, N, K, epi, fmt):
     s = got[..., 32768:].reshape(E, nbn, nkb, 2, sb // 4, 32, 4, 4)      # half, group, r % 32, r / 32, byte
     s = s.transpose(0, 1, 3, 6, 5, 2, 4, 7).reshape(full_s.shape)
     assert np.array_equal(s, full_s)
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """Codes, rows and logits more than 4 GiB into their buffers."""
+    m = moe()
+    n, K = 1_100_000, 8192                              # 18 GB of rows, 4.5 GB of codes
+    x = torch.zeros(n, K, dtype=torch.bfloat16, device="cuda")
+    tail = torch.randn(5, K, device="cuda").bfloat16()
+    x[-5:] = tail
+    codes, sf = m.new_fp4(n, K, NV)
+    m.moe_quantize_fp4(x, NV, -4, codes, sf)
+    rc, rs, rv = reference(tail.float().cpu().numpy(), NV, -4)
+    assert same_codes(unpack(codes[-5:]), rc) and np.array_equal(sf[-5:].cpu().numpy()[:, :rs.shape[1]], rs)
+    x.fill_(1)
+    m.moe_dequant_fp4(codes, sf, NV, -4, x)
+    assert torch.equal(x[-5:].float().cpu() + 0.0, torch.from_numpy(rv).float() + 0.0) and not x[:-5].any()
+    del x, sf
+    # dispatched rows beyond 4 GiB of codes
+    sf = torch.zeros(n, m.moe_fp4_scale_ld(K, MX), dtype=torch.uint8, device="cuda")
+    ws = m.new_workspace(5, 1, 1)
+    dest = torch.arange(n - 5, n, dtype=torch.int32, device="cuda").flip(0).contiguous()
+    m.moe_permute_fp4(tail, 1, dest, MX, 0, codes, sf, ws)
+    m.moe_check_device_status(ws)
+    rc, rs, _ = reference(tail.float().cpu().numpy(), MX, 0)
+    assert same_codes(unpack(codes[-5:].flip(0)), rc)
