@@ -106,21 +106,6 @@ __device__ __forceinline__ float max16(float x) {
   return x;
 }
 
-// Compensated butterfly sum; every lane ends with the same value.
-__device__ __forceinline__ float warp_sum_compensated(float x) {
-  float s = x, c = 0.0f;
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    const float os = __shfl_xor_sync(kFull, s, off);
-    const float oc = __shfl_xor_sync(kFull, c, off);
-    const float n = __fadd_rn(s, os), bb = __fsub_rn(n, s);
-    const float e = __fadd_rn(__fsub_rn(s, __fsub_rn(n, bb)), __fsub_rn(os, bb));
-    s = n;
-    c = __fadd_rn(__fadd_rn(c, oc), e);
-  }
-  return __fadd_rn(s, c);
-}
-
 // Float to an unsigned integer of the same order, and back.
 __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t u = __float_as_uint(x);
@@ -895,59 +880,92 @@ __global__ void __launch_bounds__(kManyThreads, 3)
 //   sigmoid, renorm    dl_e = scale (g_e - sum g v) v_e (1 - s_e)    selected e
 //   softmax            dl_e = s_e (scale g_e [selected] - scale sum g s)  all e
 //   softmax, renorm    dl_e = scale (g_e - sum g v) v_e              selected e
-// A row is first written whole (zeros, or -s_e scale sum g s), then lane j < k
-// overwrites the j-th chosen expert's entry.
-template <typename L, int VPL>
+// A warp takes TPW tokens at once, 32 / TPW lanes for the choices of each, so
+// that the loads of ids, logits and gradients (one behind the other) of several
+// tokens are in flight.  A row is first written whole (zeros, or -s_e scale sum
+// g s), then lane j < k of its token overwrites the j-th chosen expert's entry.
+template <int LPT>
+__device__ __forceinline__ float part_sum(float x) {
+#pragma unroll
+  for (int off = LPT / 2; off > 0; off >>= 1) x += __shfl_xor_sync(kFull, x, off);
+  return x;
+}
+template <int LPT>
+__device__ __forceinline__ float part_max(float x) {
+#pragma unroll
+  for (int off = LPT / 2; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, off));
+  return x;
+}
+
+template <typename L, int VPL, int TPW>
 __global__ void __launch_bounds__(256)
     gate_backward_kernel(const L *__restrict__ logits, int64_t ld, int64_t T, int E,
                          const int32_t *__restrict__ ids, const float *__restrict__ grad_w,
                          GateArgs a, L *__restrict__ grad_logits, int32_t *status) {
   moe::pdl_wait();
   moe::pdl_trigger();
-  const int lane = threadIdx.x & 31;
+  constexpr int LPT = 32 / TPW;
+  const int lane = threadIdx.x & 31, sub = lane / LPT, j = lane % LPT;
   const int64_t warp0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
   const bool softmax = a.score_fn == MOE_SCORE_SOFTMAX;
   const bool dense = softmax && !a.renormalize;
-  for (int64_t t = warp0; t < T; t += nwarps) {
-    L *out = grad_logits + t * E;
+  for (int64_t t0 = warp0 * TPW; t0 < T; t0 += nwarps * TPW) {
+    const int64_t t = t0 + sub;
+    const int n = (int)(T - t0 < TPW ? T - t0 : TPW);  // tokens of this turn
     int id = -1;
     float g = 0.0f, my_l = -INFINITY;
-    if (lane < a.k) {
-      id = __ldg(ids + t * a.k + lane);
+    if (sub < n && j < a.k) {
+      id = __ldg(ids + t * a.k + j);
+      g = a.scale * __ldg(grad_w + t * a.k + j);
       if (id < 0 || id >= E) {
-        moe::report_error(status, MOE_ERR_DEVICE_INDEX, (int32_t)(t * a.k + lane), moe::K_GATE);
+        moe::report_error(status, MOE_ERR_DEVICE_INDEX, (int32_t)(t * a.k + j), moe::K_GATE);
         id = -1;
+        g = 0.0f;
       } else {
-        g = a.scale * __ldg(grad_w + t * a.k + lane);
         my_l = usable(load_logit(logits + t * ld + id));
       }
     }
     const bool live = my_l > -INFINITY;
     float mine = 0.0f;  // this lane's entry
     if (dense) {
-      float x[VPL], m = -INFINITY, z = 0.0f;
+      float x[TPW][VPL], zinv[TPW], my_m = 0.0f, my_zinv = 0.0f;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int e = lane + 32 * i;
-        x[i] = e < E ? usable(load_logit(logits + t * ld + e)) : -INFINITY;
-        m = fmaxf(m, x[i]);
-      }
-      m = warp_max(m);
+      for (int s = 0; s < TPW; ++s)
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        x[i] = exp_diff(x[i], m);
-        z += x[i];
+        for (int i = 0; i < VPL; ++i) {
+          const int e = lane + 32 * i;
+          x[s][i] = s < n && e < E ? usable(load_logit(logits + (t0 + s) * ld + e)) : -INFINITY;
+        }
+#pragma unroll
+      for (int s = 0; s < TPW; ++s) {
+        float m = -INFINITY, z = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) m = fmaxf(m, x[s][i]);
+        m = warp_max(m);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+          x[s][i] = exp_diff(x[s][i], m);
+          z += x[s][i];
+        }
+        z = part_sum<32>(z);
+        zinv[s] = z > 0.0f ? __fdiv_rn(1.0f, z) : 0.0f;
+        if (sub == s) {
+          my_m = m;
+          my_zinv = zinv[s];
+        }
       }
-      z = warp_sum_compensated(z);
-      const float zinv = z > 0.0f ? __fdiv_rn(1.0f, z) : 0.0f;
-      const float p = live ? exp_diff(my_l, m) * zinv : 0.0f;
-      const float dot = warp_sum_compensated(g * p);
+      const float p = live ? exp_diff(my_l, my_m) * my_zinv : 0.0f;
+      const float dot = part_sum<LPT>(g * p);
       mine = p * (g - dot);
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int e = lane + 32 * i;
-        if (e < E) store_grad(out + e, -(x[i] * zinv) * dot);
+      for (int s = 0; s < TPW; ++s) {
+        const float f = zinv[s] * __shfl_sync(kFull, dot, s * LPT);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+          const int e = lane + 32 * i;
+          if (s < n && e < E) store_grad(grad_logits + (t0 + s) * E + e, -x[s][i] * f);
+        }
       }
     } else {
       float num = 0.0f, q = 1.0f;  // q = 1 - s
@@ -956,23 +974,27 @@ __global__ void __launch_bounds__(256)
         q = sigmoid32(-my_l);
       }
       if (a.renormalize) {
-        const float ml = warp_max(my_l);
+        const float ml = part_max<LPT>(my_l);
         if (softmax || ml < kTinyLogit) num = live ? exp_diff(my_l, ml) : 0.0f;
-        const float den = warp_sum_compensated(num);
+        const float den = part_sum<LPT>(num);
         const float v = den > 0.0f ? __fdiv_rn(num, den) : 0.0f;
-        const float dot = warp_sum_compensated(g * v);
+        const float dot = part_sum<LPT>(g * v);
         mine = (g - dot) * v * q;
       } else {
         mine = g * num * q;
       }
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int e = lane + 32 * i;
-        if (e < E) store_grad(out + e, 0.0f);
+      // zeros: the turn's rows lie one after the other
+      L *out = grad_logits + t0 * E;
+      const int64_t bytes = (int64_t)n * E * sizeof(L);
+      if ((reinterpret_cast<uintptr_t>(out) | bytes) % 16 == 0) {
+        for (int64_t i = lane; i < bytes / 16; i += 32)
+          reinterpret_cast<uint4 *>(out)[i] = make_uint4(0, 0, 0, 0);
+      } else {
+        for (int64_t i = lane; i < (int64_t)n * E; i += 32) store_grad(out + i, 0.0f);
       }
     }
-    __syncwarp();  // the row's stores come before the overwriting ones
-    if (id >= 0) store_grad(out + id, mine);
+    __syncwarp();  // the rows' stores come before the overwriting ones
+    if (id >= 0) store_grad(grad_logits + t * E + id, mine);
   }
 }
 
@@ -1126,9 +1148,17 @@ moe_status launch_backward(const void *logits, int64_t ld, int64_t T, int E, con
                            cudaStream_t st) {
   return by_size((E + 31) / 32, [&](auto v) {
     constexpr int VPL = decltype(v)::value > 16 ? 16 : decltype(v)::value;
-    return moe_host::launch_pdl(gate_backward_kernel<L, VPL>, dim3(gate_grid(T, 8)),
-                                dim3(256), 0, st, static_cast<const L *>(logits), ld, T, E, ids, g,
-                                a, static_cast<L *>(out), status);
+    constexpr int TPW = VPL > 8 ? 2 : 4;  // rows of up to 512 values in registers
+    auto run = [&](auto kernel, int tpw) {
+      return moe_host::launch_pdl(kernel, dim3(gate_grid((T + tpw - 1) / tpw, 8)), dim3(256), 0, st,
+                                  static_cast<const L *>(logits), ld, T, E, ids, g, a,
+                                  static_cast<L *>(out), status);
+    };
+    // two at once where a token's choices need 16 lanes, or where four rows in
+    // registers cost more than they hide (256 experts, 65536 tokens: 47 us)
+    const bool dense = a.score_fn == MOE_SCORE_SOFTMAX && !a.renormalize;
+    return a.k <= 8 && !(dense && VPL >= 8) ? run(gate_backward_kernel<L, VPL, TPW>, TPW)
+                                            : run(gate_backward_kernel<L, VPL, 2>, 2);
   });
 }
 
