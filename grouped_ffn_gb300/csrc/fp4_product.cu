@@ -8,17 +8,29 @@
 // shared memory exactly as they lie in memory, so one bulk copy a step), the
 // rows its N side: N is the number of rows in the tile, rounded up to 16, so
 // a segment of a few rows moves few bytes and wastes little of the tensor
-// core.  A segment of n rows is cut into ceil(n / 112) tiles of equal size.
+// core.  A segment of n rows is cut into ceil(n / ROWS) tiles of equal size.
 //
-// Per CTA (one per SM, 256 threads), a ring of 4 stages of 256 elements of K:
+// Per CTA (one per SM), a ring of stages of 256 elements of K:
 //   warp 0     weights (one bulk copy) and rows (TMA boxes of 16 rows)
 //   warp 1     copies the stage's scales into TMEM (tcgen05.cp) and issues 8
 //              block-scaled MMAs of K = 64 (4 steps x 2 weight halves)
-//   warps 2-5  epilogue: TMEM lane = weight row, column = row of x
-//   warp 7     the rows' scales into the layout that tcgen05.cp reads, loaded
-//              four stages ahead in registers
+//   warps 2-5  epilogue: TMEM lane = weight row, column = row of x (ROWS = 224:
+//              warps 8-11 too)
 //   warp 6     takes tiles from a counter (workspace) and hands them to the others
-// TMEM: two accumulators of 2 x 112 columns, 48 columns of scales.
+//   warp 7     the rows' scales into the layout that tcgen05.cp reads, loaded
+//              as many stages ahead as there are, in registers
+// TMEM: two accumulator slots of 2 x 112 columns, up to 64 columns of scales.
+//
+// ROWS = 112 (4 stages): a slot a tile, the epilogue of one under the products
+// of the next.  Bound by the weight stream: 64 experts of one row each, 4096 x
+// 4096, 85 us, 7.1 TB/s of weights; 128 rows over 64 experts, 8192 -> 2 x 2048,
+// 130 us, 6.9 TB/s.
+// ROWS = 224 (3 stages), where segments average more than 64 rows: a tile takes
+// both slots, so that a stage of weights meets twice the rows, and the epilogue
+// is not hidden.  Bound by what an SM takes in from L2 (68 KB a stage at about 96
+// bytes a ns) and by the epilogue (2 to 3 us of 14 us a tile at K = 4096): 7448
+// rows over 4 experts, 4096 x 4096, 57 us, 4.3 PFLOP/s, the tensor pipe busy 43%
+// of the time (128 x 224 x 64 MMAs run at 9.6 PFLOP/s alone).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -643,7 +655,11 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
 }
 
 // ------------------------------------------------------------------ host
-// Above this many rows a segment on average, tiles of up to 224 rows.
+// Above this many rows a segment on average, tiles of up to 224 rows.  4096 x
+// 4096: 64 experts of 64 rows 93 us either way, of 128 rows 106 us (a segment one
+// tile instead of two, its weights read once), 4 experts of 2048 rows 68 us
+// against 74 us.  Fewer rows a segment fill one slot, and four stages keep more
+// of the weight stream in flight.
 constexpr int kBigRows = 64;
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
