@@ -303,7 +303,7 @@ def moe_gate(logits, bias, cfg: GateCfg, topk_ids, topk_w, stream=None):
         _need(bias, torch.float32, "bias")
         if bias.numel() != E:
             raise ValueError("moe_gate: bias needs E entries")
-    if tuple(topk_ids.shape) != (T, cfg.k) or tuple(topk_w.shape) != (T, cfg.k):
+    if topk_ids.shape != (T, cfg.k) or topk_w.shape != (T, cfg.k):
         raise ValueError("moe_gate: inconsistent shapes")
     _check("moe_gate", lib().moe_gate(_ptr(logits), kind, _ld(logits), T, E, _ptr(bias),
                                       ctypes.byref(cfg), _ptr(topk_ids), _ptr(topk_w),
@@ -318,8 +318,8 @@ def moe_gate_backward(logits, topk_ids, grad_w, cfg: GateCfg, grad_logits, ws, s
     _need(grad_w, torch.float32, "grad_w")
     _need(grad_logits, logits.dtype, "grad_logits")
     T, E = logits.shape
-    if tuple(topk_ids.shape) != (T, cfg.k) or tuple(grad_w.shape) != (T, cfg.k) \
-            or tuple(grad_logits.shape) != (T, E):
+    if topk_ids.shape != (T, cfg.k) or grad_w.shape != (T, cfg.k) \
+            or grad_logits.shape != (T, E):
         raise ValueError("moe_gate_backward: inconsistent shapes")
     _check("moe_gate_backward", lib().moe_gate_backward(
         _ptr(logits), kind, _ld(logits), T, E, _ptr(topk_ids), _ptr(grad_w), ctypes.byref(cfg),
@@ -751,16 +751,20 @@ def _fp4(codes, sf, fmt: int, call: str):
     """(rows, K) of FP4 rows, checked."""
     _need(codes, torch.uint8, "codes")
     _need(sf, torch.uint8, "sf")
-    if codes.dim() != 2 or tuple(sf.shape) != (codes.shape[0], moe_fp4_scale_ld(2 * codes.shape[1], fmt)):
+    if codes.dim() != 2:
         raise ValueError(f"{call}: inconsistent shapes")
-    return codes.shape[0], 2 * codes.shape[1]
+    n, half = codes.shape
+    # moe_fp4_scale_ld of 2 * half elements, without a call
+    if sf.shape != (n, (half + 127) // 128 * (16 if fmt == MOE_FP4_NV else 8)):
+        raise ValueError(f"{call}: inconsistent shapes")
+    return n, 2 * half
 
 
 def moe_quantize_fp4(x, fmt: int, scale_exp: int, codes, sf, stream=None):
     """Rows of x (fp32 or bf16 [n, K]) to FP4 codes and scales (new_fp4)."""
     kind = _rows(x, "x")
     n, K = _fp4(codes, sf, fmt, "moe_quantize_fp4")
-    if tuple(x.shape) != (n, K):
+    if x.shape != (n, K):
         raise ValueError("moe_quantize_fp4: inconsistent shapes")
     _check("moe_quantize_fp4", lib().moe_quantize_fp4(
         _ptr(x), kind, _ld(x), n, K, fmt, int(scale_exp), _ptr(codes), _ptr(sf), _stream(stream)))
@@ -786,7 +790,7 @@ def moe_dequant_fp4(codes, sf, fmt: int, scale_exp: int, out, stream=None):
     if not isinstance(out, torch.Tensor) or out.dtype not in _TYPES:
         raise TypeError("out: expected float32 or bfloat16")
     _need(out, out.dtype, "out")
-    if tuple(out.shape) != (n, K):
+    if out.shape != (n, K):
         raise ValueError("moe_dequant_fp4: inconsistent shapes")
     _check("moe_dequant_fp4", lib().moe_dequant_fp4(
         _ptr(codes), _ptr(sf), n, K, fmt, int(scale_exp), _ptr(out), _TYPES[out.dtype],
@@ -806,7 +810,7 @@ def pack_weights_fp4(codes, sf, fmt: int, epilogue: int, stream=None) -> Fp4Weig
     _need(codes, torch.uint8, "codes")
     _need(sf, torch.uint8, "sf")
     E, N, K = codes.shape[0], codes.shape[1], 2 * codes.shape[2]
-    if tuple(sf.shape) != (E, N, moe_fp4_scale_ld(K, fmt)):
+    if sf.shape != (E, N, moe_fp4_scale_ld(K, fmt)):
         raise ValueError("pack_weights_fp4: inconsistent shapes")
     n = int(lib().moe_fp4_packed_bytes(E, N, K, fmt, epilogue))
     data = torch.empty(n, dtype=torch.uint8, device=codes.device)
@@ -830,7 +834,7 @@ def moe_grouped_product_fp4(codes, sf, seg_offsets, seg_expert, w: Fp4Weights, a
     _need(out, out.dtype, "out")
     S = seg_expert.numel()
     cols = w.N // 2 if w.epilogue == MOE_EPI_SWIGLU else w.N
-    if K != w.K or tuple(out.shape) != (n, cols) or seg_offsets.numel() != S + 1 \
+    if K != w.K or out.shape != (n, cols) or seg_offsets.numel() != S + 1 \
             or (alpha is not None and alpha.numel() != w.E):
         raise ValueError("moe_grouped_product_fp4: inconsistent shapes")
     _check("moe_grouped_product_fp4", lib().moe_grouped_product_fp4(
