@@ -39,6 +39,7 @@
 
 #include "common.cuh"
 #include "fp4.cuh"
+#include "tile_order.cuh"
 #include "umma.cuh"
 
 namespace {
@@ -74,8 +75,9 @@ struct Cfg {
   };
   static constexpr size_t kBarsOff = (size_t)kStages * kStageBytes;
   static constexpr size_t kMiscOff = kBarsOff + sizeof(Bars);
-  static constexpr size_t kSegOff = kMiscOff + 32;
-  static constexpr size_t kOutOff = (kSegOff + (size_t)(3 * kMaxSegs + 2) * 4 + 15) / 16 * 16;
+  static constexpr size_t kSlotsOff = (kMiscOff + 16 + 15) / 16 * 16;  // four tiles
+  static constexpr size_t kSegOff = kSlotsOff + 64;
+  static constexpr size_t kOutOff = (kSegOff + (size_t)(3 * kMaxSegs + 3) * 4 + 15) / 16 * 16;
   static constexpr size_t kSmemBytes = kOutOff + kEpiWarps * kOutWarpBytes + 1024;
   static_assert(kStageBytes % 1024 == 0 && kXOff % 1024 == 0, "swizzle atoms are 1024 bytes");
   static_assert(kSmemBytes <= 232448, "shared memory of one SM");
@@ -200,70 +202,44 @@ __device__ __forceinline__ void swiglu_fast2(float g0, float u0, float g1, float
   y1 = g1 * u1 * (r * d0);
 }
 
-// One tile: weight tile nb of expert e times rows [row0, row0 + n) of x.
+// One tile: weight tile nb of expert e times rows [row0, row0 + n) of x; n = 0
+// ends the tiles of a CTA.
 struct Tile {
-  int e, nb, n;
-  int64_t row0;
+  int e, nb, n, row0;
 };
 
-// Tiles in order (segment, weight tile, row tile): CTAs side by side read the
-// same weight tile.
-struct Tiles {
-  const int32_t *pre, *off, *ex;
-  int S, nbn;
-
-  __device__ __forceinline__ Tile at(int t) const {
-    int a = 0, b = S;  // the last s with pre[s] * nbn <= t: its segment has tiles
-    while (b - a > 1) {
-      const int c = (a + b) >> 1;
-      if ((int64_t)pre[c] * nbn <= t)
-        a = c;
-      else
-        b = c;
-    }
-    const int mt = pre[a + 1] - pre[a];
-    const int r = (int)(t - (int64_t)pre[a] * nbn);
-    const int rows = off[a + 1] - off[a];
-    const int per = ((rows + mt - 1) / mt + 15) & ~15;  // <= ROWS, and (mt - 1) * per < rows
-    Tile x;
-    x.e = ex[a];
-    x.nb = r / mt;
-    const int m = r - x.nb * mt;
-    x.row0 = off[a] + m * per;
-    x.n = min(per, rows - m * per);
-    return x;
-  }
-};
-
-// The CTA's tiles in turn, handed out by the scheduling warp through two slots
-// (log_slots 1): tiles differ in cost by a factor of ten and more (rows in the
-// tile, weights in L2 or not), so each CTA takes the next one when it has room
-// for it.  Warp 7 reads up to kStages stages ahead: where those reach beyond the
-// next tile it takes four slots, or the epilogue, which frees the slots last,
+// The CTA's tiles in turn, decoded and handed out by the scheduling warp through
+// two slots (log_slots 1): tiles differ in cost by a factor of ten and more (rows
+// in the tile, weights in L2 or not), so each CTA takes the next one when it has
+// room for it.  Warp 7 reads up to four stages ahead: where those reach beyond
+// the next tile it takes four slots, or the epilogue, which frees the slots last,
 // would wait for a stage that warp 7 stores only once it has its next tile.
-// -1 ends.
 struct Feed {
   uint64_t *full, *empty;
-  volatile int32_t *slots;
+  const volatile int4 *slots;
   volatile int32_t *abort_flag;
   int32_t *status;
   uint32_t log_slots, n;
 
-  // One thread: the next tile, -1 at the end (or after an abort).
-  __device__ __forceinline__ int next() {
+  // One thread: the next tile (n = 0 after an abort too).
+  __device__ __forceinline__ Tile next() {
     const uint32_t i = n & ((1u << log_slots) - 1u);
     if (!mbar_wait(full + i, (n >> log_slots) & 1u, abort_flag, status, moe::K_FP4_PRODUCT))
-      return -1;
-    const int t = slots[i];
+      return Tile{0, 0, 0, 0};
+    const Tile t{slots[i].x, slots[i].y, slots[i].z, slots[i].w};
     mbar_arrive(empty + i);
     ++n;
     return t;
   }
   // A whole warp.
-  __device__ __forceinline__ int next_warp(int lane) {
-    int t = -1;
+  __device__ __forceinline__ Tile next_warp(int lane) {
+    Tile t{0, 0, 0, 0};
     if (lane == 0) t = next();
-    return __shfl_sync(0xffffffffu, t, 0);
+    t.e = __shfl_sync(0xffffffffu, t.e, 0);
+    t.nb = __shfl_sync(0xffffffffu, t.nb, 0);
+    t.n = __shfl_sync(0xffffffffu, t.n, 0);
+    t.row0 = __shfl_sync(0xffffffffu, t.row0, 0);
+    return t;
   }
 };
 
@@ -283,8 +259,9 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
   volatile int32_t *abort_flag = reinterpret_cast<int32_t *>(smem + C::kMiscOff + 4);
   volatile int32_t *epi_ok = reinterpret_cast<int32_t *>(smem + C::kMiscOff + 8);
   int32_t *off = reinterpret_cast<int32_t *>(smem + C::kSegOff);  // [S + 1] first rows
-  int32_t *pre = off + kMaxSegs + 1;                           // [S + 1] row tiles before s
-  int32_t *ex = pre + kMaxSegs + 1;                            // [S]
+  // [S + 1] row tiles before s, of segments of several and of one row tile
+  int32_t *pre_h = off + kMaxSegs + 1;
+  int32_t *pre_c = pre_h + kMaxSegs + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int32_t kid = moe::K_FP4_PRODUCT;
   constexpr int kScaleBytes = fp4::Fmt<FMT>::kScaleBytes;
@@ -331,19 +308,18 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
     }
     off[s] = (int)a;
     if (s == p.S - 1) off[p.S] = (int)b;
-    ex[s] = e;
-    pre[s] = mt;
+    pre_h[s] = mt > 1 ? mt : 0;
+    pre_c[s] = mt > 1 ? 0 : mt;
   }
   const bool none = __syncthreads_or(decreasing) != 0;
-  if (warp == 0) warp_exclusive_scan(pre, p.S, lane);
+  if (warp == 0) warp_exclusive_scan(pre_h, p.S, lane);
+  if (warp == 2) warp_exclusive_scan(pre_c, p.S, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const Tiles tiles{pre, off, ex, p.S, p.nbn};
-  const int total = none ? 0 : (int)((int64_t)pre[p.S] * p.nbn);
-  volatile int32_t *slots = reinterpret_cast<int32_t *>(smem + C::kMiscOff + 16);
-  const uint32_t log_slots = p.nkb >= kStages ? 1 : 2;
+  volatile int4 *slots = reinterpret_cast<int4 *>(smem + C::kSlotsOff);
+  const uint32_t log_slots = p.nkb >= 4 ? 1 : 2;
   Feed feed{bars->sfull, bars->sempty, slots, abort_flag, p.status, log_slots, 0};
 
   if (warp == 0) {
@@ -354,8 +330,7 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
       int stage = 0;
       uint32_t phase = 0, armed = 0, armed_par = 0;
       bool ok = true;
-      for (int t; ok && (t = feed.next()) >= 0;) {
-        const Tile ti = tiles.at(t);
+      for (Tile ti; ok && (ti = feed.next()).n > 0;) {
         const int boxes = (ti.n + kBoxRows - 1) / kBoxRows;
         const uint8_t *w = p.w + ((int64_t)ti.e * p.nbn + ti.nb) * p.nkb * (int64_t)kTileBytes;
         for (int kb = 0; kb < p.nkb; ++kb) {
@@ -367,8 +342,8 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
           mbar_arrive_expect_tx(&bars->full[stage], kTileBytes + boxes * kBoxRows * 128);
           bulk_load(st, w + (int64_t)kb * kTileBytes, kTileBytes, &bars->full[stage], pol);
           for (int b = 0; b < boxes; ++b)
-            tma_load_2d(st + kXOff + b * kBoxRows * 128, &tmap_x, kb * 128,
-                        (int)ti.row0 + b * kBoxRows, &bars->full[stage]);
+            tma_load_2d(st + kXOff + b * kBoxRows * 128, &tmap_x, kb * 128, ti.row0 + b * kBoxRows,
+                        &bars->full[stage]);
           armed |= 1u << stage;
           armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
           if (++stage == kStages) {
@@ -392,8 +367,7 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
       int stage = 0, acc = 0;
       uint32_t phase = 0, pe = 0;  // bit i: slot i's phase
       bool ok = true;
-      for (int t; ok && (t = feed.next()) >= 0;) {
-        const Tile ti = tiles.at(t);
+      for (Tile ti; ok && (ti = feed.next()).n > 0;) {
         const uint32_t nmma = (uint32_t)((ti.n + 15) & ~15);
         // e2m1 operands (bits 7-9, 10-11), N / 8 at 17, scales E8M0 (1) or
         // E4M3 (0) at 23, M = 128 at 27
@@ -464,10 +438,9 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
     constexpr int kPer = 4 * kBlocks;  // rows of a lane
     uint32_t v[kStages][kPer][kGroups];
     bool have[kStages];  // which of v hold a stage
-    Tile ti{};
-    int kb = 0, t = feed.next_warp(lane);
-    bool more = t >= 0;
-    if (more) ti = tiles.at(t);
+    int kb = 0;
+    Tile ti = feed.next_warp(lane);
+    bool more = ti.n > 0;
     auto load = [&](uint32_t (&u)[kPer][kGroups]) {
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {  // rows lane, lane + 32, ...
@@ -475,7 +448,7 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
         for (int g = 0; g < kGroups; ++g) u[j][g] = 0;
         const int r = lane + 32 * j;
         if (more && r < ti.n) {
-          const uint8_t *src = p.sf + (ti.row0 + r) * p.sf_ld + kb * kScaleBytes;
+          const uint8_t *src = p.sf + (int64_t)(ti.row0 + r) * p.sf_ld + kb * kScaleBytes;
           if constexpr (FMT == 1) {
             const uint4 x = __ldg(reinterpret_cast<const uint4 *>(src));
             u[j][0] = x.x;
@@ -492,9 +465,8 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
       const bool got = more;
       if (more && ++kb == p.nkb) {
         kb = 0;
-        t = feed.next_warp(lane);
-        more = t >= 0;
-        if (more) ti = tiles.at(t);
+        ti = feed.next_warp(lane);
+        more = ti.n > 0;
       }
       return got;
     };
@@ -528,16 +500,39 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
     }
   } else if (warp == 6) {
     // ------------------------------------------------------------ scheduler
+    // Tiles in order (segment, weight tile, row tile), so that CTAs side by side
+    // read the same weight tile; those of segments of several row tiles (bound
+    // by what SMs take in from L2) and of one (bound by HBM) merged in
+    // proportion to their numbers.
     if (lane == 0) {
-      int t = blockIdx.x;
+      const int64_t Mh = none ? 0 : pre_h[p.S], Mc = none ? 0 : pre_c[p.S];
+      const int64_t total = (Mh + Mc) * p.nbn;
+      int64_t t = blockIdx.x;
       for (uint32_t n = 0;; ++n) {
+        Tile x{0, 0, 0, 0};
+        if (t < total) {
+          int s, m;
+          if (Mh > 0 && Mc > 0)  // (the merge costs two 64-bit divisions)
+            tile_order::merged(t, pre_h, pre_c, p.S, p.nbn, Mh, Mc, s, x.nb, m);
+          else
+            tile_order::in_stream(t, Mh > 0 ? pre_h : pre_c, p.S, p.nbn, s, x.nb, m);
+          const int mt = pre_h[s + 1] - pre_h[s] + pre_c[s + 1] - pre_c[s];
+          const int rows = off[s + 1] - off[s];
+          const int per = ((rows + mt - 1) / mt + 15) & ~15;  // <= ROWS, and (mt - 1) * per < rows
+          x.e = __ldg(p.seg_expert + s);
+          x.row0 = off[s] + m * per;
+          x.n = min(per, rows - m * per);
+        }
         const uint32_t i = n & ((1u << log_slots) - 1u);
         if (!mbar_wait(&bars->sempty[i], ((n >> log_slots) & 1u) ^ 1u, abort_flag, p.status, kid))
           break;
-        slots[i] = t < total ? t : -1;
+        slots[i].x = x.e;
+        slots[i].y = x.nb;
+        slots[i].z = x.n;
+        slots[i].w = x.row0;
         mbar_arrive(&bars->sfull[i]);
-        if (t >= total) break;
-        t = (int)gridDim.x + atomicAdd(p.counter, 1);
+        if (x.n == 0) break;
+        t = (int64_t)gridDim.x + atomicAdd(p.counter, 1);
       }
     }
   } else {
@@ -547,8 +542,7 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
     constexpr int kStep = 16 * (C::kEpiWarps / 4);  // they take 16 rows in turn
     int acc = 0;
     uint32_t pf = 0;  // bit i: slot i's phase
-    for (int t; (t = feed.next_warp(lane)) >= 0;) {
-      const Tile ti = tiles.at(t);
+    for (Tile ti; (ti = feed.next_warp(lane)).n > 0;) {
       const bool big = ROWS > kSlotRows && ti.n > kSlotRows;
       if (big) acc = 0;
       const int slot = acc, rows = big ? ROWS : kSlotRows;
@@ -564,7 +558,7 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
       if constexpr (sizeof(Y) == 4) {
         // fp32: a lane's weight row is a column of out, 128 bytes a store
         const int col0 = colw + lane;
-        Y *out = static_cast<Y *>(p.out) + ti.row0 * p.out_n + col0;
+        Y *out = static_cast<Y *>(p.out) + (int64_t)ti.row0 * p.out_n + col0;
 #pragma unroll 1
         for (int c = 16 * part; c < ti.n; c += kStep) {
           uint32_t a[16], b[16];
@@ -592,7 +586,7 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
         const int piece = lane >> 3, st_row = (lane & 7) + (piece >> 1) * 8;
         const uint32_t st = smem_u32(buf) + st_row * 64;
         const int st_sw = (st_row >> 1) & 3;
-        Y *out = static_cast<Y *>(p.out) + ti.row0 * p.out_n;
+        Y *out = static_cast<Y *>(p.out) + (int64_t)ti.row0 * p.out_n;
 #pragma unroll 1
         for (int c = 16 * part; c < ti.n; c += kStep) {
           uint32_t v[2][2][8];  // [weight half][16 lanes][8]

@@ -180,6 +180,15 @@ def test_long_segments(case, fmt, out_t):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("S", [767, 768, 1024])
+def test_many_segments(S):
+    """As many segments as the kernel's tables hold, empty ones among them."""
+    rng = np.random.default_rng(S)
+    counts = tuple(int(c) for c in rng.choice([0, 0, 1, 2, 17, 130], S))
+    test_exact_sums((counts, 1, 9, 40, 96, False, True), NV)
+
+
+@pytest.mark.gpu
 def test_nan_stays_in_its_row():
     m = moe()
     args, ref, n = setup(((20, 20), 0, 2, 64, 128, False, False), NV, 3)
