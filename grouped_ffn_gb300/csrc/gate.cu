@@ -22,7 +22,7 @@
 //
 // Bound by instruction issue, far above the 10 us that 65536 rows of 256 fp32
 // logits take to read: about 1000 instructions a token with a warp a token (78
-// us), 335 with four lanes a token (39 us, of which 5 us wait for rows chosen
+// us), about 300 with four lanes a token (36 us, of which 5 us wait for rows chosen
 // again).  One token: 3.8 us, latency of the launch and of the warp's rounds.
 #include <cuda_bf16.h>
 
@@ -341,8 +341,8 @@ __device__ __noinline__ void exact_token(const L *row, int E, const float *bias,
 
 // ------------------------------------------------------------ fp32 selection
 // Descending sort of V (a power of two) keys: Batcher's odd-even merge network.
-template <int V>
-__device__ __forceinline__ void sort_keys(uint32_t (&k)[V]) {
+template <int V, typename K>
+__device__ __forceinline__ void sort_keys(K (&k)[V]) {
 #pragma unroll
   for (int p = 1; p < V; p <<= 1)
 #pragma unroll
@@ -352,17 +352,17 @@ __device__ __forceinline__ void sort_keys(uint32_t (&k)[V]) {
 #pragma unroll
         for (int i = 0; i < q; ++i)
           if (i + j + q < V && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
-            const uint32_t hi = max(k[i + j], k[i + j + q]);
+            const K hi = max(k[i + j], k[i + j + q]);
             k[i + j + q] = min(k[i + j], k[i + j + q]);
             k[i + j] = hi;
           }
 }
 
-template <int V>
-__device__ __forceinline__ void pop(uint32_t (&k)[V], bool yes) {
+template <int V, typename K>
+__device__ __forceinline__ void pop(K (&k)[V], bool yes, K none = 0) {
 #pragma unroll
   for (int i = 0; i + 1 < V; ++i) k[i] = yes ? k[i + 1] : k[i];
-  if (yes) k[V - 1] = 0;
+  if (yes) k[V - 1] = none;
 }
 
 // V logits from p (16-byte pieces where the launch says that they line up).
@@ -600,28 +600,32 @@ __global__ void __launch_bounds__(256, V <= 8 ? 4 : 2)
 // without groups, a quarter of the row), and goes through them in batches of
 // eight: sort the batch, keep the eight largest of it and the group's list.
 //
-// Keys are fixed-point numbers, c 2^28 + 2^31 rounded down, their low log2 P
+// Keys are fixed-point numbers, c 2^28 rounded down to 32 bits, their low log2 P
 // bits the place in the lane: 2^-22 of |c| < 8 at P = 64, where a float key
-// would lose 2^-17 of c.  Rows with a |c| beyond kKeyRange go to exact_token,
-// as do rows in doubt.
-constexpr float kKeyRange = 7.9f;
+// would lose 2^-17 of c.  Scores beyond that range stay at its ends: among
+// themselves they count as ties, which are in doubt like any other, and a group
+// whose score they enter puts its row in doubt.  Keys below kNoScore(P) are
+// masked experts (kMasked and a place) and none (INT_MIN).
 constexpr int kManyThreads = 256;
 
+template <int P>
+constexpr int32_t kNoScore = (int32_t)0x80000000 + 4 * P;
+
 // Descending bitonic merge of eight keys that first fall and then rise.
-__device__ __forceinline__ void merge8(uint32_t (&k)[8]) {
+__device__ __forceinline__ void merge8(int32_t (&k)[8]) {
 #pragma unroll
   for (int d = 4; d >= 1; d >>= 1)
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if ((i & d) == 0) {
-        const uint32_t hi = max(k[i], k[i + d]);
+        const int32_t hi = max(k[i], k[i + d]);
         k[i + d] = min(k[i], k[i + d]);
         k[i] = hi;
       }
 }
 
 // The eight largest of two descending lists, descending.
-__device__ __forceinline__ void merge_top8(uint32_t (&a)[8], const uint32_t (&b)[8]) {
+__device__ __forceinline__ void merge_top8(int32_t (&a)[8], const int32_t (&b)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) a[i] = max(a[i], b[7 - i]);
   merge8(a);
@@ -635,11 +639,11 @@ __device__ __forceinline__ float quad_sum(float x) {
   x += __shfl_xor_sync(kFull, x, 1);
   return x + __shfl_xor_sync(kFull, x, 2);
 }
-__device__ __forceinline__ uint32_t quad_max(uint32_t x) {
+__device__ __forceinline__ int32_t quad_max(int32_t x) {
   x = max(x, __shfl_xor_sync(kFull, x, 1));
   return max(x, __shfl_xor_sync(kFull, x, 2));
 }
-__device__ __forceinline__ uint32_t quad_min(uint32_t x) {
+__device__ __forceinline__ int32_t quad_min(int32_t x) {
   x = min(x, __shfl_xor_sync(kFull, x, 1));
   return min(x, __shfl_xor_sync(kFull, x, 2));
 }
@@ -666,13 +670,13 @@ __global__ void __launch_bounds__(kManyThreads, 3)
                      const float *__restrict__ bias, GateArgs a, int32_t *__restrict__ ids,
                      float *__restrict__ w) {
   constexpr int P = 8 * NB, E = 4 * P, NBG = NB / GL;
-  constexpr uint32_t kPlace = P - 1;
-  constexpr int kPad = P + 4;  // a lane's biases, off the other lanes' banks
+  constexpr int32_t kPlace = P - 1, kNone = (int32_t)0x80000000, kLow = kNoScore<P>;
+  constexpr int kPad = P + 4;  // a lane's biases (times 2^28), off the other lanes' banks
   __shared__ __align__(16) float bias_s[4 * kPad];
   moe::pdl_wait();
   moe::pdl_trigger();
   for (int e = threadIdx.x; e < E; e += kManyThreads)
-    bias_s[e / P * kPad + e % P] = bias != nullptr ? clamp_bias(__ldg(bias + e)) : 0.0f;
+    bias_s[e / P * kPad + e % P] = bias != nullptr ? clamp_bias(__ldg(bias + e)) * 0x1p28f : 0.0f;
   __syncthreads();
   const int lane = threadIdx.x & 31, q = lane & 3;
   const uint32_t quad = 0xFu << (lane & 28);
@@ -710,12 +714,11 @@ __global__ void __launch_bounds__(kManyThreads, 3)
         z = quad_sum(z);
         zinv = z > 0.0f ? __fdiv_rn(1.0f, z) : 0.0f;
       }
-      bool wild = false;
-      uint32_t list[GL][8];
+      int32_t list[GL][8];
 #pragma unroll
       for (int g = 0; g < GL; ++g) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) list[g][i] = 0;
+        for (int i = 0; i < 8; ++i) list[g][i] = kNone;
 #pragma unroll 1
         for (int b = 0; b < NBG; ++b) {
           const int at = (g * NBG + b) * 8;
@@ -723,17 +726,15 @@ __global__ void __launch_bounds__(kManyThreads, 3)
           load8(row + at, l);
           *reinterpret_cast<float4 *>(bb) = *reinterpret_cast<const float4 *>(my_bias + at);
           *reinterpret_cast<float4 *>(bb + 4) = *reinterpret_cast<const float4 *>(my_bias + at + 4);
-          uint32_t key[8];
+          int32_t key[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float x = usable(l[i]);
-            const float s = softmax ? exp2_fast((x - m) * 1.442695041f) * zinv
+            const float x = l[i];
+            const float s = softmax ? exp2_fast((fminf(x, m) - m) * 1.442695041f) * zinv
                                     : rcp_fast(1.0f + exp2_fast(x * -1.442695041f));
-            const float c = s + bb[i];
-            const bool on = x > -INFINITY;
-            wild |= on && fabsf(c) > kKeyRange;
-            const uint32_t k = (uint32_t)__float2int_rd(c * 0x1p28f) ^ 0x80000000u;
-            key[i] = (on ? k & ~kPlace : (uint32_t)P) | (kPlace - (uint32_t)(at + i));
+            const int32_t k = max(__float2int_rd(__fmaf_rn(s, 0x1p28f, bb[i])), kLow);
+            // (a NaN fails the comparison)
+            key[i] = (x > -INFINITY ? k & ~kPlace : kNone + P) | (kPlace - (at + i));
           }
           sort_keys<8>(key);
           merge_top8(list[g], key);
@@ -742,30 +743,37 @@ __global__ void __launch_bounds__(kManyThreads, 3)
       // What a key may be off by: its place and rounding, the score (see
       // gate_kernel; a softmax's are at most zinv) and the addition.
       const uint32_t err = P + (uint32_t)((softmax ? 1.2e-6f * zinv : 3e-7f) * 0x1p28f) + 130u;
-      bool sure = !wild;
+      bool sure = true;
 
       if (a.n_groups > 1) {
         // a group's score, halved: c as in the keys, 0 for what is masked
-        uint32_t gs[GL];
+        int32_t gs[GL];
         int rank[GL];
+        constexpr int32_t kTop = 0x7FFFFFFF - P;
+        bool end = false;  // a score at an end of the range
 #pragma unroll
         for (int g = 0; g < GL; ++g) {
-          gs[g] = list[g][0] < 2u * P ? 0u : list[g][0] >> 1;
-          if (a.group_topn > 1 && gs[g] != 0)
-            gs[g] += list[g][1] < 2u * P ? 0x40000000u : list[g][1] >> 1;
+          const int32_t k0 = list[g][0], k1 = list[g][1];
+          gs[g] = k0 < kLow ? kNone : k0 >> 1;
+          if (k0 >= kLow) end |= k0 < kLow + P || k0 > kTop;
+          if (a.group_topn > 1 && k1 >= kLow) {
+            gs[g] += k1 >> 1;
+            end |= k1 < kLow + P || k1 > kTop;
+          }
           rank[g] = 0;
         }
+        if (end) sure = false;
 #pragma unroll
         for (int d = 0; d < 4; ++d)
 #pragma unroll
           for (int h = 0; h < GL; ++h) {
-            const uint32_t o = __shfl_xor_sync(kFull, gs[h], d);
+            const int32_t o = __shfl_xor_sync(kFull, gs[h], d);
             const int id = (q ^ d) * GL + h;
 #pragma unroll
             for (int g = 0; g < GL; ++g)
               if (o > gs[g] || (o == gs[g] && id < q * GL + g)) ++rank[g];
           }
-        uint32_t least = 0xFFFFFFFFu, most = 0;
+        int32_t least = 0x7FFFFFFF, most = kNone;
 #pragma unroll
         for (int g = 0; g < GL; ++g) {
           const bool keep = rank[g] < a.topk_groups;
@@ -775,26 +783,30 @@ __global__ void __launch_bounds__(kManyThreads, 3)
             most = max(most, gs[g]);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (!keep) list[g][i] = 0;
+            if (!keep) list[g][i] = kNone;
         }
         least = quad_min(least);
         most = quad_max(most);
         // (groups without an unmasked expert are exact ties, taken by id)
-        if (a.topk_groups < a.n_groups && most != 0 && least - most <= 2 * err + 4) sure = false;
+        if (a.topk_groups < a.n_groups && most != kNone &&
+            (uint32_t)least - (uint32_t)most <= 2 * err + 4)
+          sure = false;
       }
 #pragma unroll
       for (int g = 1; g < GL; ++g) merge_top8(list[0], list[g]);
 
-      uint32_t my_key[2] = {0, 0}, last = 0, close = 0;  // close: bit j, entries j and j + 1
+      int32_t my_key[2] = {0, 0}, last = 0;
+      uint32_t close = 0;  // bit j: entries j and j + 1
       int my_q[2] = {0, 0};
       for (int j = 0; j <= a.k; ++j) {
-        const uint32_t head = list[0][0] & ~kPlace;
-        const uint32_t best = quad_max(head);
-        if (j > 0 && best >= 2u * P && last - best <= 2 * err) close |= 1u << (j - 1);
+        const int32_t head = list[0][0] & ~kPlace;
+        const int32_t best = quad_max(head);
+        if (j > 0 && best >= kLow && (uint32_t)last - (uint32_t)best <= 2 * err)
+          close |= 1u << (j - 1);
         if (j == a.k) break;
         last = best;
         const int src = __ffs(__ballot_sync(kFull, head == best) & quad) - 1;
-        const uint32_t won = __shfl_sync(kFull, list[0][0], src);
+        const int32_t won = __shfl_sync(kFull, list[0][0], src);
         if ((j & 3) == q) {
           if (j < 4) {
             my_key[0] = won;
@@ -804,14 +816,14 @@ __global__ void __launch_bounds__(kManyThreads, 3)
             my_q[1] = src & 3;
           }
         }
-        pop<8>(list[0], lane == src);
+        pop<8>(list[0], lane == src, kNone);
       }
       // entries q and q + 4
       int my_id[2];
       float my_l[2];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        my_id[s] = my_q[s] * P + (int)(kPlace - (my_key[s] & kPlace));
+        my_id[s] = my_q[s] * P + (kPlace - (my_key[s] & kPlace));
         my_l[s] = 4 * s + q < a.k ? usable(load_logit(logits + t * ld + my_id[s])) : -INFINITY;
       }
       if (__any_sync(kFull, close != 0)) {
@@ -839,8 +851,10 @@ __global__ void __launch_bounds__(kManyThreads, 3)
         open &= __shfl_xor_sync(kFull, open, 2);
         if (open != 0) sure = false;
       }
-      // lane 4 i speaks for token i: bits 4 i to bits i
-      uint32_t bits = __ballot_sync(kFull, !sure && real && q == 0);
+      // any lane of a token speaks for it: bits 4 i ... 4 i + 3 to bit i
+      uint32_t bits = __ballot_sync(kFull, !sure && real);
+      bits |= bits >> 1;
+      bits = (bits | bits >> 2) & 0x11111111u;
       bits = (bits | bits >> 3) & 0x03030303u;
       bits = (bits | bits >> 6) & 0x000F000Fu;
       bits = (bits | bits >> 12) & 0xFFu;
@@ -1079,7 +1093,7 @@ moe_status by_size(int n, F &&f) {
 // whole groups, 16-byte loads.  Fewer tokens than kManyTokens leave SMs idle
 // and take a warp each: 256 experts in 8 groups, 4096 tokens 9.8 us with a warp
 // a token against 14.9 us here, 8192 tokens 19 against 15 us, 65536 78 against
-// 39 us; 32 experts 3.7 and 5.7, 7.1 and 5.8, 27 and 13 us.
+// 36 us; 32 experts 3.7 and 5.7, 7.1 and 5.8, 27 and 13 us.
 constexpr int64_t kManyTokens = 8192;
 
 template <typename L>
@@ -1099,7 +1113,7 @@ moe_status launch_many_parts(const L *l, int64_t ld, int64_t T, const float *bia
   constexpr int per_block = kManyThreads / 4;
   int64_t blocks = (T + per_block - 1) / per_block;
   // four times as many as are resident: a block that meets a row in doubt takes
-  // longer, and others take its place (65536 tokens: 39 us, 45 with three an SM)
+  // longer, and others take its place (65536 tokens: 13% less than with three an SM)
   const int64_t cap = (int64_t)moe_host::sm_count() * 12;
   if (blocks > cap) blocks = cap;
   return moe_host::launch_pdl(gate_many_kernel<L, NB, GL>, dim3((unsigned)blocks),

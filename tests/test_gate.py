@@ -348,6 +348,28 @@ def test_many_tokens_with_large_biases(fn):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("first", [0, 1, 2, 3])
+def test_many_tokens_groups_with_disabled_experts(first):
+    """Group scores that large negative biases enter: one group with a single usable expert, one
+    with all experts disabled a little, of which the first has to go."""
+    T, E = 8192, 64
+    t, l, rng = make(T, E, "f32", 5)
+    bias = np.zeros(E, np.float32)
+    g = lambda i: slice(16 * ((first + i) % 4), 16 * ((first + i) % 4) + 16)
+    bias[g(0)] = -30.0
+    bias[g(0).start + 3] = 0.0
+    bias[g(1)] = -10.0
+    cfg = moe().GateCfg(SIGMOID, 6, 4, 3, 2, 1, 1.0)
+    ids, w = run_gate(t.cuda(), torch.from_numpy(bias).cuda(), cfg)
+    sample = rng.integers(0, T, 200)
+    rid, rw = reference(l[sample], bias, SIGMOID, 6, 4, 3, 2, True, 1.0)
+    assert not ((rid // 16) == first).any()
+    assert np.array_equal(ids.cpu().numpy()[sample], rid)
+    i2, _ = run_gate(t.cuda()[:4096], torch.from_numpy(bias).cuda(), cfg)
+    assert torch.equal(ids[:4096], i2)
+
+
+@pytest.mark.gpu
 def test_row_stride_and_bias_order():
     """Rows further apart than their length; a large bias decides the choice, not the weights."""
     m = moe()
