@@ -76,7 +76,8 @@ struct Cfg {
   static constexpr size_t kBarsOff = (size_t)kStages * kStageBytes;
   static constexpr size_t kMiscOff = kBarsOff + sizeof(Bars);
   static constexpr size_t kSlotsOff = (kMiscOff + 16 + 15) / 16 * 16;  // four tiles
-  static constexpr size_t kSegOff = kSlotsOff + 64;
+  static constexpr size_t kEpiOff = kSlotsOff + 64;                     // the epilogue's tile, twice
+  static constexpr size_t kSegOff = kEpiOff + 32;
   static constexpr size_t kOutOff = (kSegOff + (size_t)(3 * kMaxSegs + 3) * 4 + 15) / 16 * 16;
   static constexpr size_t kSmemBytes = kOutOff + kEpiWarps * kOutWarpBytes + 1024;
   static_assert(kStageBytes % 1024 == 0 && kXOff % 1024 == 0, "swizzle atoms are 1024 bytes");
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
   Bars *bars = reinterpret_cast<Bars *>(smem + C::kBarsOff);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kMiscOff);
   volatile int32_t *abort_flag = reinterpret_cast<int32_t *>(smem + C::kMiscOff + 4);
-  volatile int32_t *epi_ok = reinterpret_cast<int32_t *>(smem + C::kMiscOff + 8);
+  volatile int4 *epi_tile = reinterpret_cast<int4 *>(smem + C::kEpiOff);
   int32_t *off = reinterpret_cast<int32_t *>(smem + C::kSegOff);  // [S + 1] first rows
   // [S + 1] row tiles before s, of segments of several and of one row tile
   int32_t *pre_h = off + kMaxSegs + 1;
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&bars->sfull[i], 1);
-      mbar_init(&bars->sempty[i], 3 + C::kEpiWarps);  // every warp that works on tiles
+      mbar_init(&bars->sempty[i], 4);  // producer, MMA, row scales, epilogue
     }
     mbar_init(&bars->drain, 1);
     *abort_flag = 0;
@@ -540,16 +541,29 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
     const int q = warp & 3;          // TMEM lane quadrant this warp may access
     const int part = warp >= 8;      // which of the quadrant's warps
     constexpr int kStep = 16 * (C::kEpiWarps / 4);  // they take 16 rows in turn
-    int acc = 0;
+    int acc = 0, turn = 0;
     uint32_t pf = 0;  // bit i: slot i's phase
-    for (Tile ti; (ti = feed.next_warp(lane)).n > 0;) {
-      const bool big = ROWS > kSlotRows && ti.n > kSlotRows;
+    for (;; turn ^= 1) {
+      // One thread takes the tile and waits for its products; all act on what it
+      // leaves in one of two places in turn, so that the barrier is always
+      // reached by every epilogue warp or, after an abort, by none.
+      auto is_big = [](const Tile &t) { return ROWS > kSlotRows && t.n > kSlotRows; };
+      if (warp == 2 && lane == 0) {
+        Tile t = feed.next();
+        const int slot = is_big(t) ? 0 : acc;
+        if (t.n > 0 && !mbar_wait(&bars->tfull[slot], pf >> slot & 1u, abort_flag, p.status, kid))
+          t.n = 0;
+        epi_tile[turn].x = t.e;
+        epi_tile[turn].y = t.nb;
+        epi_tile[turn].z = t.n;
+        epi_tile[turn].w = t.row0;
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory");
+      const Tile ti{epi_tile[turn].x, epi_tile[turn].y, epi_tile[turn].z, epi_tile[turn].w};
+      if (ti.n == 0) break;
+      const bool big = is_big(ti);
       if (big) acc = 0;
       const int slot = acc, rows = big ? ROWS : kSlotRows;
-      if (warp == 2 && lane == 0)
-        epi_ok[slot] = mbar_wait(&bars->tfull[slot], pf >> slot & 1u, abort_flag, p.status, kid) ? 1 : 0;
-      asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory");
-      if (!epi_ok[slot]) break;
       pf ^= 1u << slot;
       tc_fence_after();
       const float alpha = p.alpha ? __ldg(p.alpha + ti.e) : 1.0f;
