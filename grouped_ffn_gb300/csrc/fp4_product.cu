@@ -191,16 +191,40 @@ __device__ __forceinline__ float swiglu_accurate(float g, float u) {
 // errors, a few fp32 steps, are far below the rounding of the result.  e^-g is
 // held below 2^62, so that the product stays finite: silu(g) is then off by
 // less than 2^-56 for any g.
-__device__ __forceinline__ void swiglu_fast2(float g0, float u0, float g1, float u1, float &y0,
-                                             float &y1) {
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// silu(alpha g) (alpha u) for two pairs g, u, as bf16 (two fp32 operations an
+// instruction).
+__device__ __forceinline__ uint32_t swiglu_fast2(uint32_t g0, uint32_t g1, uint32_t u0, uint32_t u1,
+                                                 uint64_t alpha2) {
   constexpr float kLog2e = 1.4426950409f;
-  float e0, e1, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(fminf(g0 * -kLog2e, 62.0f)));
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(fminf(g1 * -kLog2e, 62.0f)));
-  const float d0 = 1.0f + e0, d1 = 1.0f + e1;
+  const uint64_t g = mul2(pack2(__uint_as_float(g0), __uint_as_float(g1)), alpha2);
+  const uint64_t u = mul2(pack2(__uint_as_float(u0), __uint_as_float(u1)), alpha2);
+  float x0, x1, d0, d1, r, y0, y1;
+  unpack2(mul2(g, pack2(-kLog2e, -kLog2e)), x0, x1);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d0) : "f"(fminf(x0, 62.0f)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d1) : "f"(fminf(x1, 62.0f)));
+  unpack2(add2(pack2(d0, d1), pack2(1.0f, 1.0f)), d0, d1);
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d0 * d1));
-  y0 = g0 * u0 * (r * d1);
-  y1 = g1 * u1 * (r * d0);
+  unpack2(mul2(mul2(g, u), mul2(pack2(d1, d0), pack2(r, r))), y0, y1);
+  return pack_bf16x2(y0, y1);
 }
 
 // One tile: weight tile nb of expert e times rows [row0, row0 + n) of x; n = 0
@@ -600,6 +624,7 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
         const int piece = lane >> 3, st_row = (lane & 7) + (piece >> 1) * 8;
         const uint32_t st = smem_u32(buf) + st_row * 64;
         const int st_sw = (st_row >> 1) & 3;
+        const uint64_t alpha2 = pack2(alpha, alpha);
         Y *out = static_cast<Y *>(p.out) + (int64_t)ti.row0 * p.out_n;
 #pragma unroll 1
         for (int c = 16 * part; c < ti.n; c += kStep) {
@@ -617,12 +642,12 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
               uint32_t pk[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                float x = __uint_as_float(v[h][r][2 * i]) * alpha;
-                float y = __uint_as_float(v[h][r][2 * i + 1]) * alpha;
                 if (SWIGLU)
-                  swiglu_fast2(x, __uint_as_float(v[1][r][2 * i]) * alpha, y,
-                               __uint_as_float(v[1][r][2 * i + 1]) * alpha, x, y);
-                pk[i] = pack_bf16x2(x, y);
+                  pk[i] = swiglu_fast2(v[0][r][2 * i], v[0][r][2 * i + 1], v[1][r][2 * i],
+                                       v[1][r][2 * i + 1], alpha2);
+                else
+                  pk[i] = pack_bf16x2(__uint_as_float(v[h][r][2 * i]) * alpha,
+                                      __uint_as_float(v[h][r][2 * i + 1]) * alpha);
               }
               stmatrix_t(st + (((2 * r + (piece & 1)) ^ st_sw) << 4), pk[0], pk[1], pk[2], pk[3]);
             }
