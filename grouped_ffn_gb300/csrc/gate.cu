@@ -22,7 +22,7 @@
 //
 // Bound by instruction issue, far above the 10 us that 65536 rows of 256 fp32
 // logits take to read: about 1000 instructions a token with a warp a token (78
-// us), about 300 with four lanes a token (36 us, of which 5 us wait for rows chosen
+// us), about 300 with four lanes a token (39 us, of which 5 us wait for rows chosen
 // again).  One token: 3.8 us, latency of the launch and of the warp's rounds.
 #include <cuda_bf16.h>
 
@@ -596,20 +596,21 @@ __global__ void __launch_bounds__(256, V <= 8 ? 4 : 2)
 // ------------------------------------------------------- many tokens at once
 // Four lanes a token, eight tokens a warp: what a warp does once a token in
 // gate_kernel (rounds, checks, weights) it does here once for eight.  Lane q
-// of a token holds experts [q P, (q + 1) P), P = 8 NB, as GL whole groups (or,
+// of a token holds experts [q P, (q + 1) P), P = E / 4, as GL whole groups (or,
 // without groups, a quarter of the row), and goes through them in batches of
 // eight: sort the batch, keep the eight largest of it and the group's list.
 //
-// Keys are fixed-point numbers, c 2^28 rounded down to 32 bits, their low log2 P
-// bits the place in the lane: 2^-22 of |c| < 8 at P = 64, where a float key
-// would lose 2^-17 of c.  Scores beyond that range stay at its ends: among
+// Keys are fixed-point numbers, c 2^28 rounded down to 32 bits, the low bits
+// that count to P given to the place in the lane: 2^-22 of |c| < 8 at P = 64,
+// where a float key would lose 2^-17 of c.  Scores beyond that range stay at its ends: among
 // themselves they count as ties, which are in doubt like any other, and a group
-// whose score they enter puts its row in doubt.  Keys below kNoScore(P) are
-// masked experts (kMasked and a place) and none (INT_MIN).
+// whose score they enter puts its row in doubt.  Keys below kLow are masked
+// experts (kMasked and a place) and none (kNone).
 constexpr int kManyThreads = 256;
 
-template <int P>
-constexpr int32_t kNoScore = (int32_t)0x80000000 + 4 * P;
+constexpr int kManyMaxP = 128;  // E <= 512
+constexpr int32_t kNone = (int32_t)0x80000000, kMasked = kNone + kManyMaxP,
+                  kLow = kNone + 4 * kManyMaxP;
 
 // Descending bitonic merge of eight keys that first fall and then rise.
 __device__ __forceinline__ void merge8(int32_t (&k)[8]) {
@@ -664,26 +665,41 @@ __device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&l)[8]) {
   }
 }
 
-template <typename L, int NB, int GL>
+template <typename L>
+__device__ __forceinline__ void exact_token_of(const L *row, int E, const float *bias,
+                                               const GateArgs &a, int32_t *ids, float *w) {
+  if (E <= 32)
+    exact_token<L, 1>(row, E, bias, a, ids, w);
+  else if (E <= 64)
+    exact_token<L, 2>(row, E, bias, a, ids, w);
+  else if (E <= 128)
+    exact_token<L, 4>(row, E, bias, a, ids, w);
+  else if (E <= 256)
+    exact_token<L, 8>(row, E, bias, a, ids, w);
+  else
+    exact_token<L, 16>(row, E, bias, a, ids, w);
+}
+
+template <typename L, int GL>
 __global__ void __launch_bounds__(kManyThreads, 3)
-    gate_many_kernel(const L *__restrict__ logits, int64_t ld, int64_t T,
+    gate_many_kernel(const L *__restrict__ logits, int64_t ld, int64_t T, int E,
                      const float *__restrict__ bias, GateArgs a, int32_t *__restrict__ ids,
                      float *__restrict__ w) {
-  constexpr int P = 8 * NB, E = 4 * P, NBG = NB / GL;
-  constexpr int32_t kPlace = P - 1, kNone = (int32_t)0x80000000, kLow = kNoScore<P>;
-  constexpr int kPad = P + 4;  // a lane's biases (times 2^28), off the other lanes' banks
-  __shared__ __align__(16) float bias_s[4 * kPad];
+  const int P = E / 4, NB = P / 8, NBG = NB / GL;
+  const int32_t place = (1 << (32 - __clz(P - 1))) - 1;  // the bits of a place
+  const int pad = P + 4;  // a lane's biases (times 2^28), off the other lanes' banks
+  __shared__ __align__(16) float bias_s[4 * (kManyMaxP + 4)];
   moe::pdl_wait();
   moe::pdl_trigger();
   for (int e = threadIdx.x; e < E; e += kManyThreads)
-    bias_s[e / P * kPad + e % P] = bias != nullptr ? clamp_bias(__ldg(bias + e)) * 0x1p28f : 0.0f;
+    bias_s[e / P * pad + e % P] = bias != nullptr ? clamp_bias(__ldg(bias + e)) * 0x1p28f : 0.0f;
   __syncthreads();
   const int lane = threadIdx.x & 31, q = lane & 3;
   const uint32_t quad = 0xFu << (lane & 28);
   const int64_t warp0 = ((int64_t)blockIdx.x * kManyThreads + threadIdx.x) >> 5;
   const int64_t nwarps = ((int64_t)gridDim.x * kManyThreads) >> 5;
   const bool softmax = a.score_fn == MOE_SCORE_SOFTMAX;
-  const float *my_bias = bias_s + q * kPad;
+  const float *my_bias = bias_s + q * pad;
 
   for (int64_t first = warp0 * 8; first < T; first += nwarps * 32) {
     uint32_t doubtful = 0;  // a bit a token, eight a turn
@@ -734,7 +750,7 @@ __global__ void __launch_bounds__(kManyThreads, 3)
                                     : rcp_fast(1.0f + exp2_fast(x * -1.442695041f));
             const int32_t k = max(__float2int_rd(__fmaf_rn(s, 0x1p28f, bb[i])), kLow);
             // (a NaN fails the comparison)
-            key[i] = (x > -INFINITY ? k & ~kPlace : kNone + P) | (kPlace - (at + i));
+            key[i] = (x > -INFINITY ? k & ~place : kMasked) | (place - (at + i));
           }
           sort_keys<8>(key);
           merge_top8(list[g], key);
@@ -742,23 +758,23 @@ __global__ void __launch_bounds__(kManyThreads, 3)
       }
       // What a key may be off by: its place and rounding, the score (see
       // gate_kernel; a softmax's are at most zinv) and the addition.
-      const uint32_t err = P + (uint32_t)((softmax ? 1.2e-6f * zinv : 3e-7f) * 0x1p28f) + 130u;
+      const uint32_t err = place + (uint32_t)((softmax ? 1.2e-6f * zinv : 3e-7f) * 0x1p28f) + 130u;
       bool sure = true;
 
       if (a.n_groups > 1) {
         // a group's score, halved: c as in the keys, 0 for what is masked
         int32_t gs[GL];
         int rank[GL];
-        constexpr int32_t kTop = 0x7FFFFFFF - P;
+        const int32_t top = 0x7FFFFFFF - place;
         bool end = false;  // a score at an end of the range
 #pragma unroll
         for (int g = 0; g < GL; ++g) {
           const int32_t k0 = list[g][0], k1 = list[g][1];
           gs[g] = k0 < kLow ? kNone : k0 >> 1;
-          if (k0 >= kLow) end |= k0 < kLow + P || k0 > kTop;
+          if (k0 >= kLow) end |= k0 <= kLow + place || k0 >= top;
           if (a.group_topn > 1 && k1 >= kLow) {
             gs[g] += k1 >> 1;
-            end |= k1 < kLow + P || k1 > kTop;
+            end |= k1 <= kLow + place || k1 >= top;
           }
           rank[g] = 0;
         }
@@ -799,7 +815,7 @@ __global__ void __launch_bounds__(kManyThreads, 3)
       uint32_t close = 0;  // bit j: entries j and j + 1
       int my_q[2] = {0, 0};
       for (int j = 0; j <= a.k; ++j) {
-        const int32_t head = list[0][0] & ~kPlace;
+        const int32_t head = list[0][0] & ~place;
         const int32_t best = quad_max(head);
         if (j > 0 && best >= kLow && (uint32_t)last - (uint32_t)best <= 2 * err)
           close |= 1u << (j - 1);
@@ -823,15 +839,14 @@ __global__ void __launch_bounds__(kManyThreads, 3)
       float my_l[2];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        my_id[s] = my_q[s] * P + (kPlace - (my_key[s] & kPlace));
+        my_id[s] = my_q[s] * P + (place - (my_key[s] & place));
         my_l[s] = 4 * s + q < a.k ? usable(load_logit(logits + t * ld + my_id[s])) : -INFINITY;
       }
       if (__any_sync(kFull, close != 0)) {
         // equal logits with equal biases are exact ties, already by id
         float my_b[2], nl[2], nb[2];
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-          my_b[s] = bias_s[my_id[s] / P * kPad + my_id[s] % P];
+        for (int s = 0; s < 2; ++s) my_b[s] = bias_s[my_id[s] + 4 * my_q[s]];
         const int next = (lane & 28) | ((q + 1) & 3);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -888,7 +903,7 @@ __global__ void __launch_bounds__(kManyThreads, 3)
     for (; doubtful != 0; doubtful &= doubtful - 1) {
       const int i = __ffs(doubtful) - 1;
       const int64_t u = first + (i >> 3) * nwarps * 8 + (i & 7);
-      exact_token<L, E / 32>(logits + u * ld, E, bias, a, ids + u * a.k, w + u * a.k);
+      exact_token_of<L>(logits + u * ld, E, bias, a, ids + u * a.k, w + u * a.k);
     }
   }
 }
@@ -1093,48 +1108,38 @@ moe_status by_size(int n, F &&f) {
 // whole groups, 16-byte loads.  Fewer tokens than kManyTokens leave SMs idle
 // and take a warp each: 256 experts in 8 groups, 4096 tokens 9.8 us with a warp
 // a token against 14.9 us here, 8192 tokens 19 against 15 us, 65536 78 against
-// 36 us; 32 experts 3.7 and 5.7, 7.1 and 5.8, 27 and 13 us.
+// 39 us; 32 experts 3.7 and 5.7, 7.1 and 5.8, 27 and 15 us.
 constexpr int64_t kManyTokens = 8192;
 
 template <typename L>
 bool many_fits(const void *logits, int64_t ld, int64_t T, int E, const float *bias,
                const GateArgs &a) {
-  const int per_lane = a.n_groups / 4;  // groups
-  return T >= kManyTokens && (E == 32 || E == 64 || E == 128 || E == 256) &&
-         (a.n_groups == 1 || a.n_groups == 4 || a.n_groups == 8) &&
-         (a.n_groups > 1 || bias != nullptr) && (per_lane == 0 || E / 32 % per_lane == 0) &&
-         a.k <= 8 && a.group_topn <= 2 && ld % 8 == 0 &&
-         reinterpret_cast<uintptr_t>(logits) % (8 * sizeof(L) > 16 ? 16 : 8 * sizeof(L)) == 0;
+  const int G = a.n_groups;
+  return T >= kManyTokens && E % 32 == 0 && a.k <= 8 && a.group_topn <= 2 &&
+         (G == 1 ? bias != nullptr
+                 : G % 4 == 0 && G <= 16 && G != 12 && E / G % 8 == 0) &&
+         ld % 8 == 0 && reinterpret_cast<uintptr_t>(logits) % 16 == 0;
 }
 
-template <typename L, int NB, int GL>
-moe_status launch_many_parts(const L *l, int64_t ld, int64_t T, const float *bias, GateArgs a,
-                             int32_t *ids, float *w, cudaStream_t st) {
+template <typename L, int GL>
+moe_status launch_many_parts(const void *logits, int64_t ld, int64_t T, int E, const float *bias,
+                             GateArgs a, int32_t *ids, float *w, cudaStream_t st) {
   constexpr int per_block = kManyThreads / 4;
   int64_t blocks = (T + per_block - 1) / per_block;
   // four times as many as are resident: a block that meets a row in doubt takes
   // longer, and others take its place (65536 tokens: 13% less than with three an SM)
   const int64_t cap = (int64_t)moe_host::sm_count() * 12;
   if (blocks > cap) blocks = cap;
-  return moe_host::launch_pdl(gate_many_kernel<L, NB, GL>, dim3((unsigned)blocks),
-                              dim3(kManyThreads), 0, st, l, ld, T, bias, a, ids, w);
+  return moe_host::launch_pdl(gate_many_kernel<L, GL>, dim3((unsigned)blocks), dim3(kManyThreads),
+                              0, st, static_cast<const L *>(logits), ld, T, E, bias, a, ids, w);
 }
 
 template <typename L>
 moe_status launch_many(const void *logits, int64_t ld, int64_t T, int E, const float *bias,
                        GateArgs a, int32_t *ids, float *w, cudaStream_t st) {
-  const L *l = static_cast<const L *>(logits);
-  return by_size(E / 32, [&](auto v) -> moe_status {
-    constexpr int NB = decltype(v)::value;
-    if constexpr (NB <= 8) {
-      if constexpr (NB >= 2) {
-        if (a.n_groups == 8) return launch_many_parts<L, NB, 2>(l, ld, T, bias, a, ids, w, st);
-      }
-      return launch_many_parts<L, NB, 1>(l, ld, T, bias, a, ids, w, st);
-    } else {
-      return MOE_ERR_UNSUPPORTED;
-    }
-  });
+  if (a.n_groups == 16) return launch_many_parts<L, 4>(logits, ld, T, E, bias, a, ids, w, st);
+  if (a.n_groups == 8) return launch_many_parts<L, 2>(logits, ld, T, E, bias, a, ids, w, st);
+  return launch_many_parts<L, 1>(logits, ld, T, E, bias, a, ids, w, st);
 }
 
 template <typename L>

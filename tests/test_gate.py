@@ -287,6 +287,11 @@ MANY = [  # sizes that take four lanes a token, and neighbours of them
     (8197, 256, SOFTMAX, 7, 1, 1, 1, 1, 1.0, True, "f32"),
     (8198, 96, SIGMOID, 4, 1, 1, 1, 1, 1.0, True, "f32"),
     (9000, 256, SIGMOID, 16, 8, 4, 2, 1, 1.0, True, "f32"),
+    (8196, 512, SIGMOID, 8, 16, 5, 2, 1, 1.0, True, "f32"),
+    (8203, 384, SOFTMAX, 6, 8, 4, 2, 1, 1.0, True, "bf16"),
+    (8192, 160, SIGMOID, 8, 4, 3, 1, 1, 1.0, True, "f32"),
+    (8192, 512, SOFTMAX, 8, 1, 1, 1, 0, 1.0, True, "bf16"),
+    (8192, 320, SIGMOID, 3, 1, 1, 1, 1, 1.0, True, "f32"),
 ]
 
 
