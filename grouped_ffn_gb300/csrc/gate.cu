@@ -6,11 +6,13 @@
 //   groups by the sum of their group_topn largest c, then the k largest c of
 //   the kept groups (ties: lower id);   w = scale s  or  scale s / sum_k s.
 //
-// One warp per token, or (gate_many_kernel) four lanes.  GB300 issues fp64 at a small fraction of the fp32 rate
-// and the choice needs more than fp32 only where two scores nearly meet, so
-// the warp chooses in fp32 with a bound on every score's error, and chooses
-// again in fp64 (exact_token) when a gap that decides something is within the
-// bounds: about one token in a thousand of a spread-out router.
+// One warp per token, or (gate_many_kernel) four lanes.  GB300 issues fp64 at a
+// small fraction of the fp32 rate and the choice needs more than fp32 only where
+// two scores nearly meet, so the choice is made in fp32 with a bound on every
+// score's error, and made again with scores to about 45 bits (the closest
+// candidates one a lane, or the whole row in exact_token) when a gap that
+// decides something is within the bounds: about one token in a thousand of a
+// spread-out router.
 //
 // Layout: a group takes p = floor(32 / n_groups) neighbouring lanes and each
 // of them V consecutive experts (without groups p = 32), so a lane never
@@ -247,7 +249,7 @@ __device__ __noinline__ double sigmoid_64(float x) {
   return (double)ph + (double)pl;
 }
 
-// One row again: the scores in fp64 (whose order as integers is theirs), the
+// One row again: the scores to 45 bits as doubles (whose order as integers is theirs), the
 // definition step by step; lane j < k writes the j-th choice.
 template <typename L, int V>
 __device__ __noinline__ void exact_token(const L *row, int E, const float *bias, const GateArgs &a,
@@ -557,7 +559,7 @@ __global__ void __launch_bounds__(256, V <= 8 ? 4 : 2)
       float my_l = lane < n_cand && my_key != 0 ? usable(load_logit(row + my_id)) : -INFINITY;
       if (doubt && sure) {
         // one candidate a lane: the logits in order (scores rise with them)
-        // without a bias, else the scores in fp64; ties by id
+        // without a bias, else the scores to 45 bits; ties by id
         double c = my_l;
         if (bias != nullptr && my_l > -INFINITY)
           c = sigmoid_64(my_l) + clamp_bias(__ldg(bias + my_id));
