@@ -601,6 +601,9 @@ __global__ void __launch_bounds__(256, V <= 8 ? 4 : 2)
 // of a token holds experts [q P, (q + 1) P), P = E / 4, as GL whole groups (or,
 // without groups, a quarter of the row), and goes through them in batches of
 // eight: sort the batch, keep the eight largest of it and the group's list.
+// Where all eight choices are one lane's, its list is empty when the last of
+// them is compared with the best expert left out, so the largest key that a
+// list let go is kept beside it.
 //
 // Keys are fixed-point numbers, c 2^28 rounded down to 32 bits, the low bits
 // that count to P given to the place in the lane: 2^-22 of |c| < 8 at P = 64,
@@ -627,10 +630,14 @@ __device__ __forceinline__ void merge8(int32_t (&k)[8]) {
       }
 }
 
-// The eight largest of two descending lists, descending.
-__device__ __forceinline__ void merge_top8(int32_t (&a)[8], const int32_t (&b)[8]) {
+// The eight largest of two descending lists, descending; ninth becomes the
+// largest key left out where that is larger.
+__device__ __forceinline__ void merge_top8(int32_t (&a)[8], const int32_t (&b)[8], int32_t &ninth) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a[i] = max(a[i], b[7 - i]);
+  for (int i = 0; i < 8; ++i) {
+    ninth = max(ninth, min(a[i], b[7 - i]));
+    a[i] = max(a[i], b[7 - i]);
+  }
   merge8(a);
 }
 
@@ -732,9 +739,10 @@ __global__ void __launch_bounds__(kManyThreads, 3)
         z = quad_sum(z);
         zinv = z > 0.0f ? __fdiv_rn(1.0f, z) : 0.0f;
       }
-      int32_t list[GL][8];
+      int32_t list[GL][8], ninth[GL];  // (the largest key that the list let go)
 #pragma unroll
       for (int g = 0; g < GL; ++g) {
+        ninth[g] = kNone;
 #pragma unroll
         for (int i = 0; i < 8; ++i) list[g][i] = kNone;
 #pragma unroll 1
@@ -755,7 +763,7 @@ __global__ void __launch_bounds__(kManyThreads, 3)
             key[i] = (x > -INFINITY ? k & ~place : kMasked) | (place - (at + i));
           }
           sort_keys<8>(key);
-          merge_top8(list[g], key);
+          merge_top8(list[g], key, ninth[g]);
         }
       }
       // What a key may be off by: its place and rounding, the score (see
@@ -799,6 +807,7 @@ __global__ void __launch_bounds__(kManyThreads, 3)
             least = min(least, gs[g]);
           else
             most = max(most, gs[g]);
+          if (!keep) ninth[g] = kNone;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             if (!keep) list[g][i] = kNone;
@@ -811,13 +820,17 @@ __global__ void __launch_bounds__(kManyThreads, 3)
           sure = false;
       }
 #pragma unroll
-      for (int g = 1; g < GL; ++g) merge_top8(list[0], list[g]);
+      for (int g = 1; g < GL; ++g) {
+        merge_top8(list[0], list[g], ninth[0]);
+        ninth[0] = max(ninth[0], ninth[g]);
+      }
 
       int32_t my_key[2] = {0, 0}, last = 0;
       uint32_t close = 0;  // bit j: entries j and j + 1
       int my_q[2] = {0, 0};
       for (int j = 0; j <= a.k; ++j) {
-        const int32_t head = list[0][0] & ~place;
+        // (at least what the list let go, unless all its eight entries are taken)
+        const int32_t head = max(list[0][0], ninth[0]) & ~place;
         const int32_t best = quad_max(head);
         if (j > 0 && best >= kLow && (uint32_t)last - (uint32_t)best <= 2 * err)
           close |= 1u << (j - 1);
