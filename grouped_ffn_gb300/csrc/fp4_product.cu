@@ -548,11 +548,9 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
           else
             tile_order::in_stream(t, Mh > 0 ? pre_h : pre_c, p.S, p.nbn, s, x.nb, m);
           const int mt = pre_h[s + 1] - pre_h[s] + pre_c[s + 1] - pre_c[s];
-          const int rows = off[s + 1] - off[s];
-          const int per = ((rows + mt - 1) / mt + 15) & ~15;  // <= ROWS, and (mt - 1) * per < rows
           x.e = __ldg(p.seg_expert + s);
-          x.row0 = off[s] + m * per;
-          x.n = min(per, rows - m * per);
+          tile_order::row_tile(off[s + 1] - off[s], mt, m, x.row0, x.n);
+          x.row0 += off[s];
           if (mt > 1) x.nb |= kShared;
         }
         const uint32_t i = n & ((1u << log_slots) - 1u);

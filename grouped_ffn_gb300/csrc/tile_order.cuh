@@ -67,6 +67,17 @@ TILE_ORDER_HD void merged(int64_t u, const int32_t *pre_h, const int32_t *pre_c,
     in_stream(u - hb, pre_c, S, NB, s, n_blk, m_blk);
 }
 
+// Rows [first, first + n) of row tile m of the mt = ceil(rows / R) that a segment
+// of `rows` rows is cut into, R a multiple of 16: tiles of equal size, a multiple
+// of 16 and at most R, the last one shorter and never empty, since (mt - 1) * R <
+// rows.  rows < 2^31 (the sum that rounds up is unsigned: it may pass 2^31).
+TILE_ORDER_HD void row_tile(int rows, int mt, int m, int &first, int &n) {
+  const uint32_t even = ((uint32_t)rows + (uint32_t)mt - 1u) / (uint32_t)mt;
+  const int per = (int)((even + 15u) & ~15u);
+  first = m * per;
+  n = rows - first < per ? rows - first : per;
+}
+
 // The positions u0, u0 + G, u0 + 2G, ... of merged(), in order.  The walk
 // carries q = floor(u * Lh / L) (hot tiles before u) and r = u * Lh - q * L,
 // 0 <= r < L.  Position u is hot when floor((u + 1) * Lh / L) > q, which is
