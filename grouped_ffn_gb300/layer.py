@@ -238,6 +238,9 @@ class MoELayer:
         rows = max_tokens * self.k + (max_tokens if self.fp4_shared else 0)
         self.x_codes, self.x_sf = moe.new_fp4(rows, self.H, fmt, dev)
         self.h_codes, self.h_sf = moe.new_fp4(rows, self.I, fmt, dev)
+        if self.fp4_shared:
+            # where each token goes for the shared expert: rows [A, A + T)
+            self._row_index = torch.arange(rows, dtype=torch.int32, device=dev)
         se = self.placement.slot_expert
         self._fp4_experts = torch.cat((se, se.new_tensor([self.E]))) if self.fp4_shared else se
 
@@ -248,8 +251,10 @@ class MoELayer:
         moe.moe_permute_fp4(x, self.k, self.dest_row[:A], fmt, self.x_exp, self.x_codes[:A],
                             self.x_sf[:A], self.ws, stream)
         if self.fp4_shared:
-            # rows [A, A + T) carry every token for the shared expert
-            moe.moe_quantize_fp4(x, fmt, self.x_exp, self.x_codes[A:rows], self.x_sf[A:rows], stream)
+            # rows [A, A + T) carry every token for the shared expert (dispatched
+            # from the buffers' start: scales A rows in need not lie on 16 bytes)
+            moe.moe_permute_fp4(x, 1, self._row_index[A:rows], fmt, self.x_exp, self.x_codes[:rows],
+                                self.x_sf[:rows], self.ws, stream)
             with torch.cuda.stream(stream or torch.cuda.current_stream()):
                 self._seg_offsets_all[-1:].fill_(rows)
             offs = self._seg_offsets_all
