@@ -69,8 +69,9 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// (the maximum first: of a NaN and a number it is the number)
 __device__ __forceinline__ float clamp_bias(float b) {
-  return fmaxf(fminf(b, kBiasClamp), -kBiasClamp);
+  return fminf(fmaxf(b, -kBiasClamp), kBiasClamp);
 }
 
 __device__ __forceinline__ float rcp_fast(float x) {  // within 1 ulp
