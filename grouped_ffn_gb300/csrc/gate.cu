@@ -264,6 +264,8 @@ __device__ __noinline__ void exact_token(const L *row, int E, const float *bias,
     if (i < sh.n) m = fmaxf(m, usable(load_logit(row + sh.e0 + i)));
   double z = 0.0;
   const bool softmax = a.score_fn == MOE_SCORE_SOFTMAX;
+  // as in gate_kernel: the logits' order, where scores would vanish in fp64 too
+  const bool by_logit = bias == nullptr && a.n_groups == 1;
   auto exp_of = [&](float l) {  // e^(l - m)
     if (l == -INFINITY) return 0.0;
     const float d = __fsub_rn(l, m), bb = __fsub_rn(d, l);
@@ -283,7 +285,7 @@ __device__ __noinline__ void exact_token(const L *row, int E, const float *bias,
       key[i] = 1;
       const float l = usable(load_logit(row + sh.e0 + i));
       if (l > -INFINITY) {
-        double c = softmax ? exp_of(l) * zinv : sigmoid_64(l);
+        double c = by_logit ? (double)l : softmax ? exp_of(l) * zinv : sigmoid_64(l);
         if (bias) c += clamp_bias(__ldg(bias + sh.e0 + i));
         key[i] = ordered(c);
       }
@@ -558,6 +560,10 @@ __global__ void __launch_bounds__(256, V <= 8 ? 4 : 2)
       }
       int my_id = __shfl_sync(kFull, e0, my_src) + (V - 1 - (int)(my_key & (V - 1)));
       float my_l = lane < n_cand && my_key != 0 ? usable(load_logit(row + my_id)) : -INFINITY;
+      // scores that vanish in fp64 are exact ties, among experts left out too
+      if (doubt && bias == nullptr && a.n_groups > 1 &&
+          __any_sync(kFull, my_l > -INFINITY && my_l - (softmax ? m : 0.0f) < -700.0f))
+        sure = false;
       if (doubt && sure) {
         // one candidate a lane: the logits in order (scores rise with them)
         // without a bias, else the scores to 45 bits; ties by id

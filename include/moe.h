@@ -202,7 +202,9 @@ typedef struct moe_gate_cfg {
  *   topk_w = scale * s_e / (sum of the k chosen s), or scale * s_e.
  *  The choice is the one of real arithmetic up to differences of c (or of
  *  group scores) below about 2^-40 of their size; equal logits with equal
- *  biases are exact ties.  The weights are within a few fp32 ulps.
+ *  biases are exact ties.  Without bias and groups it is the logits' order at
+ *  any size; otherwise scores below fp64's range (e^-745) count as 0.  The
+ *  weights are within a few fp32 ulps.
  *  A logit of -inf or NaN masks its expert: s = 0, it is chosen only when the
  *  kept groups hold fewer than k unmasked experts (lower ids first, weight
  *  0), it adds nothing to its group's score, and a group without an unmasked
