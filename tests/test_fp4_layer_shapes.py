@@ -1,6 +1,7 @@
 """The layer with FP4 experts on shapes where its parts meet: a shared
 expert's rows behind an odd number of dispatched rows, with widths of an odd
-number of 256-element steps.
+number of 256-element steps; replicas, row tiles of either size and a stream
+of the caller; a step without tokens.
 
 Each step of forward is compared with its definition on the step's own inputs
 as in test_fp4_layer, with its tolerances.
@@ -79,3 +80,53 @@ def test_shared_expert_behind_an_odd_number_of_rows(T, k, H, I, fmt):
         layer.forward(logits[:n].contiguous(), x[:n].contiguous(), y)
         layer.check()
         check_step(layer, pl, x[:n], y, *ws)
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("relax", [None, (5, 4)])
+def test_replicas_on_a_stream_of_the_caller(relax, shared, fmt):
+    """Experts with replicas, segments long enough for the product's larger row tiles, and steps on a
+    stream of the caller whose inputs another stream is still writing."""
+    from grouped_ffn_gb300 import MoELayer
+    w = wl.WORKLOADS["replica"].scaled(T=901, H=288, I=96, E=32, k=3)
+    dev = torch.device("cuda:0")
+    pl = wl.make_placement(w)
+    logits, x = wl.make_logits(w, dev), wl.make_x(w, dev)
+    ws = weights(w, shared, 7, dev)
+    layer = MoELayer(H=w.H, I=w.I, E=w.E, k=w.k, placement=moe().DevicePlacement.from_tables(pl, dev), w_gate_up=ws[0],
+                     w_down=ws[1], max_tokens=w.T, shared_w_gate_up=ws[2], shared_w_down=ws[3], device=dev, fp4=fmt,
+                     replica_relax=relax)
+    assert pl.n_slots > w.E and w.T * w.k > 64 * (pl.n_slots + 1)
+    late_x, late_logits = torch.zeros_like(x), torch.zeros_like(logits)
+    y, ready, side = torch.empty_like(x), torch.cuda.Event(), torch.cuda.Stream()
+    layer.forward(logits, x, torch.empty_like(x))
+    torch.cuda.synchronize()
+    layer._seg_offsets_all.zero_(), layer.h.zero_(), layer.y_perm.zero_()
+    busy = torch.randn(8192, 8192, device=dev)
+    for _ in range(3):
+        busy = busy @ busy * 1e-4
+    late_x.copy_(x), late_logits.copy_(logits)
+    ready.record()
+    side.wait_event(ready)
+    layer.forward(late_logits, late_x, y, side)
+    side.synchronize()
+    layer.check(side)
+    check_step(layer, pl, x, y, *ws)
+
+
+def test_empty_step():
+    """No tokens at all: nothing is written, nothing fails."""
+    from grouped_ffn_gb300 import MoELayer
+    w = wl.WORKLOADS["tiny"].scaled(T=5, H=256, I=96, E=16, k=2)
+    dev = torch.device("cuda:0")
+    pl = wl.make_placement(w)
+    logits, x = wl.make_logits(w, dev), wl.make_x(w, dev)
+    ws = weights(w, True, 8, dev)
+    layer = MoELayer(H=w.H, I=w.I, E=w.E, k=w.k, placement=moe().DevicePlacement.from_tables(pl, dev), w_gate_up=ws[0],
+                     w_down=ws[1], max_tokens=w.T, shared_w_gate_up=ws[2], shared_w_down=ws[3], device=dev, fp4=MX)
+    for n in (w.T, 0, w.T):
+        y = torch.empty(n, w.H, dtype=torch.bfloat16, device=dev)
+        layer.forward(logits[:n], x[:n], y)
+        layer.check()
+    check_step(layer, pl, x, y, *ws)
