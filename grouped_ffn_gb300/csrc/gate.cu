@@ -37,8 +37,9 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxTopn = 8;
 constexpr float kBiasClamp = 1e30f;  // group sums of clamped biases stay finite
-// below this logit sigmoid(l) is e^l to fp32 precision; where the largest chosen
-// one is, renormalised weights are taken from e^(l - max l), which cannot vanish
+// below this logit sigmoid(l) is e^l to fp32 precision, and from -87 on it has fewer
+// bits than a float or vanishes: where a chosen one is, renormalised weights are
+// taken from scores relative to the largest (sigmoid_rel)
 constexpr float kTinyLogit = -80.0f;
 
 struct GateArgs {
@@ -101,6 +102,12 @@ __device__ __forceinline__ float sigmoid32(float x) {
   const float e = expf(x < kTinyLogit ? x : -x);
   return x < kTinyLogit ? e : rcp_fast(__fadd_rn(1.0f, e));
 }
+
+// sigmoid(l) e^-ml for l <= ml < 0: e^(l - ml) / (1 + e^l).
+__device__ __forceinline__ float sigmoid_rel(float l, float ml) {
+  return exp_diff(l, ml) * sigmoid32(-l);
+}
+__device__ __forceinline__ bool tiny_logit(float l) { return l < kTinyLogit && l > -INFINITY; }
 
 // Sum over lanes 0..15 (the others hold 0), in those lanes: four roundings.
 __device__ __forceinline__ float sum16(float x) {
@@ -175,7 +182,10 @@ __device__ __forceinline__ float chosen_weight(const GateArgs &a, float l, float
     if (!a.renormalize) v *= zinv;
   } else {
     v = sigmoid32(l);
-    if (a.renormalize && !__any_sync(kFull, l >= kTinyLogit)) v = exp_diff(l, max16(l));
+    if (a.renormalize && __any_sync(kFull, tiny_logit(l))) {
+      const float ml = max16(l);
+      if (ml < 0.0f) v = sigmoid_rel(l, ml);
+    }
   }
   if (a.renormalize) {
     const float den = sum16(v);
@@ -899,16 +909,25 @@ __global__ void __launch_bounds__(kManyThreads, 3)
 
       // weights, as chosen_weight
       float v[2];
-      float ml = 0.0f;
-      const bool tiny = a.renormalize && quad_max(fmaxf(my_l[0], my_l[1])) < kTinyLogit;
-      const bool rel = softmax || tiny;
-      if (__any_sync(kFull, rel)) ml = softmax && !a.renormalize ? m : quad_max(fmaxf(my_l[0], my_l[1]));
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (!softmax) v[s] = sigmoid32(my_l[s]);
-        if (rel) v[s] = exp_diff(my_l[s], ml);
-        if (4 * s + q >= a.k) v[s] = 0.0f;
+      if (softmax) {
+        const float ml = a.renormalize ? quad_max(fmaxf(my_l[0], my_l[1])) : m;
+        v[0] = exp_diff(my_l[0], ml);
+        v[1] = exp_diff(my_l[1], ml);
+      } else {
+        v[0] = sigmoid32(my_l[0]);
+        v[1] = sigmoid32(my_l[1]);
+        const uint32_t tiny = __ballot_sync(kFull, tiny_logit(my_l[0]) || tiny_logit(my_l[1]));
+        if (a.renormalize && tiny != 0) {
+          const float ml = quad_max(fmaxf(my_l[0], my_l[1]));
+          if ((tiny & quad) != 0 && ml < 0.0f) {
+            v[0] = sigmoid_rel(my_l[0], ml);
+            v[1] = sigmoid_rel(my_l[1], ml);
+          }
+        }
       }
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (4 * s + q >= a.k) v[s] = 0.0f;
       float f = softmax ? zinv : 1.0f;
       if (a.renormalize) {
         const float den = quad_sum(v[0] + v[1]);
@@ -1032,7 +1051,12 @@ __global__ void __launch_bounds__(256)
       }
       if (a.renormalize) {
         const float ml = part_max<LPT>(my_l);
-        if (softmax || ml < kTinyLogit) num = live ? exp_diff(my_l, ml) : 0.0f;
+        const uint32_t tiny = __ballot_sync(kFull, tiny_logit(my_l));
+        const uint32_t part = (LPT == 32 ? kFull : (1u << LPT) - 1u) << (sub * LPT);
+        if (softmax)
+          num = live ? exp_diff(my_l, ml) : 0.0f;
+        else if ((tiny & part) != 0 && ml < 0.0f)
+          num = live ? sigmoid_rel(my_l, ml) : 0.0f;
         const float den = part_sum<LPT>(num);
         const float v = den > 0.0f ? __fdiv_rn(num, den) : 0.0f;
         const float dot = part_sum<LPT>(g * v);

@@ -1,12 +1,12 @@
 """The router with a balance bias at the ends of its inputs' range: a bias
-that is NaN, and scores that vanish in 64 bits.  Ids are equal to the
+that is NaN, scores that vanish in 64 bits, scores far apart.  Ids are equal to the
 definition's."""
 
 import numpy as np
 import pytest
 import torch
 
-from test_gate import SIGMOID, SOFTMAX, moe, reference, run_gate
+from test_gate import SIGMOID, SOFTMAX, check, make, moe, reference, run_gate
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -74,3 +74,23 @@ def test_vanishing_scores_in_groups(n, fn, bias):
     ids, _ = ids_of(l, b, fn, k, G, G, 2)
     rid, _ = reference(l, b, fn, k, G, G, 2, True, 1.0)
     assert np.array_equal(ids, rid)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [60, 8192])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_weights_of_scores_far_apart(dtype, T):
+    """Renormalised sigmoids whose smallest have fewer bits than a float holds, beside larger ones that are
+    small themselves: weights and gradients to the last bits all the same (tolerances of test_gate)."""
+    def edit(l, rng):
+        n = l.shape[0]
+        l[:] = -np.inf
+        best = rng.choice([3.0, -1.0, -15.0, -30.0, -70.0, -79.0, -85.0], n)
+        on = np.argsort(rng.random(l.shape), 1)[:, :9]
+        v = best[:, None] - rng.uniform(0, 1, (n, 9)) * rng.choice([10.0, 50.0, 90.0], n)[:, None]
+        v[:, 0] = best
+        np.put_along_axis(l, on, v.astype(np.float32), 1)
+    E = 32
+    case = (T, E, SIGMOID, 8, 4, 4, 2, 1, 2.5, True, dtype)
+    t, l, rng = make(T, E, dtype, T, edit=edit)
+    check(t, l, rng, case, np.zeros(E, np.float32))
