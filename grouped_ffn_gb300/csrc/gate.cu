@@ -650,11 +650,14 @@ __device__ __forceinline__ void merge8(int32_t (&k)[8]) {
 // The eight largest of two descending lists, descending; ninth becomes the
 // largest key left out where that is larger.
 __device__ __forceinline__ void merge_top8(int32_t (&a)[8], const int32_t (&b)[8], int32_t &ninth) {
+  int32_t out[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    ninth = max(ninth, min(a[i], b[7 - i]));
+    out[i] = min(a[i], b[7 - i]);
     a[i] = max(a[i], b[7 - i]);
   }
+  ninth = __vimax3_s32(__vimax3_s32(out[0], out[1], out[2]), __vimax3_s32(out[3], out[4], out[5]),
+                       __vimax3_s32(out[6], out[7], ninth));
   merge8(a);
 }
 
