@@ -813,7 +813,10 @@ def pack_weights_fp4(codes, sf, fmt: int, epilogue: int, stream=None) -> Fp4Weig
     if sf.shape != (E, N, moe_fp4_scale_ld(K, fmt)):
         raise ValueError("pack_weights_fp4: inconsistent shapes")
     n = int(lib().moe_fp4_packed_bytes(E, N, K, fmt, epilogue))
-    data = torch.empty(n, dtype=torch.uint8, device=codes.device)
+    # allocated on the stream that writes it: a block of another stream may still
+    # be read there by work queued before its last owner was freed
+    with torch.cuda.stream(stream):
+        data = torch.empty(n, dtype=torch.uint8, device=codes.device)
     _check("moe_pack_weights_fp4", lib().moe_pack_weights_fp4(
         _ptr(codes), _ptr(sf), E, N, K, fmt, epilogue, _ptr(data), _stream(stream)))
     return Fp4Weights(data, E, N, K, fmt, epilogue)
