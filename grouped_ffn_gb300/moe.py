@@ -223,7 +223,8 @@ def new_workspace(T: int, k: int, n_slots: int, device=None, stream=None,
     n = max(moe_workspace_size(T, k, n_slots), WS_STATUS_BYTES)
     if n_experts and n_ranks:
         n = max(n, moe_route_replicas_workspace_size(T, k, n_experts, n_slots, n_ranks))
-    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    with torch.cuda.stream(stream):  # of the stream that clears it, see pack_weights_fp4
+        ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
     moe_workspace_init(ws, stream)
     return ws
 

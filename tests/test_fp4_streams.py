@@ -1,4 +1,4 @@
-"""Memory that the FP4 calls allocate, on a stream of the caller."""
+"""Memory that calls allocate, on a stream of the caller."""
 
 import pytest
 import torch
@@ -28,5 +28,25 @@ def test_packed_weights_belong_to_the_stream_that_writes_them():
     got = m.pack_weights_fp4(codes, sf, m.MOE_FP4_NV, m.MOE_EPI_NONE, side)
     side.synchronize()
     assert torch.equal(got.data, want.data)
+    torch.cuda.synchronize()
+    assert (copy == 77).all()
+
+
+@pytest.mark.gpu
+def test_a_workspace_belongs_to_the_stream_that_clears_it():
+    from grouped_ffn_gb300 import build, moe as m
+    build.build()
+    a = torch.randn(4096, 4096, device="cuda")
+    held = torch.full_like(m.new_workspace(4096, 8, 256), 77)
+    copy = torch.empty_like(held)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        a = a @ a * 1e-3
+    copy.copy_(held)
+    del held
+    ws = m.new_workspace(4096, 8, 256, stream=side)
+    side.synchronize()
+    assert not ws.any()
     torch.cuda.synchronize()
     assert (copy == 77).all()
