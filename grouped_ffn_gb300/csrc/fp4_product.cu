@@ -29,8 +29,8 @@
 // both slots, so that a stage of weights meets twice the rows, and the epilogue
 // is not hidden.  Bound by what an SM takes in from L2 (68 KB a stage at about 96
 // bytes a ns) and by the epilogue (2 to 3 us of 14 us a tile at K = 4096): 7448
-// rows over 4 experts, 4096 x 4096, 57 us, 4.3 PFLOP/s, the tensor pipe busy 43%
-// of the time (128 x 224 x 64 MMAs run at 9.6 PFLOP/s alone).
+// rows over 4 experts, 4096 x 4096, 57 us, 4.4 PFLOP/s, the tensor pipe busy 45%
+// of the time (this kernel's 128 x 224 x 64 MMAs run at 9.6 PFLOP/s alone).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -695,7 +695,9 @@ __global__ void __launch_bounds__(Cfg<ROWS>::kThreads, 1)
 }
 
 // ------------------------------------------------------------------ host
-// Above this many rows a segment on average, tiles of up to 224 rows.  4096 x
+// Above this many rows a segment on average, tiles of up to 224 rows.  (Empty
+// segments count: how many there are is known on the device only, so a few long
+// segments among many empty ones take the smaller tiles.)  Equal segments, 4096 x
 // 4096: 64 experts of 64 rows 93 us either way, of 128 rows 106 us (a segment one
 // tile instead of two, its weights read once), 4 experts of 2048 rows 68 us
 // against 74 us.  Fewer rows a segment fill one slot, and four stages keep more

@@ -12,7 +12,10 @@
 // score's error, and made again with scores to about 45 bits (the closest
 // candidates one a lane, or the whole row in exact_token) when a gap that
 // decides something is within the bounds: about one token in a thousand of a
-// spread-out router.
+// spread-out router with fp32 logits.  Of bf16 logits neighbours are often
+// equal: without a bias the last choice ties with the first expert left out in
+// about one row of twenty, which gate_many_kernel chooses again as well (65536
+// such rows 74 us, with a bias 40 us).
 //
 // Layout: a group takes p = floor(32 / n_groups) neighbouring lanes and each
 // of them V consecutive experts (without groups p = 32), so a lane never
@@ -22,10 +25,13 @@
 // Each lane sorts its V keys once; a round of the top-k is then one warp
 // reduction over the lanes' heads, and the winner moves up its list.
 //
-// Bound by instruction issue, far above the 10 us that 65536 rows of 256 fp32
-// logits take to read: about 1000 instructions a token with a warp a token (78
-// us), about 300 with four lanes a token (39 us, of which 5 us wait for rows chosen
-// again).  One token: 3.8 us, latency of the launch and of the warp's rounds.
+// 65536 rows of 256 fp32 logits take 11 us to read, the kernels 78 us with a warp
+// a token (1100 instructions a token, 62% of the issue slots) and 39 us with four
+// lanes a token (330).  The latter fills neither HBM (19%) nor the issue slots (54%
+// while an SM has work, 38% of the launch): a third of a warp's time goes to its
+// loads (a request of 16 bytes a lane touches 30 sectors, and none is in flight
+// ahead), and rows chosen again hold up the end.  One token: 3.6 us, latency of
+// the launch and of the warp's rounds.
 #include <cuda_bf16.h>
 
 #include <cfloat>
@@ -960,9 +966,12 @@ __global__ void __launch_bounds__(kManyThreads, 3)
 //   softmax, renorm    dl_e = scale (g_e - sum g v) v_e              selected e
 // A warp takes TPW tokens at once, 32 / TPW lanes for the choices of each, so
 // that the loads of ids, logits and gradients (one behind the other) of several
-// tokens are in flight: 65536 rows of 256, renormalised, 21.6 us (3.3 TB/s),
-// 30.6 us with one token; every expert's score 44.5 us.  A row is first written whole (zeros, or -s_e scale sum
-// g s), then lane j < k of its token overwrites the j-th chosen expert's entry.
+// tokens are in flight: 65536 fp32 rows of 256, renormalised, 20.6 us (30.6 us with
+// one token at a time), every expert's score 44 us; 10 and 20 us are what the
+// bytes take.  The zeros' stores wait for that chain, and the loads and stores of
+// whole rows are 4 bytes a lane.  A row is first written whole (zeros, or -s_e
+// scale sum g s), then lane j < k of its token overwrites the j-th chosen
+// expert's entry.
 template <int LPT>
 __device__ __forceinline__ float part_sum(float x) {
 #pragma unroll

@@ -63,9 +63,11 @@ class MoELayer:
         quantized and packed once, here; token rows are quantized on their
         way into the dispatched rows (moe_permute_fp4), and both GEMMs are
         grouped FP4 products with the hidden rows quantized in between.
-        fp4_scale_exp: NV's tensor scale exponents of token rows and of
+        fp4_scale_exp: NV's tensor scale exponents e of token rows and of
         hidden rows (full precision for blocks whose largest magnitude lies
-        in [2^(e-3), 2^(e+11)]).  A shared expert needs the routed experts'
+        in [2^(e-3), 2^(e+11)]; values beyond 2688 * 2^e, 42 with the default
+        -6, are held as that, without a report: choose e from the largest
+        magnitude that the rows reach, or MX, whose scales have no such end).  A shared expert needs the routed experts'
         width and runs as one more segment.  Contiguous layout only."""
         if (gather or masked_cap is not None) and not packed:
             raise ValueError("gather and fixed-capacity modes stream packed weights")

@@ -201,7 +201,7 @@ typedef struct moe_gate_cfg {
  *   are chosen, in descending order; ties go to the lower id.
  *   topk_w = scale * s_e / (sum of the k chosen s), or scale * s_e.
  *  The choice is the one of real arithmetic up to differences of c (or of
- *  group scores) below about 2^-40 of their size; equal logits with equal
+ *  group scores) below about 2^-40 of their terms' size; equal logits with equal
  *  biases are exact ties.  Without bias and groups it is the logits' order at
  *  any size; otherwise scores below fp64's range (e^-745) count as 0.  The
  *  weights are within a few fp32 ulps.
@@ -486,6 +486,8 @@ int64_t moe_fp4_scale_ld(int32_t K, int32_t fmt);
  *   MX  2^e with the smallest e in [-127, 127] that has amax <= 6 * 2^e;
  *   NV  s = E4M3(amax / (6 * 2^scale_exp)), nearest even, at most 448;
  *   code = e2m1(x / scale), nearest even, at most 6 in magnitude; 0 where s is 0.
+ * So NV holds magnitudes beyond 2688 * 2^scale_exp as 2688 * 2^scale_exp, and a
+ * block of no more than 6 * 2^(scale_exp - 10) as zeros, without a report.
  * The codes are those of real arithmetic (no rounding but these).  A zero may
  * carry either sign.  A block with an infinity or NaN gets the NaN scale and
  * zero codes.
