@@ -80,7 +80,7 @@ def draw(rng):
     if op != "int4":
         H = 8 * _log_int(rng, 32, 1024)
         k = rng.randint(2, 8)
-        T = min(_log_int(rng, 1, 16384), 16384 * 4096 * 8 // (H * (k + 5)))
+        T = min(_log_int(rng, 1, 16384), 16384 * 4096 * 7 // (H * (k + 4)))
         dtype = rng.choice(("bf16", "bf16", "f32"))
         drop = rng.choice((0.0, 0.0, 0.1))
         if op == "sort":
