@@ -22,6 +22,8 @@ enum KernelId : int32_t {
   K_SELFTEST = 9,
   K_GATE = 10,
   K_FP4_PRODUCT = 11,
+  K_BLOCK = 12,
+  K_INT4_PRODUCT = 13,
 };
 
 // Status block at the start of every workspace (int32 words):

@@ -57,6 +57,15 @@ class GateCfg(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class BlockCfg(ctypes.Structure):
+    """moe_block_cfg: the block's norm, and the residual beside it."""
+    _fields_ = [("post_norm", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("residual_scale", ctypes.c_float)]
+
+    def __init__(self, post_norm=1, eps=1e-6, residual_scale=1.0):
+        super().__init__(post_norm, eps, residual_scale)
+
+
 class FfnSchedule(ctypes.Structure):
     """moe_ffn_schedule: which CTA runs which FFN tile (never a row's bits).
     ph1_shift -1 = default; interleave and small_tiles 1 = default; cta_pairs
@@ -146,6 +155,19 @@ _SIGNATURES = {
     "moe_pack_weights_fp4": (ctypes.c_int, [_P, _P, _I32, _I32, _I32, _I32, _I32, _P, _P]),
     "moe_grouped_product_fp4": (ctypes.c_int, [_P, _P, _I64, _P, _P, _I32, _I32, _P, _I32, _I32,
                                                _I32, _I32, _P, _P, _I32, _P, _SZ, _P]),
+    "moe_norm": (ctypes.c_int, [_P, _I32, _I64, _I32, _P, _F32, _P, _P]),
+    "moe_combine_norm": (ctypes.c_int, [_P, _I64, _P, _P, _I64, _I32, _I32, _P, _P, _I32, _P, _P,
+                                        ctypes.POINTER(BlockCfg), _P, _P, _P, _P, _SZ, _P]),
+    "moe_combine_backward": (ctypes.c_int, [_P, _I32, _P, _I64, _P, _P, _I64, _I32, _I32, _P, _P, _P,
+                                            _SZ, _P]),
+    "moe_permute_backward": (ctypes.c_int, [_P, _I64, _P, _P, _I64, _I32, _I32, _P, _I32, _P, _SZ,
+                                            _P]),
+    "moe_norm_scratch_bytes": (_SZ, [_I64, _I32]),
+    "moe_combine_norm_backward": (ctypes.c_int, [_P, _I32, _P, _I64, _P, _P, _I64, _I32, _I32, _P, _P,
+                                                 _P, ctypes.POINTER(BlockCfg), _P, _P, _P, _P, _P, _P,
+                                                 _SZ, _P, _SZ, _P]),
+    "moe_norm_backward": (ctypes.c_int, [_P, _I64, _P, _I32, _P, _P, _I32, _I64, _I32, _P, _F32, _P,
+                                         _F32, _P, _P, _P, _SZ, _P, _SZ, _P]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_version": (ctypes.c_char_p, []),
 }
@@ -845,6 +867,171 @@ def moe_grouped_product_fp4(codes, sf, seg_offsets, seg_expert, w: Fp4Weights, a
         _ptr(codes), _ptr(sf), n, _ptr(seg_offsets), _ptr(seg_expert), S, w.E, _ptr(w.data), w.N, K,
         w.fmt, w.epilogue, _ptr(alpha), _ptr(out), _TYPES[out.dtype], _ptr(ws), ws.numel(),
         _stream(stream)))
+
+
+# ------------------------------------------------------------------ the block around the experts
+def _typed(t: torch.Tensor, name: str) -> int:
+    """The element type code of a contiguous fp32 or bf16 CUDA tensor."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _TYPES:
+        raise TypeError(f"{name}: expected a contiguous CUDA tensor of float32 or bfloat16")
+    _need(t, t.dtype, name)
+    return _TYPES[t.dtype]
+
+
+def _maybe(t: Optional[torch.Tensor], dtype, shape, name: str, call: str):
+    """An optional tensor of a type and shape."""
+    if t is not None:
+        _need(t, dtype, name)
+        if t.shape != shape:
+            raise ValueError(f"{call}: inconsistent shapes")
+
+
+def new_norm_scratch(T: int, H: int, device=None, stream=None) -> torch.Tensor:
+    """Allocate (torch) scratch for the gradients of norm weights, for calls on
+    up to T rows of H."""
+    with torch.cuda.device(device or torch.cuda.current_device()):
+        n = int(lib().moe_norm_scratch_bytes(max(T, 1), H))
+    if n == 0:
+        raise ValueError("new_norm_scratch: H must be a positive multiple of 8, at most 16384")
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def moe_norm(x, weight, eps: float, out, stream=None):
+    """out (bf16 [T, H]) = x / rms(x) * weight; x fp32 or bf16, weight fp32 [H]
+    or None."""
+    kind = _typed(x, "x")
+    _bf16(out, "out")
+    if x.dim() != 2 or out.shape != x.shape:
+        raise ValueError("moe_norm: inconsistent shapes")
+    T, H = x.shape
+    _maybe(weight, torch.float32, (H,), "weight", "moe_norm")
+    _check("moe_norm", lib().moe_norm(_ptr(x), kind, T, H, _ptr(weight), eps, _ptr(out),
+                                      _stream(stream)))
+
+
+def _block_shapes(call: str, row, y_perm, dest_row, topk_w):
+    """(T, k, H) of a combine: row [T, H], y_perm [n_rows, H], dest_row and topk_w [T, k]
+    (dest_row may also be flat, as the layout writes it)."""
+    _bf16(y_perm, "y_perm")
+    _need(dest_row, torch.int32, "dest_row")
+    _need(topk_w, torch.float32, "topk_w")
+    if row.dim() != 2 or y_perm.dim() != 2 or topk_w.dim() != 2:
+        raise ValueError(f"{call}: inconsistent shapes")
+    T, H = row.shape
+    k = topk_w.shape[1]
+    if topk_w.shape[0] != T or y_perm.shape[1] != H or dest_row.numel() != T * k:
+        raise ValueError(f"{call}: inconsistent shapes")
+    return T, k, H
+
+
+def moe_combine_norm(y_perm, dest_row, topk_w, residual, cfg: BlockCfg, y, ws, shared=None, weight=None,
+                     gate=None, next_weight=None, next_out=None, stream=None):
+    """y = residual_scale * residual + gate * norm(shared + weighted sum of the experts' rows), and
+    next_out = moe_norm of y.  residual and y fp32 or bf16 [T, H] (y may be residual); weight,
+    next_weight fp32 [H] or None; gate fp32 [T] or None; dest_row -1 is a drop."""
+    call = "moe_combine_norm"
+    kind = _typed(residual, "residual")
+    _need(y, residual.dtype, "y")
+    T, k, H = _block_shapes(call, residual, y_perm, dest_row, topk_w)
+    if y.shape != residual.shape:
+        raise ValueError("moe_combine_norm: inconsistent shapes")
+    _maybe(shared, torch.bfloat16, (T, H), "shared", call)
+    _maybe(weight, torch.float32, (H,), "weight", call)
+    _maybe(gate, torch.float32, (T,), "gate", call)
+    _maybe(next_weight, torch.float32, (H,), "next_weight", call)
+    _maybe(next_out, torch.bfloat16, (T, H), "next_out", call)
+    _check(call, lib().moe_combine_norm(
+        _ptr(y_perm), y_perm.shape[0], _ptr(dest_row), _ptr(topk_w), T, k, H, _ptr(shared),
+        _ptr(residual), kind, _ptr(weight), _ptr(gate), ctypes.byref(cfg), _ptr(y),
+        _ptr(next_weight), _ptr(next_out), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def moe_combine_backward(grad_y, y_perm, dest_row, topk_w, grad_y_perm, grad_topk_w, ws, stream=None):
+    """Gradients of moe_combine's expert rows and weights for grad_y (fp32 or bf16 [T, H]); rows of
+    grad_y_perm that no assignment lands on are left as they are."""
+    kind = _typed(grad_y, "grad_y")
+    T, k, H = _block_shapes("moe_combine_backward", grad_y, y_perm, dest_row, topk_w)
+    _bf16(grad_y_perm, "grad_y_perm")
+    _need(grad_topk_w, torch.float32, "grad_topk_w")
+    if grad_y_perm.shape != y_perm.shape or grad_topk_w.shape != topk_w.shape:
+        raise ValueError("moe_combine_backward: inconsistent shapes")
+    _check("moe_combine_backward", lib().moe_combine_backward(
+        _ptr(grad_y), kind, _ptr(y_perm), y_perm.shape[0], _ptr(dest_row), _ptr(topk_w), T, k, H,
+        _ptr(grad_y_perm), _ptr(grad_topk_w), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def moe_permute_backward(grad, dest_row, grad_x, ws, add=None, stream=None):
+    """grad_x (fp32 or bf16 [T, H]) = add + the sum of grad (bf16 [n_rows, H]) over each token's
+    rows; dest_row int32 [T, k]."""
+    kind = _typed(grad_x, "grad_x")
+    _bf16(grad, "grad")
+    _need(dest_row, torch.int32, "dest_row")
+    if grad_x.dim() != 2 or grad.dim() != 2 or dest_row.dim() != 2 or dest_row.shape[0] != grad_x.shape[0] \
+            or grad.shape[1] != grad_x.shape[1]:
+        raise ValueError("moe_permute_backward: inconsistent shapes")
+    T, H = grad_x.shape
+    _maybe(add, torch.bfloat16, (T, H), "add", "moe_permute_backward")
+    _check("moe_permute_backward", lib().moe_permute_backward(
+        _ptr(grad), grad.shape[0], _ptr(dest_row), _ptr(add), T, dest_row.shape[1], H, _ptr(grad_x),
+        kind, _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def moe_combine_norm_backward(grad_y, y_perm, dest_row, topk_w, cfg: BlockCfg, grad_y_perm, grad_topk_w,
+                              ws, scratch=None, shared=None, weight=None, gate=None, grad_shared=None,
+                              grad_weight=None, grad_gate=None, stream=None):
+    """Gradients of moe_combine_norm's expert rows, weights, shared rows, norm weight and gate for
+    grad_y; the last three are written where a tensor is given (grad_weight needs scratch)."""
+    call = "moe_combine_norm_backward"
+    kind = _typed(grad_y, "grad_y")
+    T, k, H = _block_shapes(call, grad_y, y_perm, dest_row, topk_w)
+    _bf16(grad_y_perm, "grad_y_perm")
+    _need(grad_topk_w, torch.float32, "grad_topk_w")
+    if grad_y_perm.shape != y_perm.shape or grad_topk_w.shape != topk_w.shape:
+        raise ValueError("moe_combine_norm_backward: inconsistent shapes")
+    _maybe(shared, torch.bfloat16, (T, H), "shared", call)
+    _maybe(weight, torch.float32, (H,), "weight", call)
+    _maybe(gate, torch.float32, (T,), "gate", call)
+    _maybe(grad_shared, torch.bfloat16, (T, H), "grad_shared", call)
+    _maybe(grad_weight, torch.float32, (H,), "grad_weight", call)
+    _maybe(grad_gate, torch.float32, (T,), "grad_gate", call)
+    if scratch is not None:
+        _need(scratch, torch.uint8, "scratch")
+    _check(call, lib().moe_combine_norm_backward(
+        _ptr(grad_y), kind, _ptr(y_perm), y_perm.shape[0], _ptr(dest_row), _ptr(topk_w), T, k, H,
+        _ptr(shared), _ptr(weight), _ptr(gate), ctypes.byref(cfg), _ptr(grad_y_perm),
+        _ptr(grad_topk_w), _ptr(grad_shared), _ptr(grad_weight), _ptr(grad_gate), _ptr(scratch),
+        0 if scratch is None else scratch.numel(), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def moe_norm_backward(grad, x, weight, eps: float, grad_x, grad_weight, ws, scratch=None, dest_row=None,
+                      add=None, residual_grad=None, residual_scale: float = 1.0, stream=None):
+    """grad_x (the type of x) = residual_scale * residual_grad + the gradient of moe_norm for
+    add + grad (bf16 [T, H]), or with dest_row (int32 [T, k]) for add + the sum of each token's rows
+    of grad (bf16 [n_rows, H]).  grad_weight fp32 [H] (with scratch) or None."""
+    call = "moe_norm_backward"
+    kind = _typed(x, "x")
+    _bf16(grad, "grad")
+    _need(grad_x, x.dtype, "grad_x")
+    if x.dim() != 2 or grad.dim() != 2 or grad_x.shape != x.shape or grad.shape[1] != x.shape[1]:
+        raise ValueError("moe_norm_backward: inconsistent shapes")
+    T, H = x.shape
+    k = 0
+    if dest_row is not None:
+        _need(dest_row, torch.int32, "dest_row")
+        if dest_row.dim() != 2 or dest_row.shape[0] != T:
+            raise ValueError("moe_norm_backward: inconsistent shapes")
+        k = dest_row.shape[1]
+    _maybe(weight, torch.float32, (H,), "weight", call)
+    _maybe(add, torch.bfloat16, (T, H), "add", call)
+    _maybe(residual_grad, x.dtype, (T, H), "residual_grad", call)
+    _maybe(grad_weight, torch.float32, (H,), "grad_weight", call)
+    if scratch is not None:
+        _need(scratch, torch.uint8, "scratch")
+    _check(call, lib().moe_norm_backward(
+        _ptr(grad), grad.shape[0], _ptr(dest_row), k, _ptr(add), _ptr(x), kind, T, H, _ptr(weight),
+        eps, _ptr(residual_grad), residual_scale, _ptr(grad_x), _ptr(grad_weight), _ptr(scratch),
+        0 if scratch is None else scratch.numel(), _ptr(ws), ws.numel(), _stream(stream)))
 
 
 def moe_status_string(status: int) -> str:

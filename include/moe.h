@@ -747,6 +747,127 @@ moe_status moe_combine_merged(const uint16_t *y_perm, const int32_t *dest_row, c
                               int32_t k, int32_t H, const uint16_t *shared, uint16_t *y,
                               int32_t *messages, void *ws, size_t ws_bytes, void *stream);
 
+/* The block around the experts: an RMS norm before it, and after it the
+ * weighted sum of the experts' rows through a norm, a gate and a residual.
+ *  post_norm       1: the sum is normalised; 0: it is taken as it is.
+ *  eps             of the norms, positive and finite.
+ *  residual_scale  factor of the residual, finite. */
+typedef struct moe_block_cfg {
+  int32_t post_norm;
+  float eps;
+  float residual_scale;
+} moe_block_cfg;
+
+/* Norm before the block: out[t, h] = x[t, h] / rms(x[t]) * weight[h] with
+ * rms(v) = sqrt(mean(v^2) + eps), in fp32 with one rounding.  The rows that the
+ * router reads and moe_permute dispatches ("14. Serving Mixture-of-Experts
+ * Models", "Follow one token").
+ *  x       device fp32 or bf16 (x_type) [T, H];  out device bf16 [T, H], which
+ *          may be x itself when x is bf16.
+ *  weight  device fp32 [H], 16-byte aligned, or NULL for ones.
+ *  Rows of finite values have a finite norm whatever their size (squares beyond
+ *  fp32's range are summed scaled down).  Limits: H % 8 == 0, H <= 16384. */
+moe_status moe_norm(const void *x, int32_t x_type, int64_t T, int32_t H, const float *weight,
+                    float eps, uint16_t *out, void *stream);
+
+/* Combine through the norm after the block, its gate and the residual; and the
+ * norm before the next block in the same pass:
+ *   c[t] = shared[t] + sum_j topk_w[t, j] * y_perm[dest_row[t, j]]      (fp32)
+ *   f[t] = c[t] / rms(c[t]) * weight  (cfg->post_norm), or c[t]
+ *   y[t] = residual_scale * residual[t] + gate[t] * f[t]   (rounded once)
+ *   next_out[t] = moe_norm of y[t], as it is held, with next_weight.
+ * "14. Serving Mixture-of-Experts Models", "Follow one token", step 4 (the
+ * inverse permutation followed by a weighted sum).
+ *  y_perm    device bf16 [n_rows, H];  dest_row device int32 [T, k]: -1 is a
+ *            dropped assignment and adds nothing.
+ *  topk_w    device fp32 [T, k];  shared device bf16 [T, H] or NULL.
+ *  residual  device fp32 or bf16 (x_type) [T, H];  y the same type, and it may
+ *            be residual itself.
+ *  weight    device fp32 [H] or NULL for ones (NULL without post_norm);
+ *  gate      device fp32 [T] or NULL for ones.
+ *  next_out  device bf16 [T, H] or NULL;  next_weight device fp32 [H] or NULL.
+ *  Other outputs overlap no input.  Weights are 16-byte aligned.  ws: at least
+ *  MOE_WS_STATUS_BYTES.  Limits: H % 8 == 0, H <= 16384, k <= 16, T * k < 2^31,
+ *  n_rows < 2^31.  Device errors: MOE_ERR_DEVICE_INDEX (a row outside
+ *  [-1, n_rows): its assignment is skipped). */
+moe_status moe_combine_norm(const uint16_t *y_perm, int64_t n_rows, const int32_t *dest_row,
+                            const float *topk_w, int64_t T, int32_t k, int32_t H,
+                            const uint16_t *shared, const void *residual, int32_t x_type,
+                            const float *weight, const float *gate, const moe_block_cfg *cfg,
+                            void *y, const float *next_weight, uint16_t *next_out, void *ws,
+                            size_t ws_bytes, void *stream);
+
+/* Gradient of moe_combine's sum y[t] = sum_j topk_w[t, j] y_perm[dest_row[t, j]]:
+ *   grad_y_perm[dest_row[t, j]] = topk_w[t, j] * grad_y[t]     (rounded once)
+ *   grad_topk_w[t, j] = grad_y[t] . y_perm[dest_row[t, j]]     (fp32)
+ * A dropped assignment (-1) gets the weight gradient 0; rows of grad_y_perm that
+ * no assignment lands on are left unwritten.  The gradient of moe_combine's
+ * shared rows is grad_y itself.
+ *  grad_y device fp32 or bf16 (x_type) [T, H]; grad_y_perm bf16 [n_rows, H],
+ *  overlapping no input; grad_topk_w fp32 [T, k].  The rows of dest_row are
+ *  distinct.  Other arguments, limits and errors as moe_combine_norm. */
+moe_status moe_combine_backward(const void *grad_y, int32_t x_type, const uint16_t *y_perm,
+                                int64_t n_rows, const int32_t *dest_row, const float *topk_w,
+                                int64_t T, int32_t k, int32_t H, uint16_t *grad_y_perm,
+                                float *grad_topk_w, void *ws, size_t ws_bytes, void *stream);
+
+/* Gradient of moe_permute: grad_x[t] = add[t] + sum_j grad[dest_row[t, j]], in
+ * fp32 with one rounding; a dropped assignment (-1) adds nothing.
+ *  grad device bf16 [n_rows, H]; add device bf16 [T, H] or NULL (what reaches x
+ *  by other ways: the router, a shared expert); grad_x device fp32 or bf16
+ *  (x_type) [T, H], overlapping no input.  Other arguments, limits and errors as
+ *  moe_combine_norm. */
+moe_status moe_permute_backward(const uint16_t *grad, int64_t n_rows, const int32_t *dest_row,
+                                const uint16_t *add, int64_t T, int32_t k, int32_t H, void *grad_x,
+                                int32_t x_type, void *ws, size_t ws_bytes, void *stream);
+
+/* Bytes of scratch that the gradient of a norm's weight needs for T rows of H
+ * on the current device; 0 for no rows or invalid sizes.  Scratch holds nothing
+ * between calls; calls that share it must be ordered on one stream. */
+size_t moe_norm_scratch_bytes(int64_t T, int32_t H);
+
+/* Gradient of moe_combine_norm's y.  With c, f as there, grad_y = dy and
+ * e = dy * weight, r = 1 / rms(c):
+ *   dc = gate * r * (e - c * r^2 * mean(e c))    (without post_norm gate * dy)
+ *   grad_y_perm[dest_row[t, j]] = topk_w[t, j] * dc[t]
+ *   grad_topk_w[t, j] = dc[t] . y_perm[dest_row[t, j]]
+ *   grad_shared[t] = dc[t];  grad_gate[t] = sum_h dy f
+ *   grad_weight[h] = sum_t gate dy c r
+ * and the gradient of the residual is residual_scale * grad_y (see
+ * moe_norm_backward).  Sums are fp32 in an order fixed by the sizes and the
+ * device: the same call gives the same bits.
+ *  grad_shared device bf16 [T, H], grad_weight fp32 [H] (post_norm only) and
+ *  grad_gate fp32 [T] may each be NULL; grad_weight needs scratch of
+ *  moe_norm_scratch_bytes, 16-byte aligned.  Outputs overlap no input.  Other
+ *  arguments, limits and errors as moe_combine_norm and moe_combine_backward. */
+moe_status moe_combine_norm_backward(const void *grad_y, int32_t x_type, const uint16_t *y_perm,
+                                     int64_t n_rows, const int32_t *dest_row, const float *topk_w,
+                                     int64_t T, int32_t k, int32_t H, const uint16_t *shared,
+                                     const float *weight, const float *gate,
+                                     const moe_block_cfg *cfg, uint16_t *grad_y_perm,
+                                     float *grad_topk_w, uint16_t *grad_shared, float *grad_weight,
+                                     float *grad_gate, void *scratch, size_t scratch_bytes,
+                                     void *ws, size_t ws_bytes, void *stream);
+
+/* Gradient of moe_norm and of the residual beside it, reading the gradient of
+ * its output from the dispatched rows (moe_permute_backward in the same pass):
+ *   u[t] = add[t] + sum_j grad[dest_row[t, j]], or add[t] + grad[t] where
+ *          dest_row is NULL (n_rows == T then, and k is not used)
+ *   grad_x[t] = residual_scale * residual_grad[t]
+ *               + r (u weight - x r^2 mean(u weight x)),  r = 1 / rms(x[t])
+ *   grad_weight[h] = sum_t u x r
+ *  grad device bf16 [n_rows, H]; add device bf16 [T, H] or NULL; x, residual_grad
+ *  (or NULL) and grad_x device fp32 or bf16 (x_type) [T, H]; grad_x may be
+ *  residual_grad itself and overlaps no other input.  grad_weight fp32 [H] or
+ *  NULL; scratch as for moe_combine_norm_backward.  Limits and errors as
+ *  moe_combine_norm. */
+moe_status moe_norm_backward(const uint16_t *grad, int64_t n_rows, const int32_t *dest_row,
+                             int32_t k, const uint16_t *add, const void *x, int32_t x_type,
+                             int64_t T, int32_t H, const float *weight, float eps,
+                             const void *residual_grad, float residual_scale, void *grad_x,
+                             float *grad_weight, void *scratch, size_t scratch_bytes, void *ws,
+                             size_t ws_bytes, void *stream);
+
 /* Balancedness of one step: mean per-rank load over the busiest rank's
  * load, total / (R * max) in fp64; 1.0 when total is 0.  "14. Serving
  * Mixture-of-Experts Models", "The slowest expert sets the pace" (loads
