@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libmoe.so")
 
 SOURCES = ["api.cu", "route.cu", "layout.cu", "movers.cu", "fp8.cu", "grouped_ffn.cu",
            "grouped_ffn_pair.cu", "gate.cu", "fp4.cu", "fp4_product.cu",
-           "block.cu"]
+           "block.cu", "int4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-I", INCLUDE, "-I", CSRC]

@@ -155,6 +155,10 @@ _SIGNATURES = {
     "moe_pack_weights_fp4": (ctypes.c_int, [_P, _P, _I32, _I32, _I32, _I32, _I32, _P, _P]),
     "moe_grouped_product_fp4": (ctypes.c_int, [_P, _P, _I64, _P, _P, _I32, _I32, _P, _I32, _I32,
                                                _I32, _I32, _P, _P, _I32, _P, _SZ, _P]),
+    "moe_int4_packed_bytes": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32]),
+    "moe_pack_weights_int4": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _P]),
+    "moe_grouped_product_int4": (ctypes.c_int, [_P, _I64, _P, _P, _I32, _I32, _P, _I32, _I32, _I32,
+                                                _I32, _I32, _P, _I32, _P, _SZ, _P]),
     "moe_norm": (ctypes.c_int, [_P, _I32, _I64, _I32, _P, _F32, _P, _P]),
     "moe_combine_norm": (ctypes.c_int, [_P, _I64, _P, _P, _I64, _I32, _I32, _P, _P, _I32, _P, _P,
                                         ctypes.POINTER(BlockCfg), _P, _P, _P, _P, _SZ, _P]),
@@ -867,6 +871,53 @@ def moe_grouped_product_fp4(codes, sf, seg_offsets, seg_expert, w: Fp4Weights, a
         _ptr(codes), _ptr(sf), n, _ptr(seg_offsets), _ptr(seg_expert), S, w.E, _ptr(w.data), w.N, K,
         w.fmt, w.epilogue, _ptr(alpha), _ptr(out), _TYPES[out.dtype], _ptr(ws), ws.numel(),
         _stream(stream)))
+
+
+# ------------------------------------------------------------------ 4-bit integer experts
+class Int4Weights:
+    """Expert weights in the int4 product's layout (moe_pack_weights_int4)."""
+
+    def __init__(self, data: torch.Tensor, E: int, N: int, K: int, group: int, has_zeros: bool, epilogue: int):
+        self.data, self.E, self.N, self.K = data, E, N, K
+        self.group, self.has_zeros, self.epilogue = group, has_zeros, epilogue
+
+
+def pack_weights_int4(codes, scales, zeros, epilogue: int, stream=None) -> Int4Weights:
+    """4-bit expert weights (codes uint8 [E, N, K/2], scales bf16 [E, N, K/group], zeros uint8 of
+    the scales' shape or None for 8) into a new Int4Weights for products with `epilogue`."""
+    _need(codes, torch.uint8, "codes")
+    _bf16(scales, "scales")
+    if codes.dim() != 3 or scales.dim() != 3 or scales.shape[:2] != codes.shape[:2] or scales.shape[2] < 1:
+        raise ValueError("pack_weights_int4: inconsistent shapes")
+    E, N, K = codes.shape[0], codes.shape[1], 2 * codes.shape[2]
+    group = K // scales.shape[2]
+    if group * scales.shape[2] != K:
+        raise ValueError("pack_weights_int4: inconsistent shapes")
+    _maybe(zeros, torch.uint8, scales.shape, "zeros", "pack_weights_int4")
+    has = zeros is not None
+    n = int(lib().moe_int4_packed_bytes(E, N, K, group, int(has), epilogue))
+    # allocated on the stream that writes it, see pack_weights_fp4
+    with torch.cuda.stream(stream):
+        data = torch.empty(n, dtype=torch.uint8, device=codes.device)
+    _check("moe_pack_weights_int4", lib().moe_pack_weights_int4(
+        _ptr(codes), _ptr(scales), _ptr(zeros), E, N, K, group, epilogue, _ptr(data), _stream(stream)))
+    return Int4Weights(data, E, N, K, group, has, epilogue)
+
+
+def moe_grouped_product_int4(x, seg_offsets, seg_expert, w: Int4Weights, out, ws, stream=None):
+    """bf16 rows [n, K] in per-expert segments times the experts' 4-bit weights, with the epilogue
+    that w was packed for: out fp32 or bf16 [n, N] (SwiGLU: [n, N/2])."""
+    _bf16(x, "x")
+    _need(seg_offsets, torch.int32, "seg_offsets")
+    _need(seg_expert, torch.int32, "seg_expert")
+    kind = _typed(out, "out")
+    S = seg_expert.numel()
+    cols = w.N // 2 if w.epilogue == MOE_EPI_SWIGLU else w.N
+    if x.dim() != 2 or x.shape[1] != w.K or out.shape != (x.shape[0], cols) or seg_offsets.numel() != S + 1:
+        raise ValueError("moe_grouped_product_int4: inconsistent shapes")
+    _check("moe_grouped_product_int4", lib().moe_grouped_product_int4(
+        _ptr(x), x.shape[0], _ptr(seg_offsets), _ptr(seg_expert), S, w.E, _ptr(w.data), w.N, w.K, w.group,
+        int(w.has_zeros), w.epilogue, _ptr(out), kind, _ptr(ws), ws.numel(), _stream(stream)))
 
 
 # ------------------------------------------------------------------ the block around the experts

@@ -705,6 +705,51 @@ moe_status moe_grouped_product_fp4(const uint8_t *codes, const uint8_t *sf, int6
                                    void *out, int32_t out_type, void *ws, size_t ws_bytes,
                                    void *stream);
 
+/* 4-bit integer expert weights with group scales: w[n, k] = (q[n, k] - z) * s,
+ * with codes q in 0..15, two to a byte, the even k in the low half (uint8 [E, N,
+ * K/2]), and scale s and zero z shared by `group` (32, 64 or 128) consecutive k
+ * of a row: scales bf16 [E, N, K/group], zeros uint8 [E, N, K/group] with values
+ * 0..127, or NULL for z = 8.  "Mixture-of-Experts Inference", "Memory pressure"
+ * (a decode step is dominated by loading the expert weights).
+ * moe_pack_weights_int4 rearranges them into the order that
+ * moe_grouped_product_int4 streams; done once per set of weights.  epilogue is
+ * the product's: with MOE_EPI_SWIGLU rows 0..N/2-1 of an expert are gate, the
+ * others up.  packed: device, moe_int4_packed_bytes bytes (0 for invalid
+ * arguments), not overlapping the inputs; codes and packed 16-byte aligned.
+ * Limits: K % group == 0, K <= 2^24, N % 8 == 0 (SwiGLU: N % 16 == 0). */
+size_t moe_int4_packed_bytes(int32_t E, int32_t N, int32_t K, int32_t group, int32_t has_zeros,
+                             int32_t epilogue);
+moe_status moe_pack_weights_int4(const uint8_t *codes, const uint16_t *scales,
+                                 const uint8_t *zeros, int32_t E, int32_t N, int32_t K,
+                                 int32_t group, int32_t epilogue, uint8_t *packed, void *stream);
+
+/* Grouped product of bf16 rows with 4-bit integer expert weights, one segment an
+ * expert ("14. Serving Mixture-of-Experts Models", "Follow one token", step 3),
+ * for decode steps: the weights are streamed once for up to 32 rows of a segment
+ * and again (from L2) for more, so large segments are better served by the
+ * bf16 or FP4 experts.  For segment s, e = seg_expert[s], row r in
+ * [seg_offsets[s], seg_offsets[s+1]) (no weight is rounded, fp32 accumulation,
+ * one rounding):
+ *   MOE_EPI_NONE    out[r, n] = sum_K x[r, K] w[e, n, K],  n < N
+ *   MOE_EPI_SWIGLU  out[r, n] = silu(g) * u,  n < N/2, with g from weight row n
+ *                   and u from weight row N/2 + n
+ *  x           device bf16 [n_rows, K], contiguous, 16-byte aligned.
+ *  seg_offsets device int32 [S+1], seg_expert device int32 [S].
+ *  w_packed    moe_pack_weights_int4 of the same E, N, K, group, zeros or none
+ *              (has_zeros) and epilogue.
+ *  out         device fp32 or bf16 (out_type) [n_rows, N or N/2], contiguous,
+ *              16-byte aligned; rows outside every segment are left unwritten.
+ *  Limits: those of moe_pack_weights_int4, S <= 1024, n_rows < 2^31 - 64, and
+ *  (n_rows / 8 + S) * N / 32 (SwiGLU: the same) below 2^31 - 65536 tiles.  ws: at
+ *  least MOE_WS_STATUS_BYTES.  Device errors: MOE_ERR_DEVICE_INDEX (an expert id
+ *  or a segment outside its range: the segment is skipped; offsets that decrease:
+ *  nothing is computed). */
+moe_status moe_grouped_product_int4(const uint16_t *x, int64_t n_rows, const int32_t *seg_offsets,
+                                    const int32_t *seg_expert, int32_t S, int32_t E,
+                                    const uint8_t *w_packed, int32_t N, int32_t K, int32_t group,
+                                    int32_t has_zeros, int32_t epilogue, void *out,
+                                    int32_t out_type, void *ws, size_t ws_bytes, void *stream);
+
 /* Combine: y[t] = bf16(acc) with acc = shared[t] (or 0) and, for j = 0..k-1
  * in order, acc = fmaf(topk_w[t,j], y_perm[dest_row[t*k+j]], acc) in fp32.
  * "14. Serving Mixture-of-Experts Models", "Follow one token", step 4 (the
