@@ -725,7 +725,7 @@ moe_status moe_pack_weights_int4(const uint8_t *codes, const uint16_t *scales,
 
 /* Grouped product of bf16 rows with 4-bit integer expert weights, one segment an
  * expert ("14. Serving Mixture-of-Experts Models", "Follow one token", step 3),
- * for decode steps: the weights are streamed once for up to 32 rows of a segment
+ * for decode steps: the weights are streamed once for up to 16 rows of a segment
  * and again (from L2) for more, so large segments are better served by the
  * bf16 or FP4 experts.  For segment s, e = seg_expert[s], row r in
  * [seg_offsets[s], seg_offsets[s+1]) (no weight is rounded, fp32 accumulation,

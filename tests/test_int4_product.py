@@ -164,7 +164,8 @@ def test_against_64_bits(case, dtype):
 
 @pytest.mark.gpu
 def test_a_row_does_not_depend_on_the_others():
-    """The same row alone, among few and among many of its segment: the same bits."""
+    """The same row alone, among few and among many of its segment: the same bits (as long as the
+    number of tasks does not change how K is split)."""
     case = ((100,), 0, 1, 72, 640, 64, True, False)
     args, _, n = setup(case, 3)
     x, _, experts, w = args
