@@ -9,7 +9,7 @@
 //
 // All are bound by HBM: a row is read once, kept in registers across the row's
 // reductions, and each result is written once.  A token takes a team of threads.
-// Every thread copies its own 16-byte pieces of the token's rows to its own place
+// Every thread copies its own 16-byte pieces of the token's rows to its own places
 // in shared memory (cp.async, no barrier), and as soon as it has used a piece it
 // asks for the next token's: the reads go on while a token's sums meet and its
 // results are written.  With plain loads into registers instead, 4096 tokens of
@@ -35,22 +35,58 @@ struct Rows {
   int32_t *status;
 };
 
-__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(u[i] << 16);
-    f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-  }
-}
-
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&p);
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+// Two fp32 numbers for the instructions that take two at a time.
+typedef unsigned long long Pair;
+__device__ __forceinline__ Pair pair(float a, float b) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ Pair both(float a) { return pair(a, a); }
+__device__ __forceinline__ void split(Pair v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ float sum(Pair v) {
+  float a, b;
+  split(v, a, b);
+  return a + b;
+}
+__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair plus(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float dot(const Pair (&a)[4], const Pair (&b)[4]) {
+  return sum(fma(a[3], b[3], fma(a[2], b[2], fma(a[1], b[1], mul(a[0], b[0])))));
+}
+__device__ __forceinline__ void unpack(const uint4 &v, Pair (&f)[4]) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    f[i] = pair(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t pack_pair(Pair v) {
+  float a, b;
+  split(v, a, b);
+  return pack2(a, b);
+}
+__device__ __forceinline__ uint4 pack(const Pair (&f)[4]) {
+  return make_uint4(pack_pair(f[0]), pack_pair(f[1]), pack_pair(f[2]), pack_pair(f[3]));
 }
 
 // Eight elements of a row held as bf16 (one 16-byte access) or fp32 (two).
@@ -67,8 +103,8 @@ struct Chunk<__nv_bfloat16> {
   __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
     a = *reinterpret_cast<const uint4 *>(p);
   }
-  __device__ __forceinline__ void get(float (&f)[8]) const { unpack8(a, f); }
-  __device__ __forceinline__ void set(const float (&f)[8]) { a = pack8(f); }
+  __device__ __forceinline__ void get(Pair (&f)[4]) const { unpack(a, f); }
+  __device__ __forceinline__ void set(const Pair (&f)[4]) { a = pack(f); }
   __device__ __forceinline__ void store(__nv_bfloat16 *p) const {
     *reinterpret_cast<uint4 *>(p) = a;
   }
@@ -85,13 +121,14 @@ struct Chunk<float> {
     a = reinterpret_cast<const float4 *>(p)[0];
     b = reinterpret_cast<const float4 *>(p)[1];
   }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  __device__ __forceinline__ void get(Pair (&f)[4]) const {
+    f[0] = pair(a.x, a.y), f[1] = pair(a.z, a.w), f[2] = pair(b.x, b.y), f[3] = pair(b.z, b.w);
   }
-  __device__ __forceinline__ void set(const float (&f)[8]) {
-    a = make_float4(f[0], f[1], f[2], f[3]);
-    b = make_float4(f[4], f[5], f[6], f[7]);
+  __device__ __forceinline__ void set(const Pair (&f)[4]) {
+    split(f[0], a.x, a.y);
+    split(f[1], a.z, a.w);
+    split(f[2], b.x, b.y);
+    split(f[3], b.z, b.w);
   }
   __device__ __forceinline__ void store(float *p) const {
     reinterpret_cast<float4 *>(p)[0] = a;
@@ -100,16 +137,16 @@ struct Chunk<float> {
 };
 
 // Eight weights of a norm (ones without).
-__device__ __forceinline__ void load_weight(const float *w, int c, float (&f)[8]) {
+__device__ __forceinline__ void load_weight(const float *w, int c, Pair (&f)[4]) {
   if (w == nullptr) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = 1.0f;
+    for (int i = 0; i < 4; ++i) f[i] = both(1.0f);
     return;
   }
-  const float4 a = __ldg(reinterpret_cast<const float4 *>(w) + 2 * c);
-  const float4 b = __ldg(reinterpret_cast<const float4 *>(w) + 2 * c + 1);
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-  f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  Chunk<float> v;
+  v.a = __ldg(reinterpret_cast<const float4 *>(w) + 2 * c);
+  v.b = __ldg(reinterpret_cast<const float4 *>(w) + 2 * c + 1);
+  v.get(f);
 }
 
 // Sums over a warp of N values (a power of two) in N - 1 + log2(32 / N)
@@ -165,8 +202,19 @@ struct Team {
   }
 };
 
-__device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 16 bytes, or zeros where there are none to copy.
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool some) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(some ? 16 : 0)
+               : "memory");
+}
+// A piece of a row of X, `at` elements into p.
+template <typename X>
+__device__ __forceinline__ void copy_piece(uint32_t dst, int step, const void *p, int64_t at,
+                                           bool some) {
+#pragma unroll
+  for (int i = 0; i < Chunk<X>::N; ++i)
+    copy_async(dst + i * step, static_cast<const X *>(p) + at + 4 * i, some);
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -184,35 +232,32 @@ struct Norm {
   float pre, r;  // the row's factor, and 1 / rms of the row times it
 };
 template <int U>
-__device__ __forceinline__ Norm row_norm(float (&x)[U][8], int H, float eps, float *buf,
+__device__ __forceinline__ Norm row_norm(Pair (&x)[U][4], int H, float eps, float *buf,
                                          const Team &tm) {
-  const int warp = tm.warp, nw = tm.nw, lane = tm.lane;
-  float s[1] = {0.0f};
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s[0] = fmaf(x[u][i], x[u][i], s[0]);
-  put_sums(s, buf, warp, lane);
-  tm.sync();
-  float sum = total(buf, 0, nw, lane);
-  Norm n{1.0f, 0.0f};
-  if (!(sum <= FLT_MAX)) {
-    n.pre = kShrink;
-    s[0] = 0.0f;
+  auto squares = [&]() {
+    Pair s = mul(x[0][0], x[0][0]);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[u][i] *= kShrink;
-        s[0] = fmaf(x[u][i], x[u][i], s[0]);
-      }
+      for (int i = u == 0; i < 4; ++i) s = fma(x[u][i], x[u][i], s);
+    float v[1] = {sum(s)};
+    put_sums(v, buf, tm.warp, tm.lane);
     tm.sync();
-    put_sums(s, buf, warp, lane);
+    return total(buf, 0, tm.nw, tm.lane);
+  };
+  float s = squares();
+  Norm n{1.0f, 0.0f};
+  if (!(s <= FLT_MAX)) {
+    n.pre = kShrink;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[u][i] = mul(x[u][i], both(kShrink));
     tm.sync();
-    sum = total(buf, 0, nw, lane);
+    s = squares();
     eps = 0.0f;
   }
-  n.r = inv_rms(sum, H, eps);
+  n.r = inv_rms(s, H, eps);
   return n;
 }
 
@@ -252,16 +297,27 @@ __device__ __forceinline__ Meta load_meta(const int32_t *dest_row, const float *
   }
   return m;
 }
-// Rows outside are reported and dropped.
+// Rows outside are reported and dropped; a dropped assignment weighs nothing.
 __device__ __forceinline__ void settle(Meta &m, const Rows &p, int64_t t, int k, const Team &tm) {
   if (m.row != -1 && (m.row < 0 || m.row >= p.n_rows)) {
     if (tm.warp == 0)
       moe::report_error(p.status, MOE_ERR_DEVICE_INDEX, (int32_t)(t * k + tm.lane), moe::K_BLOCK);
     m.row = -1;
   }
+  if (m.row < 0) m.w = 0.0f;
+}
+// A token's rows to a thread's places, `step` bytes apart: zeros for dropped ones
+// and for threads past the row's end (which take its last piece's address c).
+__device__ __forceinline__ void copy_rows(uint32_t dst, int step, const uint4 *rows, const Meta &m,
+                                          int k, int H8, int c, bool in) {
+#pragma unroll 4
+  for (int j = 0; j < k; ++j) {
+    const int32_t r = __shfl_sync(0xffffffffu, m.row, j);
+    copy_async(dst + j * step, rows + (int64_t)max(r, 0) * H8 + c, in && r >= 0);
+  }
 }
 
-// out = x / rms(x) * weight.
+// out = x / rms(x) * weight.  R / U tokens are on their way.
 template <int U, int R, typename X>
 __global__ void __launch_bounds__(kRowThreads)
     norm_kernel(const X *x, int64_t T, int H, const float *__restrict__ weight, float eps,
@@ -274,41 +330,37 @@ __global__ void __launch_bounds__(kRowThreads)
   const uint32_t dst = smem_u32(mine);
   moe::pdl_wait();
   moe::pdl_trigger();
-  auto fetch = [&](int64_t t, int u) {
+  auto fetch = [&](int64_t t, int u, int at) {
     const int c = tm.tid + u * tm.threads;
-    if (t < T && c < H8) {
-      const X *src = x + t * H + 8 * c;
-#pragma unroll
-      for (int i = 0; i < Chunk<X>::N; ++i)
-        copy_async(dst + (u % R) * slot + i * step, src + 4 * i);
-    }
+    if (t < T)
+      copy_piece<X>(dst + at * slot, step, x, t * H + 8 * (int64_t)min(c, H8 - 1), c < H8);
     copy_commit();
   };
+  static_assert(R % U == 0, "whole tokens");
 #pragma unroll
-  for (int u = 0; u < R; ++u) fetch(blockIdx.x, u);
-  int par = 0;
+  for (int u = 0; u < R; ++u) fetch(blockIdx.x + u / U * (int64_t)gridDim.x, u % U, u);
+  int par = 0, at = 0;
   for (int64_t t = blockIdx.x; t < T; t += gridDim.x, par ^= 1) {
-    float v[U][8] = {};
+    Pair v[U][4];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       copy_wait<R - 1>();
-      if (tm.tid + u * tm.threads < H8) {
-        Chunk<X> in;
-        in.take(mine + (u % R) * slot, step);
-        in.get(v[u]);
-      }
-      fetch(u + R < U ? t : t + gridDim.x, (u + R) % U);
+      Chunk<X> in;
+      in.take(mine + (at + u) * slot, step);
+      in.get(v[u]);
+      fetch(t + R / U * (int64_t)gridDim.x, u, at + u);
     }
+    at = at + U == R ? 0 : at + U;
     const Norm n = row_norm(v, H, eps, buf[par], tm);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c = tm.tid + u * tm.threads;
       if (c >= H8) continue;
-      float w[8], o[8];
+      Pair w[4];
       load_weight(weight, c, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = v[u][i] * n.r * w[i];
-      *reinterpret_cast<uint4 *>(out + t * H + 8 * c) = pack8(o);
+      for (int i = 0; i < 4; ++i) w[i] = mul(mul(v[u][i], both(n.r)), w[i]);
+      *reinterpret_cast<uint4 *>(out + t * H + 8 * c) = pack(w);
     }
   }
 }
@@ -347,20 +399,13 @@ __global__ void __launch_bounds__(kRowThreads) combine_norm_kernel(const Combine
   };
   auto fetch = [&](int64_t t, const Meta &m, int u) {
     if (t < p.T) {
-      const int c = tm.tid + u * tm.threads;
+      const int c = tm.tid + u * tm.threads, cl = min(c, H8 - 1);
       const bool in = c < H8;
       const uint32_t d = dst + (u % R) * slot;
-      for (int j = 0; j < p.k; ++j) {
-        const int32_t r = __shfl_sync(0xffffffffu, m.row, j);
-        if (in && r >= 0) copy_async(d + j * step, p.yp + (int64_t)r * H8 + c);
-      }
-      if (in) {
-        // (y may be the residual itself: a token's row is read before it is written)
-        const X *src = static_cast<const X *>(p.residual) + t * p.H + 8 * c;
-#pragma unroll
-        for (int i = 0; i < Chunk<X>::N; ++i) copy_async(d + at_res + i * step, src + 4 * i);
-        if (p.shared) copy_async(d + at_shared, p.shared + t * H8 + c);
-      }
+      copy_rows(d, step, p.yp, m, p.k, H8, cl, in);
+      // (y may be the residual itself: a token's row is read before it is written)
+      copy_piece<X>(d + at_res, step, p.residual, t * p.H + 8 * (int64_t)cl, in);
+      if (p.shared) copy_async(d + at_shared, p.shared + t * H8 + cl, in);
     }
     copy_commit();
   };
@@ -373,27 +418,23 @@ __global__ void __launch_bounds__(kRowThreads) combine_norm_kernel(const Combine
   for (int64_t t = blockIdx.x; t < p.T; t += stride, par ^= 1) {
     settle(next, p.rows, t + stride, p.k, tm);
     const Meta after = meta(t + 2 * stride);
-    float acc[U][8] = {};
+    Pair acc[U][4];
     Chunk<X> res[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       copy_wait<R - 1>();
-      const bool in = tm.tid + u * tm.threads < H8;
       const uint8_t *s = mine + (u % R) * slot;
-      if (in) {
-        res[u].take(s + at_res, step);
-        if (p.shared) unpack8(*reinterpret_cast<const uint4 *>(s + at_shared), acc[u]);
-      }
+      res[u].take(s + at_res, step);
+      uint4 first = make_uint4(0, 0, 0, 0);
+      if (p.shared) first = *reinterpret_cast<const uint4 *>(s + at_shared);
+      unpack(first, acc[u]);
 #pragma unroll 4
       for (int j = 0; j < p.k; ++j) {
-        const float w = __shfl_sync(0xffffffffu, now.w, j);
-        const int32_t r = __shfl_sync(0xffffffffu, now.row, j);
-        if (in && r >= 0) {
-          float f[8];
-          unpack8(*reinterpret_cast<const uint4 *>(s + j * step), f);
+        const Pair w = both(__shfl_sync(0xffffffffu, now.w, j));
+        Pair f[4];
+        unpack(*reinterpret_cast<const uint4 *>(s + j * step), f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) acc[u][i] = fmaf(w, f[i], acc[u][i]);
-        }
+        for (int i = 0; i < 4; ++i) acc[u][i] = fma(w, f[i], acc[u][i]);
       }
       if (u + R < U)
         fetch(t, now, u + R);
@@ -405,14 +446,16 @@ __global__ void __launch_bounds__(kRowThreads) combine_norm_kernel(const Combine
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c = tm.tid + u * tm.threads;
-      if (c >= H8) continue;
-      float wt[8], x[8];
-      load_weight(p.weight, c, wt);
+      Pair wt[4], x[4];
+      load_weight(p.weight, min(c, H8 - 1), wt);
       res[u].get(x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[u][i] = fmaf(p.scale, x[i], now.g * (acc[u][i] * rc * wt[i]));
+      for (int i = 0; i < 4; ++i) {
+        const Pair f = mul(mul(acc[u][i], both(rc)), wt[i]);
+        acc[u][i] = fma(both(p.scale), x[i], mul(both(now.g), f));
+      }
       res[u].set(acc[u]);
-      res[u].store(static_cast<X *>(p.y) + t * p.H + 8 * c);
+      if (c < H8) res[u].store(static_cast<X *>(p.y) + t * p.H + 8 * c);
       res[u].get(acc[u]);  // as it is held
     }
     if (p.next) {
@@ -421,11 +464,11 @@ __global__ void __launch_bounds__(kRowThreads) combine_norm_kernel(const Combine
       for (int u = 0; u < U; ++u) {
         const int c = tm.tid + u * tm.threads;
         if (c >= H8) continue;
-        float wt[8], o[8];
+        Pair wt[4];
         load_weight(p.next_weight, c, wt);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = acc[u][i] * n.r * wt[i];
-        p.next[t * H8 + c] = pack8(o);
+        for (int i = 0; i < 4; ++i) wt[i] = mul(mul(acc[u][i], both(n.r)), wt[i]);
+        p.next[t * H8 + c] = pack(wt);
       }
     }
     now = next;
@@ -464,11 +507,11 @@ __global__ void __launch_bounds__(128) combine_bwd_kernel(const CombineBwdParams
   for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, par ^= 1) {
     int32_t r[KMAX];
     const uint32_t live = token_rows(p.rows, t, p.k, r);
-    float w[KMAX], dot[KMAX];
+    float w[KMAX], sums[KMAX];
 #pragma unroll
     for (int j = 0; j < KMAX; ++j) {
       if (j < p.k) w[j] = __ldg(p.topk_w + t * p.k + j);
-      dot[j] = 0.0f;
+      sums[j] = 0.0f;
     }
     for (int c = threadIdx.x; c < H8; c += blockDim.x) {
       uint4 v[KMAX];
@@ -477,22 +520,20 @@ __global__ void __launch_bounds__(128) combine_bwd_kernel(const CombineBwdParams
         if ((live >> j) & 1u) v[j] = moe::ld_stream_u4(p.yp + (int64_t)r[j] * H8 + c);
       Chunk<X> in;
       in.load(static_cast<const X *>(p.gy) + t * p.H + 8 * c);
-      float g[8];
+      Pair g[4];
       in.get(g);
 #pragma unroll
       for (int j = 0; j < KMAX; ++j)
         if ((live >> j) & 1u) {
-          float f[8], o[8];
-          unpack8(v[j], f);
+          Pair f[4], o[4];
+          unpack(v[j], f);
+          sums[j] += dot(g, f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            dot[j] = fmaf(g[i], f[i], dot[j]);
-            o[i] = w[j] * g[i];
-          }
-          p.gyp[(int64_t)r[j] * H8 + c] = pack8(o);
+          for (int i = 0; i < 4; ++i) o[i] = mul(both(w[j]), g[i]);
+          p.gyp[(int64_t)r[j] * H8 + c] = pack(o);
         }
     }
-    put_sums(dot, buf[par], warp, lane);
+    put_sums(sums, buf[par], warp, lane);
     __syncthreads();
     for (int j = warp; j < p.k; j += nw) {
       const float d = total(buf[par], j, nw, lane);
@@ -504,7 +545,7 @@ __global__ void __launch_bounds__(128) combine_bwd_kernel(const CombineBwdParams
 // A norm weight's gradient over a CTA's tokens: the teams' sums, added in order,
 // to the CTA's partial row.  Uses the CTA's shared memory from its start.
 template <int U>
-__device__ __forceinline__ void put_partial(const float (&pw)[U][8], float *partial, int H, int teams,
+__device__ __forceinline__ void put_partial(const Pair (&pw)[U][4], float *partial, int H, int teams,
                                             float *smem, const Team &tm) {
   __syncthreads();  // (all copies to shared memory have been waited for)
   const int H8 = H / 8;
@@ -524,14 +565,14 @@ __device__ __forceinline__ void put_partial(const float (&pw)[U][8], float *part
   for (int u = 0; u < U; ++u) {
     const int c = tm.tid + u * tm.threads;
     if (c >= H8) continue;
-    float a[8], b[8];
+    Pair a[4], b[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = pw[u][i];
+    for (int i = 0; i < 4; ++i) a[i] = pw[u][i];
     for (int m = 1; m < teams; ++m) {
       o.load(smem + (m - 1) * H + 8 * c);
       o.get(b);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] += b[i];
+      for (int i = 0; i < 4; ++i) a[i] = plus(a[i], b[i]);
     }
     o.set(a);
     o.store(partial + (int64_t)blockIdx.x * H + 8 * c);
@@ -567,19 +608,12 @@ __global__ void __launch_bounds__(kRowThreads)
   };
   auto fetch = [&](int64_t t, const Meta &m, int u) {
     if (t < p.T) {
-      const int c = tm.tid + u * tm.threads;
+      const int c = tm.tid + u * tm.threads, cl = min(c, H8 - 1);
       const bool in = c < H8;
       const uint32_t d = dst + (u % R) * slot;
-      for (int j = 0; j < p.k; ++j) {
-        const int32_t r = __shfl_sync(0xffffffffu, m.row, j);
-        if (in && r >= 0) copy_async(d + j * step, p.yp + (int64_t)r * H8 + c);
-      }
-      if (in) {
-        const X *src = static_cast<const X *>(p.gy) + t * p.H + 8 * c;
-#pragma unroll
-        for (int i = 0; i < Chunk<X>::N; ++i) copy_async(d + at_gy + i * step, src + 4 * i);
-        if (p.shared) copy_async(d + at_shared, p.shared + t * H8 + c);
-      }
+      copy_rows(d, step, p.yp, m, p.k, H8, cl, in);
+      copy_piece<X>(d + at_gy, step, p.gy, t * p.H + 8 * (int64_t)cl, in);
+      if (p.shared) copy_async(d + at_shared, p.shared + t * H8 + cl, in);
     }
     copy_commit();
   };
@@ -588,13 +622,16 @@ __global__ void __launch_bounds__(kRowThreads)
   settle(now, p.rows, first, p.k, tm);
 #pragma unroll
   for (int u = 0; u < R; ++u) fetch(first, now, u);
-  float pw[U][8] = {};
+  Pair pw[U][4];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pw[u][i] = 0;
   int par = 0;
   for (int64_t t = first; t < p.T; t += stride, par ^= 1) {
     settle(next, p.rows, t + stride, p.k, tm);
     const Meta after = meta(t + 2 * stride);
-    const uint32_t live = __ballot_sync(0xffffffffu, now.row >= 0);
-    float acc[U][8] = {};
+    Pair acc[U][4];
     Chunk<X> gin[U];
     float d[kSums], s[2] = {0.0f, 0.0f};  // e . Y_j, then c . Y_j
 #pragma unroll
@@ -602,43 +639,33 @@ __global__ void __launch_bounds__(kRowThreads)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       copy_wait<R - 1>();
-      const int c = tm.tid + u * tm.threads;
-      const bool in = c < H8;
       const uint8_t *sp = mine + (u % R) * slot;
-      float e[8] = {}, f[8];
-      if (in) {
-        float wt[8];
-        load_weight(p.weight, c, wt);
-        gin[u].take(sp + at_gy, step);
-        gin[u].get(e);
+      Pair e[4], f[4];
+      load_weight(p.weight, min(tm.tid + u * tm.threads, H8 - 1), f);
+      gin[u].take(sp + at_gy, step);
+      gin[u].get(e);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] *= wt[i];
-        if (p.shared) unpack8(*reinterpret_cast<const uint4 *>(sp + at_shared), acc[u]);
-      }
-#pragma unroll
-      for (int j = 0; j < KMAX; ++j) {
-        const float w = __shfl_sync(0xffffffffu, now.w, j);
-        if (in && (live >> j & 1u)) {
-          unpack8(*reinterpret_cast<const uint4 *>(sp + j * step), f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            acc[u][i] = fmaf(w, f[i], acc[u][i]);
-            d[j] = fmaf(e[i], f[i], d[j]);
-          }
-        }
-      }
+      for (int i = 0; i < 4; ++i) e[i] = mul(e[i], f[i]);
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (p.shared) v = *reinterpret_cast<const uint4 *>(sp + at_shared);
+      unpack(v, acc[u]);
 #pragma unroll
       for (int j = 0; j < KMAX; ++j)
-        if (in && (live >> j & 1u)) {
-          unpack8(*reinterpret_cast<const uint4 *>(sp + j * step), f);
+        if (j < p.k) {
+          const Pair w = both(__shfl_sync(0xffffffffu, now.w, j));
+          unpack(*reinterpret_cast<const uint4 *>(sp + j * step), f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) d[KMAX + j] = fmaf(acc[u][i], f[i], d[KMAX + j]);
+          for (int i = 0; i < 4; ++i) acc[u][i] = fma(w, f[i], acc[u][i]);
+          d[j] += dot(e, f);
         }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        s[0] = fmaf(acc[u][i], acc[u][i], s[0]);
-        s[1] = fmaf(e[i], acc[u][i], s[1]);
-      }
+      for (int j = 0; j < KMAX; ++j)
+        if (j < p.k) {
+          unpack(*reinterpret_cast<const uint4 *>(sp + j * step), f);
+          d[KMAX + j] += dot(acc[u], f);
+        }
+      s[0] += dot(acc[u], acc[u]);
+      s[1] += dot(e, acc[u]);
       if (u + R < U)
         fetch(t, now, u + R);
       else
@@ -655,6 +682,7 @@ __global__ void __launch_bounds__(kRowThreads)
       float eps = p.eps;
       if (!(s1 <= FLT_MAX)) {
         // squares beyond fp32's range: the same sums with c and Y_j times 2^-70
+        const Pair shrink = both(kShrink);
         pre = kShrink;
         eps = 0.0f;
         s[0] = s[1] = 0.0f;
@@ -663,29 +691,25 @@ __global__ void __launch_bounds__(kRowThreads)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int c = tm.tid + u * tm.threads;
-          const bool in = c < H8;
-          float e[8] = {}, wt[8], f[8];
-          if (in) {
-            load_weight(p.weight, c, wt);
-            gin[u].get(e);
+          Pair e[4], f[4];
+          load_weight(p.weight, min(c, H8 - 1), f);
+          gin[u].get(e);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              e[i] *= wt[i];
-              acc[u][i] *= kShrink;
-              s[0] = fmaf(acc[u][i], acc[u][i], s[0]);
-              s[1] = fmaf(e[i], acc[u][i], s[1]);
-            }
+          for (int i = 0; i < 4; ++i) {
+            e[i] = mul(e[i], f[i]);
+            acc[u][i] = mul(acc[u][i], shrink);
           }
+          s[0] += dot(acc[u], acc[u]);
+          s[1] += dot(e, acc[u]);
 #pragma unroll
           for (int j = 0; j < KMAX; ++j) {
             const int32_t r = __shfl_sync(0xffffffffu, now.row, j);
-            if (in && (live >> j & 1u)) {
-              unpack8(moe::ld_stream_u4(p.yp + (int64_t)r * H8 + c), f);
+            if (c < H8 && r >= 0) {
+              unpack(moe::ld_stream_u4(p.yp + (int64_t)r * H8 + c), f);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                d[j] = fmaf(e[i], f[i] * kShrink, d[j]);
-                d[KMAX + j] = fmaf(acc[u][i], f[i] * kShrink, d[KMAX + j]);
-              }
+              for (int i = 0; i < 4; ++i) f[i] = mul(f[i], shrink);
+              d[j] += dot(e, f);
+              d[KMAX + j] += dot(acc[u], f);
             }
           }
         }
@@ -701,37 +725,33 @@ __global__ void __launch_bounds__(kRowThreads)
     }
     for (int j = tm.warp; j < p.k; j += tm.nw) {
       const float ey = total(b, j, tm.nw, tm.lane), cy = total(b, KMAX + j, tm.nw, tm.lane);
-      if (tm.lane == 0) p.gw[t * p.k + j] = g * rc * (ey - m * cy);
+      if (tm.lane == j) p.gw[t * p.k + j] = now.row < 0 ? 0.0f : g * rc * (ey - m * cy);
     }
     if (p.ggate && tm.tid == 0) p.ggate[t] = s2 * rc;
-    const float a = g * rc * pre;
+    const Pair a = both(g * rc * pre), minus_m = both(-m);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c = tm.tid + u * tm.threads;
       const bool in = c < H8;
-      float gy[8] = {}, o[8];
-      if (in) {
-        float wt[8];
-        load_weight(p.weight, c, wt);
-        gin[u].get(gy);
-        if (p.partial) {
+      Pair gy[4], o[4];
+      load_weight(p.weight, min(c, H8 - 1), o);
+      gin[u].get(gy);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) pw[u][i] = fmaf(g * gy[i], acc[u][i] * rc, pw[u][i]);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) gy[i] = a * fmaf(-m, acc[u][i], gy[i] * wt[i]);
-        if (p.gshared) p.gshared[t * H8 + c] = pack8(gy);
+      for (int i = 0; i < 4; ++i) {
+        if (p.partial)
+          pw[u][i] = fma(mul(both(g), gy[i]), mul(acc[u][i], both(rc)), pw[u][i]);
+        gy[i] = mul(a, fma(minus_m, acc[u][i], mul(gy[i], o[i])));
       }
+      if (in && p.gshared) p.gshared[t * H8 + c] = pack(gy);
 #pragma unroll
-      for (int j = 0; j < KMAX; ++j) {
-        const float w = __shfl_sync(0xffffffffu, now.w, j);
-        const int32_t r = __shfl_sync(0xffffffffu, now.row, j);
-        if (in && (live >> j & 1u)) {
+      for (int j = 0; j < KMAX; ++j)
+        if (j < p.k) {
+          const Pair w = both(__shfl_sync(0xffffffffu, now.w, j));
+          const int32_t r = __shfl_sync(0xffffffffu, now.row, j);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = w * gy[i];
-          p.gyp[(int64_t)r * H8 + c] = pack8(o);
+          for (int i = 0; i < 4; ++i) o[i] = mul(w, gy[i]);
+          if (in && r >= 0) p.gyp[(int64_t)r * H8 + c] = pack(o);
         }
-      }
     }
     now = next;
     next = after;
@@ -780,23 +800,15 @@ __global__ void __launch_bounds__(kRowThreads)
   };
   auto fetch = [&](int64_t t, const Meta &m, int u) {
     if (t < p.T) {
-      const int c = tm.tid + u * tm.threads;
+      const int c = tm.tid + u * tm.threads, cl = min(c, H8 - 1);
       const bool in = c < H8;
       const uint32_t d = dst + (u % R) * slot;
-      for (int j = 0; j < p.k; ++j) {
-        const int32_t r = __shfl_sync(0xffffffffu, m.row, j);
-        if (in && r >= 0) copy_async(d + j * step, p.grad + (int64_t)r * H8 + c);
-      }
-      if (in) {
-        const int64_t at = t * p.H + 8 * c;
-#pragma unroll
-        for (int i = 0; i < Chunk<X>::N; ++i) {
-          copy_async(d + at_x + i * step, static_cast<const X *>(p.x) + at + 4 * i);
-          // (gx may be rgrad itself: a token's row is read before it is written)
-          if (p.rgrad) copy_async(d + at_res + i * step, static_cast<const X *>(p.rgrad) + at + 4 * i);
-        }
-        if (p.add) copy_async(d + at_add, p.add + t * H8 + c);
-      }
+      const int64_t at = t * p.H + 8 * (int64_t)cl;
+      copy_rows(d, step, p.grad, m, p.k, H8, cl, in);
+      copy_piece<X>(d + at_x, step, p.x, at, in);
+      // (gx may be rgrad itself: a token's row is read before it is written)
+      if (p.rgrad) copy_piece<X>(d + at_res, step, p.rgrad, at, in);
+      if (p.add) copy_async(d + at_add, p.add + t * H8 + cl, in);
     }
     copy_commit();
   };
@@ -805,45 +817,42 @@ __global__ void __launch_bounds__(kRowThreads)
   settle(now, p.rows, first, p.k, tm);
 #pragma unroll
   for (int u = 0; u < R; ++u) fetch(first, now, u);
-  float pw[U][8] = {};
+  Pair pw[U][4];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pw[u][i] = 0;
   int par = 0;
   for (int64_t t = first; t < p.T; t += stride, par ^= 1) {
     settle(next, p.rows, t + stride, p.k, tm);
     const Meta after = meta(t + 2 * stride);
-    float acc[U][8] = {}, x[U][8] = {}, s[2] = {0.0f, 0.0f};
+    Pair acc[U][4], x[U][4];
+    float s[2] = {0.0f, 0.0f};
     Chunk<X> res[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       copy_wait<R - 1>();
-      const int c = tm.tid + u * tm.threads;
-      const bool in = c < H8;
       const uint8_t *sp = mine + (u % R) * slot;
-      if (in) {
-        if (p.add) unpack8(*reinterpret_cast<const uint4 *>(sp + at_add), acc[u]);
-        Chunk<X> v;
-        v.take(sp + at_x, step);
-        v.get(x[u]);
-        if (p.rgrad) res[u].take(sp + at_res, step);
-      }
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (p.add) v = *reinterpret_cast<const uint4 *>(sp + at_add);
+      unpack(v, acc[u]);
+      Chunk<X> in;
+      in.take(sp + at_x, step);
+      in.get(x[u]);
+      if (p.rgrad) res[u].take(sp + at_res, step);
 #pragma unroll 4
       for (int j = 0; j < p.k; ++j) {
-        const int32_t r = __shfl_sync(0xffffffffu, now.row, j);
-        if (in && r >= 0) {
-          float f[8];
-          unpack8(*reinterpret_cast<const uint4 *>(sp + j * step), f);
+        Pair f[4];
+        unpack(*reinterpret_cast<const uint4 *>(sp + j * step), f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) acc[u][i] += f[i];
-        }
+        for (int i = 0; i < 4; ++i) acc[u][i] = plus(acc[u][i], f[i]);
       }
-      if (in) {
-        float wt[8];
-        load_weight(p.weight, c, wt);
+      Pair e[4];
+      load_weight(p.weight, min(tm.tid + u * tm.threads, H8 - 1), e);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          s[0] = fmaf(x[u][i], x[u][i], s[0]);
-          s[1] = fmaf(acc[u][i] * wt[i], x[u][i], s[1]);
-        }
-      }
+      for (int i = 0; i < 4; ++i) e[i] = mul(acc[u][i], e[i]);
+      s[0] += dot(x[u], x[u]);
+      s[1] += dot(e, x[u]);
       if (u + R < U)
         fetch(t, now, u + R);
       else
@@ -860,16 +869,15 @@ __global__ void __launch_bounds__(kRowThreads)
       s[0] = s[1] = 0.0f;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int c = tm.tid + u * tm.threads;
-        if (c >= H8) continue;
-        float wt[8];
-        load_weight(p.weight, c, wt);
+        Pair e[4];
+        load_weight(p.weight, min(tm.tid + u * tm.threads, H8 - 1), e);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[u][i] *= kShrink;
-          s[0] = fmaf(x[u][i], x[u][i], s[0]);
-          s[1] = fmaf(acc[u][i] * wt[i], x[u][i], s[1]);
+        for (int i = 0; i < 4; ++i) {
+          x[u][i] = mul(x[u][i], both(kShrink));
+          e[i] = mul(acc[u][i], e[i]);
         }
+        s[0] += dot(x[u], x[u]);
+        s[1] += dot(e, x[u]);
       }
       tm.sync();
       put_sums(s, b, tm.warp, tm.lane);
@@ -877,24 +885,28 @@ __global__ void __launch_bounds__(kRowThreads)
       s1 = total(b, 0, tm.nw, tm.lane);
       s2 = total(b, 1, tm.nw, tm.lane);
     }
-    const float rc = inv_rms(s1, p.H, eps), m = rc * rc * (s2 / (float)p.H), a = rc * pre;
+    const float rc = inv_rms(s1, p.H, eps);
+    const Pair a = both(rc * pre), minus_m = both(-(rc * rc * (s2 / (float)p.H)));
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c = tm.tid + u * tm.threads;
-      if (c >= H8) continue;
-      float wt[8], o[8] = {};
-      load_weight(p.weight, c, wt);
-      if (p.rgrad) res[u].get(o);
-      if (p.partial) {
+      Pair wt[4], o[4];
+      load_weight(p.weight, min(c, H8 - 1), wt);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) pw[u][i] = fmaf(acc[u][i], x[u][i] * rc, pw[u][i]);
+      for (int i = 0; i < 4; ++i) {
+        if (p.partial) pw[u][i] = fma(acc[u][i], mul(x[u][i], both(rc)), pw[u][i]);
+        wt[i] = mul(a, fma(minus_m, x[u][i], mul(acc[u][i], wt[i])));
       }
+      if (p.rgrad) {
+        res[u].get(o);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        o[i] = fmaf(p.scale, o[i], a * fmaf(-m, x[u][i], acc[u][i] * wt[i]));
-      Chunk<X> out;
-      out.set(o);
-      out.store(static_cast<X *>(p.gx) + t * p.H + 8 * c);
+        for (int i = 0; i < 4; ++i) wt[i] = fma(both(p.scale), o[i], wt[i]);
+      }
+      if (c < H8) {
+        Chunk<X> out;
+        out.set(wt);
+        out.store(static_cast<X *>(p.gx) + t * p.H + 8 * c);
+      }
     }
     now = next;
     next = after;
@@ -919,14 +931,16 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
       for (int j = 0; j < KMAX; ++j)
         if ((live >> j) & 1u) v[j] = moe::ld_stream_u4(grad + (int64_t)r[j] * H8 + c);
-      float acc[8] = {}, f[8];
-      if (add) unpack8(moe::ld_stream_u4(add + t * H8 + c), acc);
+      Pair acc[4], f[4];
+      uint4 first = make_uint4(0, 0, 0, 0);
+      if (add) first = moe::ld_stream_u4(add + t * H8 + c);
+      unpack(first, acc);
 #pragma unroll
       for (int j = 0; j < KMAX; ++j)
         if ((live >> j) & 1u) {
-          unpack8(v[j], f);
+          unpack(v[j], f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) acc[i] += f[i];
+          for (int i = 0; i < 4; ++i) acc[i] = plus(acc[i], f[i]);
         }
       Chunk<X> out;
       out.set(acc);
@@ -1125,7 +1139,8 @@ template <int U, typename X>
 moe_status run_norm(const void *x, int64_t T, int32_t H, const float *weight, float eps, uint16_t *out,
                     cudaStream_t st) {
   const int n = row_threads(H);
-  return launch_rows<norm_kernel<U, 2, X>>(T, n, 1024, (size_t)n * 32 * Chunk<X>::N, st,
+  constexpr int R = 2 * U;
+  return launch_rows<norm_kernel<U, R, X>>(T, n, 1024, (size_t)n * 16 * R * Chunk<X>::N, st,
                                            static_cast<const X *>(x), T, (int)H, weight, eps,
                                            reinterpret_cast<__nv_bfloat16 *>(out));
 }
@@ -1189,7 +1204,7 @@ extern "C" moe_status moe_norm_backward(const uint16_t *grad, int64_t n_rows,
       odd(residual_grad) || odd(grad_x))
     return MOE_ERR_INVALID_ARG;
   NormBwdParams p{};
-  p.grad = reinterpret_cast<const uint4 *>(grad);
+  p.grad = static_cast<const uint4 *>(n_rows > 0 ? grad : x);
   p.rows = Rows{dest_row, n_rows, moe_host::status_ptr(ws)};
   p.add = reinterpret_cast<const uint4 *>(add);
   p.x = x;
@@ -1246,7 +1261,8 @@ extern "C" moe_status moe_combine_norm(const uint16_t *y_perm, int64_t n_rows,
       odd(shared) || odd(residual) || odd(weight) || odd(y) || odd(next_weight) || odd(next_out))
     return MOE_ERR_INVALID_ARG;
   CombineNormParams p{};
-  p.yp = reinterpret_cast<const uint4 *>(y_perm);
+  // (without rows nothing is read there, but addresses are formed)
+  p.yp = static_cast<const uint4 *>(n_rows > 0 ? y_perm : residual);
   p.rows = Rows{dest_row, n_rows, moe_host::status_ptr(ws)};
   p.topk_w = topk_w;
   p.T = T;
@@ -1292,7 +1308,7 @@ extern "C" moe_status moe_combine_norm_backward(
     return MOE_ERR_INVALID_ARG;
   CombineBwdParams p{};
   p.gy = grad_y;
-  p.yp = reinterpret_cast<const uint4 *>(y_perm);
+  p.yp = static_cast<const uint4 *>(n_rows > 0 ? y_perm : grad_y);
   p.rows = Rows{dest_row, n_rows, moe_host::status_ptr(ws)};
   p.topk_w = topk_w;
   p.T = T;
