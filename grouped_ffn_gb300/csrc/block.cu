@@ -40,6 +40,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&p);
 }
 
+// 16 bytes to shared memory, or zeros where there are none to copy.
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool some) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(some ? 16 : 0)
+               : "memory");
+}
+
 // Two fp32 numbers for the instructions that take two at a time.
 typedef unsigned long long Pair;
 __device__ __forceinline__ Pair pair(float a, float b) {
@@ -89,33 +96,52 @@ __device__ __forceinline__ uint4 pack(const Pair (&f)[4]) {
   return make_uint4(pack_pair(f[0]), pack_pair(f[1]), pack_pair(f[2]), pack_pair(f[3]));
 }
 
-// Eight elements of a row held as bf16 (one 16-byte access) or fp32 (two).
-// N places of shared memory lie `step` bytes apart.
+// Eight elements of a row held as bf16 (16 bytes) or fp32 (32).  Two accesses of 16
+// bytes a thread each touch every sector of a warp's fp32 piece, which then crosses
+// from L2 twice; so there a warp's kilobyte is copied and stored in whole sectors.
+//  copy   a warp's pieces to its place in shared memory (N times 512 bytes at s),
+//         zeros from the row's end on;
+//  take   the thread's piece from there;
+//  store  to a row: the whole warp calls it.
 template <typename X>
 struct Chunk;
 template <>
 struct Chunk<__nv_bfloat16> {
   static constexpr int N = 1;
   uint4 a;
-  __device__ __forceinline__ void take(const uint8_t *s, int) {
-    a = *reinterpret_cast<const uint4 *>(s);
+  __device__ __forceinline__ static void copy(uint32_t s, const __nv_bfloat16 *row, int c, int H8,
+                                              int lane) {
+    copy_async(s + lane * 16, row + 8 * (int64_t)min(c, H8 - 1), c < H8);
+  }
+  __device__ __forceinline__ void take(const uint8_t *s, int lane) {
+    a = *reinterpret_cast<const uint4 *>(s + lane * 16);
   }
   __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
     a = *reinterpret_cast<const uint4 *>(p);
   }
   __device__ __forceinline__ void get(Pair (&f)[4]) const { unpack(a, f); }
   __device__ __forceinline__ void set(const Pair (&f)[4]) { a = pack(f); }
-  __device__ __forceinline__ void store(__nv_bfloat16 *p) const {
-    *reinterpret_cast<uint4 *>(p) = a;
+  __device__ __forceinline__ void store(__nv_bfloat16 *row, int c, int H8, int) const {
+    if (c < H8) reinterpret_cast<uint4 *>(row)[c] = a;
   }
 };
 template <>
 struct Chunk<float> {
   static constexpr int N = 2;
   float4 a, b;
-  __device__ __forceinline__ void take(const uint8_t *s, int step) {
-    a = *reinterpret_cast<const float4 *>(s);
-    b = *reinterpret_cast<const float4 *>(s + step);
+  // 16-byte place of a warp's i-th four elements: lanes read their two without
+  // bank conflicts
+  __device__ __forceinline__ static int place(int i) { return (i ^ (i >> 3 & 1)) * 16; }
+  __device__ __forceinline__ static void copy(uint32_t s, const float *row, int c, int H8, int lane) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = h * 32 + lane, at = 8 * (c - lane) + 4 * i;
+      copy_async(s + place(i), row + min(at, 8 * H8 - 4), at < 8 * H8);
+    }
+  }
+  __device__ __forceinline__ void take(const uint8_t *s, int lane) {
+    a = *reinterpret_cast<const float4 *>(s + place(2 * lane));
+    b = *reinterpret_cast<const float4 *>(s + place(2 * lane + 1));
   }
   __device__ __forceinline__ void load(const float *p) {
     a = reinterpret_cast<const float4 *>(p)[0];
@@ -130,9 +156,22 @@ struct Chunk<float> {
     split(f[2], b.x, b.y);
     split(f[3], b.z, b.w);
   }
-  __device__ __forceinline__ void store(float *p) const {
+  __device__ __forceinline__ void put(float *p) const {
     reinterpret_cast<float4 *>(p)[0] = a;
     reinterpret_cast<float4 *>(p)[1] = b;
+  }
+  // An even lane's second half goes out with the odd one's number in the first
+  // instruction, the odd lane's first half with the even one's in the second.
+  __device__ __forceinline__ void store(float *row, int c, int H8, int lane) const {
+    const bool odd = lane & 1;
+    const float4 v = odd ? a : b;
+    const float4 w = make_float4(
+        __shfl_xor_sync(0xffffffffu, v.x, 1), __shfl_xor_sync(0xffffffffu, v.y, 1),
+        __shfl_xor_sync(0xffffffffu, v.z, 1), __shfl_xor_sync(0xffffffffu, v.w, 1));
+    const int even = c - odd;  // the pair's first piece
+    float4 *p = reinterpret_cast<float4 *>(row) + 2 * even + odd;
+    if (even < H8) p[0] = odd ? w : a;
+    if (even + 1 < H8) p[2] = odd ? b : w;
   }
 };
 
@@ -202,20 +241,6 @@ struct Team {
   }
 };
 
-// 16 bytes, or zeros where there are none to copy.
-__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool some) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(some ? 16 : 0)
-               : "memory");
-}
-// A piece of a row of X, `at` elements into p.
-template <typename X>
-__device__ __forceinline__ void copy_piece(uint32_t dst, int step, const void *p, int64_t at,
-                                           bool some) {
-#pragma unroll
-  for (int i = 0; i < Chunk<X>::N; ++i)
-    copy_async(dst + i * step, static_cast<const X *>(p) + at + 4 * i, some);
-}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() {
@@ -325,15 +350,13 @@ __global__ void __launch_bounds__(kRowThreads)
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float buf[2][32];
   const Team tm((int)blockDim.x);
-  const int H8 = H / 8, step = tm.threads * 16, slot = step * Chunk<X>::N;
-  uint8_t *mine = smem + tm.tid * 16;
+  const int H8 = H / 8, slot = tm.threads * 16 * Chunk<X>::N;
+  uint8_t *mine = smem + tm.warp * 512 * Chunk<X>::N;  // the warp's places
   const uint32_t dst = smem_u32(mine);
   moe::pdl_wait();
   moe::pdl_trigger();
   auto fetch = [&](int64_t t, int u, int at) {
-    const int c = tm.tid + u * tm.threads;
-    if (t < T)
-      copy_piece<X>(dst + at * slot, step, x, t * H + 8 * (int64_t)min(c, H8 - 1), c < H8);
+    if (t < T) Chunk<X>::copy(dst + at * slot, x + t * H, tm.tid + u * tm.threads, H8, tm.lane);
     copy_commit();
   };
   static_assert(R % U == 0, "whole tokens");
@@ -345,9 +368,11 @@ __global__ void __launch_bounds__(kRowThreads)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       copy_wait<R - 1>();
+      __syncwarp();  // the warp's copies are there
       Chunk<X> in;
-      in.take(mine + (at + u) * slot, step);
+      in.take(mine + (at + u) * slot, tm.lane);
       in.get(v[u]);
+      __syncwarp();  // and used
       fetch(t + R / U * (int64_t)gridDim.x, u, at + u);
     }
     at = at + U == R ? 0 : at + U;
@@ -392,6 +417,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_norm_kernel(const Combine
   const int slot = at_shared + (p.shared ? step : 0);
   uint8_t *mine = smem + tm.tid * 16;
   const uint32_t dst = smem_u32(mine);
+  const int warp_res = at_res + (tm.warp * Chunk<X>::N * 32 - tm.tid) * 16;  // from `mine`
   moe::pdl_wait();
   moe::pdl_trigger();
   auto meta = [&](int64_t t) {
@@ -404,7 +430,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_norm_kernel(const Combine
       const uint32_t d = dst + (u % R) * slot;
       copy_rows(d, step, p.yp, m, p.k, H8, cl, in);
       // (y may be the residual itself: a token's row is read before it is written)
-      copy_piece<X>(d + at_res, step, p.residual, t * p.H + 8 * (int64_t)cl, in);
+      Chunk<X>::copy(d + warp_res, static_cast<const X *>(p.residual) + t * p.H, c, H8, tm.lane);
       if (p.shared) copy_async(d + at_shared, p.shared + t * H8 + cl, in);
     }
     copy_commit();
@@ -423,8 +449,9 @@ __global__ void __launch_bounds__(kRowThreads) combine_norm_kernel(const Combine
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       copy_wait<R - 1>();
+      __syncwarp();  // the warp's copies are there
       const uint8_t *s = mine + (u % R) * slot;
-      res[u].take(s + at_res, step);
+      res[u].take(s + warp_res, tm.lane);
       uint4 first = make_uint4(0, 0, 0, 0);
       if (p.shared) first = *reinterpret_cast<const uint4 *>(s + at_shared);
       unpack(first, acc[u]);
@@ -436,6 +463,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_norm_kernel(const Combine
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[u][i] = fma(w, f[i], acc[u][i]);
       }
+      __syncwarp();  // and used
       if (u + R < U)
         fetch(t, now, u + R);
       else
@@ -455,7 +483,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_norm_kernel(const Combine
         acc[u][i] = fma(both(p.scale), x[i], mul(both(now.g), f));
       }
       res[u].set(acc[u]);
-      if (c < H8) res[u].store(static_cast<X *>(p.y) + t * p.H + 8 * c);
+      res[u].store(static_cast<X *>(p.y) + t * p.H, c, H8, tm.lane);
       res[u].get(acc[u]);  // as it is held
     }
     if (p.next) {
@@ -556,7 +584,7 @@ __device__ __forceinline__ void put_partial(const Pair (&pw)[U][4], float *parti
       const int c = tm.tid + u * tm.threads;
       if (c >= H8) continue;
       o.set(pw[u]);
-      o.store(smem + (tm.index - 1) * H + 8 * c);
+      o.put(smem + (tm.index - 1) * H + 8 * c);
     }
   }
   __syncthreads();
@@ -575,7 +603,7 @@ __device__ __forceinline__ void put_partial(const Pair (&pw)[U][4], float *parti
       for (int i = 0; i < 4; ++i) a[i] = plus(a[i], b[i]);
     }
     o.set(a);
-    o.store(partial + (int64_t)blockIdx.x * H + 8 * c);
+    o.put(partial + (int64_t)blockIdx.x * H + 8 * c);
   }
 }
 
@@ -601,6 +629,7 @@ __global__ void __launch_bounds__(kRowThreads)
   uint8_t *rings = smem + teams * 2 * kBuf * 4;
   uint8_t *mine = rings + tm.index * R * slot + tm.tid * 16;
   const uint32_t dst = smem_u32(mine);
+  const int warp_gy = at_gy + (tm.warp * Chunk<X>::N * 32 - tm.tid) * 16;  // from `mine`
   moe::pdl_wait();
   moe::pdl_trigger();
   auto meta = [&](int64_t t) {
@@ -612,7 +641,7 @@ __global__ void __launch_bounds__(kRowThreads)
       const bool in = c < H8;
       const uint32_t d = dst + (u % R) * slot;
       copy_rows(d, step, p.yp, m, p.k, H8, cl, in);
-      copy_piece<X>(d + at_gy, step, p.gy, t * p.H + 8 * (int64_t)cl, in);
+      Chunk<X>::copy(d + warp_gy, static_cast<const X *>(p.gy) + t * p.H, c, H8, tm.lane);
       if (p.shared) copy_async(d + at_shared, p.shared + t * H8 + cl, in);
     }
     copy_commit();
@@ -639,10 +668,11 @@ __global__ void __launch_bounds__(kRowThreads)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       copy_wait<R - 1>();
+      __syncwarp();  // the warp's copies are there
       const uint8_t *sp = mine + (u % R) * slot;
       Pair e[4], f[4];
       load_weight(p.weight, min(tm.tid + u * tm.threads, H8 - 1), f);
-      gin[u].take(sp + at_gy, step);
+      gin[u].take(sp + warp_gy, tm.lane);
       gin[u].get(e);
 #pragma unroll
       for (int i = 0; i < 4; ++i) e[i] = mul(e[i], f[i]);
@@ -666,6 +696,7 @@ __global__ void __launch_bounds__(kRowThreads)
         }
       s[0] += dot(acc[u], acc[u]);
       s[1] += dot(e, acc[u]);
+      __syncwarp();  // and used
       if (u + R < U)
         fetch(t, now, u + R);
       else
@@ -791,6 +822,7 @@ __global__ void __launch_bounds__(kRowThreads)
   uint8_t *rings = smem + teams * 2 * kBuf * 4;
   uint8_t *mine = rings + tm.index * R * slot + tm.tid * 16;
   const uint32_t dst = smem_u32(mine);
+  const int warp_at = (tm.warp * Chunk<X>::N * 32 - tm.tid) * 16;  // the warp's places, from `mine`
   moe::pdl_wait();
   moe::pdl_trigger();
   auto meta = [&](int64_t t) {
@@ -803,11 +835,11 @@ __global__ void __launch_bounds__(kRowThreads)
       const int c = tm.tid + u * tm.threads, cl = min(c, H8 - 1);
       const bool in = c < H8;
       const uint32_t d = dst + (u % R) * slot;
-      const int64_t at = t * p.H + 8 * (int64_t)cl;
       copy_rows(d, step, p.grad, m, p.k, H8, cl, in);
-      copy_piece<X>(d + at_x, step, p.x, at, in);
+      Chunk<X>::copy(d + at_x + warp_at, static_cast<const X *>(p.x) + t * p.H, c, H8, tm.lane);
       // (gx may be rgrad itself: a token's row is read before it is written)
-      if (p.rgrad) copy_piece<X>(d + at_res, step, p.rgrad, at, in);
+      if (p.rgrad)
+        Chunk<X>::copy(d + at_res + warp_at, static_cast<const X *>(p.rgrad) + t * p.H, c, H8, tm.lane);
       if (p.add) copy_async(d + at_add, p.add + t * H8 + cl, in);
     }
     copy_commit();
@@ -832,14 +864,15 @@ __global__ void __launch_bounds__(kRowThreads)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       copy_wait<R - 1>();
+      __syncwarp();  // the warp's copies are there
       const uint8_t *sp = mine + (u % R) * slot;
       uint4 v = make_uint4(0, 0, 0, 0);
       if (p.add) v = *reinterpret_cast<const uint4 *>(sp + at_add);
       unpack(v, acc[u]);
       Chunk<X> in;
-      in.take(sp + at_x, step);
+      in.take(sp + at_x + warp_at, tm.lane);
       in.get(x[u]);
-      if (p.rgrad) res[u].take(sp + at_res, step);
+      if (p.rgrad) res[u].take(sp + at_res + warp_at, tm.lane);
 #pragma unroll 4
       for (int j = 0; j < p.k; ++j) {
         Pair f[4];
@@ -853,6 +886,7 @@ __global__ void __launch_bounds__(kRowThreads)
       for (int i = 0; i < 4; ++i) e[i] = mul(acc[u][i], e[i]);
       s[0] += dot(x[u], x[u]);
       s[1] += dot(e, x[u]);
+      __syncwarp();  // and used
       if (u + R < U)
         fetch(t, now, u + R);
       else
@@ -902,11 +936,9 @@ __global__ void __launch_bounds__(kRowThreads)
 #pragma unroll
         for (int i = 0; i < 4; ++i) wt[i] = fma(both(p.scale), o[i], wt[i]);
       }
-      if (c < H8) {
-        Chunk<X> out;
-        out.set(wt);
-        out.store(static_cast<X *>(p.gx) + t * p.H + 8 * c);
-      }
+      Chunk<X> out;
+      out.set(wt);
+      out.store(static_cast<X *>(p.gx) + t * p.H, c, H8, tm.lane);
     }
     now = next;
     next = after;
@@ -922,29 +954,31 @@ __global__ void __launch_bounds__(128)
                        int64_t T, int k, int H, X *__restrict__ gx) {
   moe::pdl_wait();
   moe::pdl_trigger();
-  const int H8 = H / 8;
+  const int H8 = H / 8, lane = threadIdx.x & 31;
   for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
     int32_t r[KMAX];
     const uint32_t live = token_rows(rows, t, k, r);
-    for (int c = threadIdx.x; c < H8; c += blockDim.x) {
+    for (int c0 = threadIdx.x - lane; c0 < H8; c0 += blockDim.x) {
+      const int c = c0 + lane;
+      const bool in = c < H8;
       uint4 v[KMAX];
 #pragma unroll
       for (int j = 0; j < KMAX; ++j)
-        if ((live >> j) & 1u) v[j] = moe::ld_stream_u4(grad + (int64_t)r[j] * H8 + c);
+        if (in && (live >> j & 1u)) v[j] = moe::ld_stream_u4(grad + (int64_t)r[j] * H8 + c);
       Pair acc[4], f[4];
       uint4 first = make_uint4(0, 0, 0, 0);
-      if (add) first = moe::ld_stream_u4(add + t * H8 + c);
+      if (in && add) first = moe::ld_stream_u4(add + t * H8 + c);
       unpack(first, acc);
 #pragma unroll
       for (int j = 0; j < KMAX; ++j)
-        if ((live >> j) & 1u) {
+        if (live >> j & 1u) {
           unpack(v[j], f);
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[i] = plus(acc[i], f[i]);
         }
       Chunk<X> out;
       out.set(acc);
-      out.store(gx + t * H + 8 * c);
+      out.store(gx + t * H, c, H8, lane);
     }
   }
 }
