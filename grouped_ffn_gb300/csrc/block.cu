@@ -222,8 +222,9 @@ __device__ __forceinline__ float total(const float *buf, int value, int nw, int 
   return x;
 }
 
-__device__ __forceinline__ float inv_rms(float sum, int H, float eps) {
-  return 1.0f / sqrtf(sum / (float)H + eps);
+// (rsqrtf is within two units of its last place)
+__device__ __forceinline__ float inv_rms(float sum, float inv_h, float eps) {
+  return rsqrtf(fmaf(sum, inv_h, eps));
 }
 
 // The threads of one token.
@@ -257,7 +258,7 @@ struct Norm {
   float pre, r;  // the row's factor, and 1 / rms of the row times it
 };
 template <int U>
-__device__ __forceinline__ Norm row_norm(Pair (&x)[U][4], int H, float eps, float *buf,
+__device__ __forceinline__ Norm row_norm(Pair (&x)[U][4], float inv_h, float eps, float *buf,
                                          const Team &tm) {
   auto squares = [&]() {
     Pair s = mul(x[0][0], x[0][0]);
@@ -282,7 +283,7 @@ __device__ __forceinline__ Norm row_norm(Pair (&x)[U][4], int H, float eps, floa
     s = squares();
     eps = 0.0f;
   }
-  n.r = inv_rms(s, H, eps);
+  n.r = inv_rms(s, inv_h, eps);
   return n;
 }
 
@@ -351,6 +352,7 @@ __global__ void __launch_bounds__(kRowThreads)
   __shared__ float buf[2][32];
   const Team tm((int)blockDim.x);
   const int H8 = H / 8, slot = tm.threads * 16 * Chunk<X>::N;
+  const float inv_h = 1.0f / (float)H;
   uint8_t *mine = smem + tm.warp * 512 * Chunk<X>::N;  // the warp's places
   const uint32_t dst = smem_u32(mine);
   moe::pdl_wait();
@@ -376,7 +378,7 @@ __global__ void __launch_bounds__(kRowThreads)
       fetch(t + R / U * (int64_t)gridDim.x, u, at + u);
     }
     at = at + U == R ? 0 : at + U;
-    const Norm n = row_norm(v, H, eps, buf[par], tm);
+    const Norm n = row_norm(v, inv_h, eps, buf[par], tm);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c = tm.tid + u * tm.threads;
@@ -413,6 +415,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_norm_kernel(const Combine
   __shared__ float buf[2][2][32];
   const Team tm((int)blockDim.x);
   const int H8 = p.H / 8, step = tm.threads * 16;
+  const float inv_h = 1.0f / (float)p.H;
   const int at_res = p.k * step, at_shared = at_res + Chunk<X>::N * step;
   const int slot = at_shared + (p.shared ? step : 0);
   uint8_t *mine = smem + tm.tid * 16;
@@ -470,7 +473,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_norm_kernel(const Combine
         fetch(t + stride, next, (u + R) % U);
     }
     float rc = 1.0f;
-    if (p.post) rc = row_norm(acc, p.H, p.eps, buf[par][0], tm).r;
+    if (p.post) rc = row_norm(acc, inv_h, p.eps, buf[par][0], tm).r;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c = tm.tid + u * tm.threads;
@@ -487,7 +490,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_norm_kernel(const Combine
       res[u].get(acc[u]);  // as it is held
     }
     if (p.next) {
-      const Norm n = row_norm(acc, p.H, p.eps, buf[par][1], tm);
+      const Norm n = row_norm(acc, inv_h, p.eps, buf[par][1], tm);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int c = tm.tid + u * tm.threads;
@@ -623,6 +626,7 @@ __global__ void __launch_bounds__(kRowThreads)
   const Team tm(team_threads);
   const int teams = blockDim.x / team_threads;
   const int H8 = p.H / 8, step = tm.threads * 16;
+  const float inv_h = 1.0f / (float)p.H;
   const int at_gy = p.k * step, at_shared = at_gy + Chunk<X>::N * step;
   const int slot = at_shared + (p.shared ? step : 0);
   float *buf = reinterpret_cast<float *>(smem) + tm.index * 2 * kBuf;
@@ -663,6 +667,9 @@ __global__ void __launch_bounds__(kRowThreads)
     Pair acc[U][4];
     Chunk<X> gin[U];
     float d[kSums], s[2] = {0.0f, 0.0f};  // e . Y_j, then c . Y_j
+    float w[KMAX];
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j) w[j] = __shfl_sync(0xffffffffu, now.w, j);
 #pragma unroll
     for (int j = 0; j < kSums; ++j) d[j] = 0.0f;
 #pragma unroll
@@ -682,10 +689,9 @@ __global__ void __launch_bounds__(kRowThreads)
 #pragma unroll
       for (int j = 0; j < KMAX; ++j)
         if (j < p.k) {
-          const Pair w = both(__shfl_sync(0xffffffffu, now.w, j));
           unpack(*reinterpret_cast<const uint4 *>(sp + j * step), f);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[u][i] = fma(w, f[i], acc[u][i]);
+          for (int i = 0; i < 4; ++i) acc[u][i] = fma(both(w[j]), f[i], acc[u][i]);
           d[j] += dot(e, f);
         }
 #pragma unroll
@@ -751,8 +757,8 @@ __global__ void __launch_bounds__(kRowThreads)
         s1 = total(b, kSums, tm.nw, tm.lane);
         s2 = total(b, kSums + 1, tm.nw, tm.lane);
       }
-      rc = inv_rms(s1, p.H, eps);
-      m = rc * rc * (s2 / (float)p.H);
+      rc = inv_rms(s1, inv_h, eps);
+      m = rc * rc * (s2 * inv_h);
     }
     for (int j = tm.warp; j < p.k; j += tm.nw) {
       const float ey = total(b, j, tm.nw, tm.lane), cy = total(b, KMAX + j, tm.nw, tm.lane);
@@ -777,10 +783,9 @@ __global__ void __launch_bounds__(kRowThreads)
 #pragma unroll
       for (int j = 0; j < KMAX; ++j)
         if (j < p.k) {
-          const Pair w = both(__shfl_sync(0xffffffffu, now.w, j));
           const int32_t r = __shfl_sync(0xffffffffu, now.row, j);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = mul(w, gy[i]);
+          for (int i = 0; i < 4; ++i) o[i] = mul(both(w[j]), gy[i]);
           if (in && r >= 0) p.gyp[(int64_t)r * H8 + c] = pack(o);
         }
     }
@@ -815,6 +820,7 @@ __global__ void __launch_bounds__(kRowThreads)
   const Team tm(team_threads);
   const int teams = blockDim.x / team_threads;
   const int H8 = p.H / 8, step = tm.threads * 16;
+  const float inv_h = 1.0f / (float)p.H;
   const int at_x = p.k * step, at_add = at_x + Chunk<X>::N * step;
   const int at_res = at_add + (p.add ? step : 0);
   const int slot = at_res + (p.rgrad ? Chunk<X>::N * step : 0);
@@ -919,8 +925,8 @@ __global__ void __launch_bounds__(kRowThreads)
       s1 = total(b, 0, tm.nw, tm.lane);
       s2 = total(b, 1, tm.nw, tm.lane);
     }
-    const float rc = inv_rms(s1, p.H, eps);
-    const Pair a = both(rc * pre), minus_m = both(-(rc * rc * (s2 / (float)p.H)));
+    const float rc = inv_rms(s1, inv_h, eps);
+    const Pair a = both(rc * pre), minus_m = both(-(rc * rc * (s2 * inv_h)));
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c = tm.tid + u * tm.threads;
