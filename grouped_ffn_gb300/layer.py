@@ -34,7 +34,10 @@ class MoELayer:
                  fp8_dispatch: bool = False, fuse_shared: bool = True,
                  ffn_schedule: Optional[moe.FfnSchedule] = None,
                  gate: Optional[moe.GateCfg] = None, gate_bias: Optional[torch.Tensor] = None,
-                 fp4: Optional[int] = None, fp4_scale_exp: tuple = (-6, -6)):
+                 fp4: Optional[int] = None, fp4_scale_exp: tuple = (-6, -6),
+                 int4: Optional[int] = None, block: Optional[moe.BlockCfg] = None,
+                 post_weight: Optional[torch.Tensor] = None,
+                 next_weight: Optional[torch.Tensor] = None):
         """replica_relax=(c_num, c_den) chooses each assignment's replica by
         locality-preferred water-filling with load bounds C = c_num/c_den
         (moe_route_replicas); None keeps the fixed replica rule.
@@ -68,7 +71,18 @@ class MoELayer:
         in [2^(e-3), 2^(e+11)]; values beyond 2688 * 2^e, 42 with the default
         -6, are held as that, without a report: choose e from the largest
         magnitude that the rows reach, or MX, whose scales have no such end).  A shared expert needs the routed experts'
-        width and runs as one more segment.  Contiguous layout only."""
+        width and runs as one more segment.  Contiguous layout only.
+        int4=32, 64 or 128 runs the experts on 4-bit integer weights with a
+        scale for so many consecutive weights (moe_grouped_product_int4), bf16
+        rows: for decode steps.  The weights are quantized to the nearest of
+        scale * (-7..7) and packed once, here; or w_gate_up and w_down are
+        Int4Weights already (pack_weights_int4, the first with SwiGLU), without a
+        shared expert.  A shared expert needs the routed experts' width and runs
+        as one more segment.  Contiguous layout only.
+        block=cfg lets forward take a residual: the combine then goes on through
+        the norm after the block (weight post_weight fp32 [H]), the gate and the
+        residual (moe_combine_norm), and writes the next block's normalised rows
+        (weight next_weight) where forward is given a place for them."""
         if (gather or masked_cap is not None) and not packed:
             raise ValueError("gather and fixed-capacity modes stream packed weights")
         if gather and (masked_cap is not None or fp8_dispatch):
@@ -84,6 +98,25 @@ class MoELayer:
                 raise ValueError("fp4: MOE_FP4_MX or MOE_FP4_NV")
             if shared_w_gate_up is not None and tuple(shared_w_gate_up.shape[1:]) != (2 * I, H):
                 raise ValueError("fp4 experts: the shared expert needs the routed experts' width")
+        packed_int4 = isinstance(w_gate_up, moe.Int4Weights) and isinstance(w_down, moe.Int4Weights)
+        self.int4 = packed_int4 or int4 is not None
+        if self.int4:
+            if fp4 is not None or gather or masked_cap is not None or fp8_dispatch or ffn_schedule is not None:
+                raise ValueError("int4 experts: contiguous layout, no FP4, gather, FP8 dispatch or schedule")
+            if packed_int4:
+                if int4 not in (None, w_gate_up.group) or shared_w_gate_up is not None:
+                    raise ValueError("packed int4 experts bring their group and no shared expert")
+                if (w_gate_up.E, w_gate_up.N, w_gate_up.K, w_gate_up.epilogue) != \
+                        (E, 2 * I, H, moe.MOE_EPI_SWIGLU) or \
+                        (w_down.E, w_down.N, w_down.K, w_down.epilogue) != (E, H, I, moe.MOE_EPI_NONE):
+                    raise ValueError("packed int4 experts: w_gate_up [E, 2I, H] with SwiGLU, w_down [E, H, I]")
+            elif int4 not in (32, 64, 128) or H % int4 or I % int4:
+                raise ValueError("int4: a group of 32, 64 or 128 that divides H and I")
+            if shared_w_gate_up is not None and tuple(shared_w_gate_up.shape[1:]) != (2 * I, H):
+                raise ValueError("int4 experts: the shared expert needs the routed experts' width")
+        if block is None and (post_weight is not None or next_weight is not None):
+            raise ValueError("post_weight and next_weight belong to a block")
+        self.block, self.post_weight, self.next_weight = block, post_weight, next_weight
         if gate is not None and gate.k != k:
             raise ValueError("gate.k must be k")
         if gate_bias is not None and gate is None:
@@ -98,14 +131,25 @@ class MoELayer:
         self.packed = packed
         self.fuse_shared = bool(
             fuse_shared and shared_w_gate_up is not None and packed and not gather
-            and fp4 is None and masked_cap is None and not fp8_dispatch
+            and fp4 is None and not self.int4 and masked_cap is None and not fp8_dispatch
             and tuple(shared_w_gate_up.shape[1:]) == (2 * I, H))
         self.fp4_shared = fp4 is not None and shared_w_gate_up is not None
+        self.int4_shared = self.int4 and shared_w_gate_up is not None
         if fp4 is not None:
             self._init_fp4(w_gate_up, w_down, shared_w_gate_up, shared_w_down, fp4_scale_exp,
                            max_tokens, device)
             w_gate_up = w_down = shared_w_gate_up = shared_w_down = None
             self.shared_I = I if self.fp4_shared else 0
+        elif self.int4:
+            if not packed_int4:
+                pack = lambda w, shared, epilogue: moe.pack_weights_int4(
+                    *self._quantize_int4(w if shared is None else torch.cat((w, shared)), int4), None, epilogue)
+                w_gate_up = pack(w_gate_up, shared_w_gate_up, moe.MOE_EPI_SWIGLU)
+                w_down = pack(w_down, shared_w_down, moe.MOE_EPI_NONE)
+            shared_w_gate_up = shared_w_down = None
+            self.shared_I = I if self.int4_shared else 0
+            se = placement.slot_expert
+            self._int4_experts = torch.cat((se, se.new_tensor([E]))) if self.int4_shared else se
         elif self.fuse_shared:
             # one packed tensor holds the routed experts and, as expert E,
             # the shared one, so that one launch serves both
@@ -136,11 +180,11 @@ class MoELayer:
         # dispatched rows: T*k in the contiguous layout (+ T for a fused
         # shared expert), S*cap in the fixed one
         rows = A if masked_cap is None else S * masked_cap
-        if self.fuse_shared or self.fp4_shared:
+        if self.fuse_shared or self.fp4_shared or self.int4_shared:
             rows = A + max_tokens
         self.slot = torch.empty(A, **i32)
         self.seg_counts = torch.empty(S, **i32)
-        # (with one more entry for a shared expert's segment of an FP4 layer)
+        # (with one more entry for a shared expert's segment of an FP4 or int4 layer)
         self._seg_offsets_all = torch.empty(S + 2, **i32)
         self.seg_offsets = self._seg_offsets_all[:S + 1]
         self.dest_row = torch.empty(A, **i32)
@@ -170,7 +214,7 @@ class MoELayer:
         self.replica_refine = replica_refine
         self.inter_node = torch.zeros(1, **i32)
         self.messages = torch.zeros(2, **i32)
-        if self.fuse_shared or fp4 is not None:
+        if self.fuse_shared or fp4 is not None or self.int4:
             pass
         elif shared_w_gate_up is not None:
             self.shared_I = shared_w_gate_up.shape[1] // 2
@@ -192,7 +236,7 @@ class MoELayer:
         # without replicas, packed weights, the contiguous layout
         small = max_tokens * k * H * 2 <= self.PREFETCH_MAX_DISPATCH
         self.prefetch_bytes = self.PREFETCH_BYTES if (
-            small and fp4 is None and packed and not gather and masked_cap is None and replica_relax is None
+            small and fp4 is None and not self.int4 and packed and not gather and masked_cap is None and replica_relax is None
             and placement.n_slots == placement.n_experts) else 0
         self._ev_route = torch.cuda.Event()
         # the layout scan takes up to 1024 assignments in one CTA, which then
@@ -205,6 +249,10 @@ class MoELayer:
         if fp4 is not None:
             # two products and the hidden rows' quantization for the FFN
             self.launches_per_step += 2 + (1 if self.fp4_shared else 0)
+        if self.int4:
+            self.launches_per_step += 1
+        # scratch of the norm weight's gradient
+        self.norm_scratch = moe.new_norm_scratch(max_tokens, H, device=dev) if block is not None else None
 
     @staticmethod
     def _quantize_experts(w, fmt):
@@ -223,6 +271,38 @@ class MoELayer:
             moe.moe_quantize_fp4(w[e], fmt, x, codes[e], sf[e])
             exps.append(x)
         return codes, sf, exps
+
+    @staticmethod
+    def _quantize_int4(w, group):
+        """Codes uint8 [E, N, K/2] and bf16 scales [E, N, K/group] of bf16 weights [E, N, K]: the
+        nearest of scale * (-7..7), the scale a seventh of the group's largest magnitude."""
+        E, N, K = w.shape
+        codes = torch.empty(E, N, K // 2, dtype=torch.uint8, device=w.device)
+        scales = torch.empty(E, N, K // group, dtype=torch.bfloat16, device=w.device)
+        for e in range(E):
+            v = w[e].float().view(N, K // group, group)
+            scales[e] = (v.abs().amax(2) / 7).bfloat16()
+            s = scales[e].float().unsqueeze(2)
+            q = torch.where(s > 0, v / s, 0).round().clamp(-7, 7).to(torch.int32).add(8).view(N, K)
+            codes[e] = (q[:, 0::2] + 16 * q[:, 1::2]).to(torch.uint8)
+        return codes, scales
+
+    def _ffn_int4(self, x, T, A, stream, mark):
+        """Dispatch and both expert products with 4-bit weights; y_perm is written."""
+        rows, offs = A + (T if self.int4_shared else 0), self.seg_offsets
+        xp = self.x_perm[:rows]
+        if self.int4_shared:
+            # rows [A, A + T) carry every token for the shared expert, expert E
+            moe.moe_permute_shared(x, self.k, self.dest_row[:A], xp, self.ws, stream)
+            with torch.cuda.stream(stream or torch.cuda.current_stream()):
+                self._seg_offsets_all[-1:].fill_(rows)
+            offs = self._seg_offsets_all
+        else:
+            moe.moe_permute(x, self.k, self.dest_row[:A], xp, self.ws, stream)
+        mark("permute")
+        moe.moe_grouped_product_int4(xp, offs, self._int4_experts, self.w_gate_up, self.h[:rows], self.ws, stream)
+        moe.moe_grouped_product_int4(self.h[:rows], offs, self._int4_experts, self.w_down, self.y_perm[:rows],
+                                     self.ws, stream)
 
     def _init_fp4(self, w_gate_up, w_down, shared_gu, shared_dn, scale_exp, max_tokens, device):
         fmt, dev = self.fp4, torch.device(device)
@@ -287,6 +367,43 @@ class MoELayer:
         moe.moe_gate_backward(logits, self.topk_ids[:logits.shape[0]], grad_w, self.gate,
                               grad_logits, self.ws, stream)
 
+    def combine_backward(self, grad_y, grad_y_perm, grad_topk_w, gate=None, grad_shared=None,
+                         grad_weight=None, grad_gate=None, stream=None):
+        """Gradients of the last step's expert rows (grad_y_perm, of y_perm's first n_rows) and
+        weights for a gradient of its output: moe_combine_norm_backward with a block (the gate that
+        forward was given; the residual's gradient is residual_scale * grad_y), else
+        moe_combine_backward, where the shared rows' gradient is grad_y itself."""
+        T = grad_y.shape[0]
+        rows, w = self.y_perm[:grad_y_perm.shape[0]], self.topk_w[:T]
+        dest = self.dest_row[:T * self.k]
+        if self.block is None:
+            if gate is not None or grad_shared is not None or grad_weight is not None or grad_gate is not None:
+                raise ValueError("combine_backward: no block")
+            moe.moe_combine_backward(grad_y, rows, dest, w, grad_y_perm, grad_topk_w, self.ws, stream)
+            return
+        moe.moe_combine_norm_backward(grad_y, rows, dest, w, self.block, grad_y_perm, grad_topk_w, self.ws,
+                                      self.norm_scratch, shared=self.shared_output(T), weight=self.post_weight,
+                                      gate=gate, grad_shared=grad_shared, grad_weight=grad_weight,
+                                      grad_gate=grad_gate, stream=stream)
+
+    def permute_backward(self, grad_x_perm, grad_x, add=None, stream=None):
+        """Gradient of the last step's tokens for a gradient of their dispatched rows
+        (moe_permute_backward); add holds what reaches them by other ways."""
+        T = grad_x.shape[0]
+        moe.moe_permute_backward(grad_x_perm, self.dest_row[:T * self.k].view(T, self.k), grad_x, self.ws, add,
+                                 stream)
+
+    def norm_backward(self, grad_x_perm, x, weight, eps, grad_x, grad_weight, add=None, residual_grad=None,
+                      stream=None):
+        """Gradient of the rows x before the norm whose result the last step dispatched, with that of
+        the residual beside them (moe_norm_backward; needs a block)."""
+        if self.block is None:
+            raise ValueError("norm_backward needs a block")
+        T = x.shape[0]
+        moe.moe_norm_backward(grad_x_perm, x, weight, eps, grad_x, grad_weight, self.ws, self.norm_scratch,
+                              dest_row=self.dest_row[:T * self.k].view(T, self.k), add=add,
+                              residual_grad=residual_grad, residual_scale=self.block.residual_scale, stream=stream)
+
     @staticmethod
     def _pack(w_gate_up, w_down):
         gu, d = torch.empty_like(w_gate_up), torch.empty_like(w_down)
@@ -309,15 +426,37 @@ class MoELayer:
             self._shared_offsets[T] = t
         return t
 
+    def _combine(self, rows, dest, w, y, shared, tail, masked, stream):
+        """Rows back to tokens: the sum alone, or on through the block's norm, gate and residual."""
+        residual, gate, next_out = tail
+        if residual is not None:
+            moe.moe_combine_norm(rows, dest, w, residual, self.block, y, self.ws, shared=shared,
+                                 weight=self.post_weight, gate=gate,
+                                 next_weight=None if next_out is None else self.next_weight,
+                                 next_out=next_out, stream=stream)
+        elif masked:
+            moe.moe_combine_masked(rows, dest, w, y, self.ws, shared, stream)
+        else:
+            moe.moe_combine(rows, dest, w, y, self.ws, shared, stream)
+
     def forward(self, logits: torch.Tensor, x: torch.Tensor, y: torch.Tensor, stream=None,
-                mark=None):
+                mark=None, residual: Optional[torch.Tensor] = None,
+                gate: Optional[torch.Tensor] = None, next_out: Optional[torch.Tensor] = None):
         """One step on device-resident inputs; y [T,H] bf16 is written.
         mark(name), if given, is called after each stage is enqueued (the
-        benchmark records a CUDA event there)."""
+        benchmark records a CUDA event there).
+        With a block and residual (fp32 or bf16 [T,H]): x is the normalised
+        residual (moe_norm), y has the residual's type and may be the residual
+        itself; gate fp32 [T] or None; next_out bf16 [T,H] or None."""
         mark = mark or (lambda name: None)
         T = x.shape[0]
         if T > self.max_tokens:
             raise ValueError("more tokens than the layer was sized for")
+        if residual is not None and self.block is None:
+            raise ValueError("a residual needs a block")
+        if residual is None and (gate is not None or next_out is not None):
+            raise ValueError("gate and next_out belong to a residual")
+        tail = (residual, gate, next_out)
         A = T * self.k
         ids, w = self.topk_ids[:T], self.topk_w[:T]
         if self.gate is not None:
@@ -327,7 +466,7 @@ class MoELayer:
         self._fork_prefetch(ids, stream)
         mark("route")
         if self.masked_cap is not None:
-            return self._forward_masked(x, y, ids, w, T, A, stream, mark)
+            return self._forward_masked(x, y, ids, w, T, A, stream, mark, tail)
         if self.replica_relax is None:
             moe.moe_dispatch_layout(ids, self.placement, self.slot[:A], self.seg_counts,
                                     self.seg_offsets, self.dest_row[:A], self.src_assign[:A],
@@ -345,6 +484,8 @@ class MoELayer:
         self._fork_balance(stream)
         if self.fp4 is not None:
             self._ffn_fp4(x, T, A, stream, mark)
+        elif self.int4:
+            self._ffn_int4(x, T, A, stream, mark)
         elif self.gather:
             mark("permute")
             moe.moe_grouped_ffn_gather(x, self.k, self.src_assign[:A], self.seg_offsets,
@@ -371,9 +512,9 @@ class MoELayer:
             self._ffn(self.x_perm[:A], self.seg_offsets, self.placement.slot_expert,
                       self.w_gate_up, self.w_down, self.h[:A], self.y_perm[:A], self.ws, stream)
         mark("grouped_ffn")
-        shared = self.shared_output(T) if self.fuse_shared or self.fp4 is not None \
+        shared = self.shared_output(T) if self.fuse_shared or self.fp4 is not None or self.int4 \
             else self._shared(x, T, stream, mark)
-        moe.moe_combine(self.y_perm[:A], self.dest_row[:A], w, y, self.ws, shared, stream)
+        self._combine(self.y_perm[:A], self.dest_row[:A], w, y, shared, tail, False, stream)
         mark("combine")
         self._join_balance(stream, mark)
         return y
@@ -406,7 +547,7 @@ class MoELayer:
     def shared_output(self, T: int):
         """The shared expert's output rows [T, H] of the last step, or None
         when the layer has no shared expert."""
-        if self.fuse_shared or self.fp4_shared:
+        if self.fuse_shared or self.fp4_shared or self.int4_shared:
             A = T * self.k
             return self.y_perm[A:A + T]
         return self.shared_y[:T] if self.shared_I else None
@@ -434,7 +575,7 @@ class MoELayer:
         (stream or torch.cuda.current_stream()).wait_event(self._ev_stats)
         mark("balance")
 
-    def _forward_masked(self, x, y, ids, w, T, A, stream, mark):
+    def _forward_masked(self, x, y, ids, w, T, A, stream, mark, tail):
         """The step on the fixed-capacity layout: every buffer and launch has
         the same shape whatever the routing; dropped assignments add
         nothing to y."""
@@ -451,25 +592,26 @@ class MoELayer:
                                    stream)
         mark("grouped_ffn")
         shared = self._shared(x, T, stream, mark)
-        moe.moe_combine_masked(self.y_perm, self.dest_row[:A], w, y, self.ws, shared, stream)
+        self._combine(self.y_perm, self.dest_row[:A], w, y, shared, tail, True, stream)
         mark("combine")
         self._join_balance(stream, mark)
         return y
 
-    def capture(self, logits: torch.Tensor, x: torch.Tensor, y: torch.Tensor):
+    def capture(self, logits: torch.Tensor, x: torch.Tensor, y: torch.Tensor, **tail):
         """Record one whole step (every kernel of forward) as a CUDA graph
         over these fixed buffers and return it; graph.replay() then reruns
         the step on whatever the buffers hold, with one launch from the
         host.  Segment sizes never reach the host, so the dynamic
-        contiguous layout needs no padding to be replayable.  Call forward
-        once first (per-device set-up happens on the first call)."""
+        contiguous layout needs no padding to be replayable.  tail:
+        forward's residual, gate and next_out.  Call forward once first
+        (per-device set-up happens on the first call)."""
         torch.cuda.synchronize()
         graph = torch.cuda.CUDAGraph()
         stream = torch.cuda.Stream(device=y.device)
         stream.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(stream):
             with torch.cuda.graph(graph, stream=stream):
-                self.forward(logits, x, y, torch.cuda.current_stream())
+                self.forward(logits, x, y, torch.cuda.current_stream(), **tail)
         torch.cuda.current_stream().wait_stream(stream)
         return graph
 

@@ -948,32 +948,53 @@ def new_norm_scratch(T: int, H: int, device=None, stream=None) -> torch.Tensor:
         return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 
 
+def _needs(dtype, names: str, *tensors):
+    """_need for several tensors (None passes): a call each costs a quarter of a microsecond."""
+    try:
+        for t in tensors:
+            if t is not None and (t.dtype is not dtype or not t.is_cuda or not t.is_contiguous()):
+                raise AttributeError
+    except AttributeError:
+        for name, t in zip(names.split(), tensors):
+            if t is not None:
+                _need(t, dtype, name)
+        raise
+
+
+def _shapes(call: str, shape, *tensors):
+    """Optional tensors of one shape."""
+    for t in tensors:
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{call}: inconsistent shapes")
+
+
+_F32T, _BF16T, _I32T = torch.float32, torch.bfloat16, torch.int32
+
+
 def moe_norm(x, weight, eps: float, out, stream=None):
     """out (bf16 [T, H]) = x / rms(x) * weight; x fp32 or bf16, weight fp32 [H]
     or None."""
     kind = _typed(x, "x")
-    _bf16(out, "out")
-    if x.dim() != 2 or out.shape != x.shape:
+    _needs(_BF16T, "out", out)
+    _needs(_F32T, "weight", weight)
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("moe_norm: inconsistent shapes")
-    T, H = x.shape
-    _maybe(weight, torch.float32, (H,), "weight", "moe_norm")
-    _check("moe_norm", lib().moe_norm(_ptr(x), kind, T, H, _ptr(weight), eps, _ptr(out),
+    T, H = shape
+    _shapes("moe_norm", shape, out)
+    _shapes("moe_norm", (H,), weight)
+    _check("moe_norm", lib().moe_norm(x.data_ptr(), kind, T, H, _ptr(weight), eps, out.data_ptr(),
                                       _stream(stream)))
 
 
 def _block_shapes(call: str, row, y_perm, dest_row, topk_w):
-    """(T, k, H) of a combine: row [T, H], y_perm [n_rows, H], dest_row and topk_w [T, k]
+    """(T, k, H, n_rows) of a combine: row [T, H], y_perm [n_rows, H], dest_row and topk_w [T, k]
     (dest_row may also be flat, as the layout writes it)."""
-    _bf16(y_perm, "y_perm")
-    _need(dest_row, torch.int32, "dest_row")
-    _need(topk_w, torch.float32, "topk_w")
-    if row.dim() != 2 or y_perm.dim() != 2 or topk_w.dim() != 2:
+    shape, rows, w = row.shape, y_perm.shape, topk_w.shape
+    if len(shape) != 2 or len(rows) != 2 or len(w) != 2 or w[0] != shape[0] or rows[1] != shape[1] \
+            or dest_row.numel() != w[0] * w[1]:
         raise ValueError(f"{call}: inconsistent shapes")
-    T, H = row.shape
-    k = topk_w.shape[1]
-    if topk_w.shape[0] != T or y_perm.shape[1] != H or dest_row.numel() != T * k:
-        raise ValueError(f"{call}: inconsistent shapes")
-    return T, k, H
+    return shape[0], w[1], shape[1], rows[0]
 
 
 def moe_combine_norm(y_perm, dest_row, topk_w, residual, cfg: BlockCfg, y, ws, shared=None, weight=None,
@@ -983,49 +1004,57 @@ def moe_combine_norm(y_perm, dest_row, topk_w, residual, cfg: BlockCfg, y, ws, s
     next_weight fp32 [H] or None; gate fp32 [T] or None; dest_row -1 is a drop."""
     call = "moe_combine_norm"
     kind = _typed(residual, "residual")
-    _need(y, residual.dtype, "y")
-    T, k, H = _block_shapes(call, residual, y_perm, dest_row, topk_w)
-    if y.shape != residual.shape:
-        raise ValueError("moe_combine_norm: inconsistent shapes")
-    _maybe(shared, torch.bfloat16, (T, H), "shared", call)
-    _maybe(weight, torch.float32, (H,), "weight", call)
-    _maybe(gate, torch.float32, (T,), "gate", call)
-    _maybe(next_weight, torch.float32, (H,), "next_weight", call)
-    _maybe(next_out, torch.bfloat16, (T, H), "next_out", call)
+    _needs(residual.dtype, "y", y)
+    _needs(_BF16T, "y_perm shared next_out", y_perm, shared, next_out)
+    _needs(_F32T, "topk_w weight gate next_weight", topk_w, weight, gate, next_weight)
+    _needs(_I32T, "dest_row", dest_row)
+    T, k, H, n = _block_shapes(call, residual, y_perm, dest_row, topk_w)
+    _shapes(call, (T, H), y, shared, next_out)
+    _shapes(call, (H,), weight, next_weight)
+    _shapes(call, (T,), gate)
     _check(call, lib().moe_combine_norm(
-        _ptr(y_perm), y_perm.shape[0], _ptr(dest_row), _ptr(topk_w), T, k, H, _ptr(shared),
-        _ptr(residual), kind, _ptr(weight), _ptr(gate), ctypes.byref(cfg), _ptr(y),
-        _ptr(next_weight), _ptr(next_out), _ptr(ws), ws.numel(), _stream(stream)))
+        y_perm.data_ptr(), n, dest_row.data_ptr(), topk_w.data_ptr(), T, k, H, _ptr(shared),
+        residual.data_ptr(), kind, _ptr(weight), _ptr(gate), ctypes.byref(cfg), y.data_ptr(),
+        _ptr(next_weight), _ptr(next_out), ws.data_ptr(), ws.numel(), _stream(stream)))
 
 
 def moe_combine_backward(grad_y, y_perm, dest_row, topk_w, grad_y_perm, grad_topk_w, ws, stream=None):
     """Gradients of moe_combine's expert rows and weights for grad_y (fp32 or bf16 [T, H]); rows of
     grad_y_perm that no assignment lands on are left as they are."""
+    call = "moe_combine_backward"
     kind = _typed(grad_y, "grad_y")
-    T, k, H = _block_shapes("moe_combine_backward", grad_y, y_perm, dest_row, topk_w)
-    _bf16(grad_y_perm, "grad_y_perm")
-    _need(grad_topk_w, torch.float32, "grad_topk_w")
-    if grad_y_perm.shape != y_perm.shape or grad_topk_w.shape != topk_w.shape:
-        raise ValueError("moe_combine_backward: inconsistent shapes")
-    _check("moe_combine_backward", lib().moe_combine_backward(
-        _ptr(grad_y), kind, _ptr(y_perm), y_perm.shape[0], _ptr(dest_row), _ptr(topk_w), T, k, H,
-        _ptr(grad_y_perm), _ptr(grad_topk_w), _ptr(ws), ws.numel(), _stream(stream)))
+    _needs(_BF16T, "y_perm grad_y_perm", y_perm, grad_y_perm)
+    _needs(_F32T, "topk_w grad_topk_w", topk_w, grad_topk_w)
+    _needs(_I32T, "dest_row", dest_row)
+    T, k, H, n = _block_shapes(call, grad_y, y_perm, dest_row, topk_w)
+    _shapes(call, (n, H), grad_y_perm)
+    _shapes(call, (T, k), grad_topk_w)
+    _check(call, lib().moe_combine_backward(
+        grad_y.data_ptr(), kind, y_perm.data_ptr(), n, dest_row.data_ptr(), topk_w.data_ptr(), T, k, H,
+        grad_y_perm.data_ptr(), grad_topk_w.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
 
 
 def moe_permute_backward(grad, dest_row, grad_x, ws, add=None, stream=None):
     """grad_x (fp32 or bf16 [T, H]) = add + the sum of grad (bf16 [n_rows, H]) over each token's
     rows; dest_row int32 [T, k]."""
+    call = "moe_permute_backward"
     kind = _typed(grad_x, "grad_x")
-    _bf16(grad, "grad")
-    _need(dest_row, torch.int32, "dest_row")
-    if grad_x.dim() != 2 or grad.dim() != 2 or dest_row.dim() != 2 or dest_row.shape[0] != grad_x.shape[0] \
-            or grad.shape[1] != grad_x.shape[1]:
+    _needs(_BF16T, "grad add", grad, add)
+    _needs(_I32T, "dest_row", dest_row)
+    shape, rows, d = grad_x.shape, grad.shape, dest_row.shape
+    if len(shape) != 2 or len(rows) != 2 or len(d) != 2 or d[0] != shape[0] or rows[1] != shape[1]:
         raise ValueError("moe_permute_backward: inconsistent shapes")
-    T, H = grad_x.shape
-    _maybe(add, torch.bfloat16, (T, H), "add", "moe_permute_backward")
-    _check("moe_permute_backward", lib().moe_permute_backward(
-        _ptr(grad), grad.shape[0], _ptr(dest_row), _ptr(add), T, dest_row.shape[1], H, _ptr(grad_x),
-        kind, _ptr(ws), ws.numel(), _stream(stream)))
+    _shapes(call, shape, add)
+    _check(call, lib().moe_permute_backward(
+        grad.data_ptr(), rows[0], dest_row.data_ptr(), _ptr(add), shape[0], d[1], shape[1],
+        grad_x.data_ptr(), kind, ws.data_ptr(), ws.numel(), _stream(stream)))
+
+
+def _scratch(scratch):
+    if scratch is None:
+        return None, 0
+    _need(scratch, torch.uint8, "scratch")
+    return scratch.data_ptr(), scratch.numel()
 
 
 def moe_combine_norm_backward(grad_y, y_perm, dest_row, topk_w, cfg: BlockCfg, grad_y_perm, grad_topk_w,
@@ -1035,24 +1064,21 @@ def moe_combine_norm_backward(grad_y, y_perm, dest_row, topk_w, cfg: BlockCfg, g
     grad_y; the last three are written where a tensor is given (grad_weight needs scratch)."""
     call = "moe_combine_norm_backward"
     kind = _typed(grad_y, "grad_y")
-    T, k, H = _block_shapes(call, grad_y, y_perm, dest_row, topk_w)
-    _bf16(grad_y_perm, "grad_y_perm")
-    _need(grad_topk_w, torch.float32, "grad_topk_w")
-    if grad_y_perm.shape != y_perm.shape or grad_topk_w.shape != topk_w.shape:
-        raise ValueError("moe_combine_norm_backward: inconsistent shapes")
-    _maybe(shared, torch.bfloat16, (T, H), "shared", call)
-    _maybe(weight, torch.float32, (H,), "weight", call)
-    _maybe(gate, torch.float32, (T,), "gate", call)
-    _maybe(grad_shared, torch.bfloat16, (T, H), "grad_shared", call)
-    _maybe(grad_weight, torch.float32, (H,), "grad_weight", call)
-    _maybe(grad_gate, torch.float32, (T,), "grad_gate", call)
-    if scratch is not None:
-        _need(scratch, torch.uint8, "scratch")
+    _needs(_BF16T, "y_perm grad_y_perm shared grad_shared", y_perm, grad_y_perm, shared, grad_shared)
+    _needs(_F32T, "topk_w grad_topk_w weight gate grad_weight grad_gate", topk_w, grad_topk_w, weight, gate,
+           grad_weight, grad_gate)
+    _needs(_I32T, "dest_row", dest_row)
+    T, k, H, n = _block_shapes(call, grad_y, y_perm, dest_row, topk_w)
+    _shapes(call, (n, H), grad_y_perm)
+    _shapes(call, (T, k), grad_topk_w)
+    _shapes(call, (T, H), shared, grad_shared)
+    _shapes(call, (H,), weight, grad_weight)
+    _shapes(call, (T,), gate, grad_gate)
     _check(call, lib().moe_combine_norm_backward(
-        _ptr(grad_y), kind, _ptr(y_perm), y_perm.shape[0], _ptr(dest_row), _ptr(topk_w), T, k, H,
-        _ptr(shared), _ptr(weight), _ptr(gate), ctypes.byref(cfg), _ptr(grad_y_perm),
-        _ptr(grad_topk_w), _ptr(grad_shared), _ptr(grad_weight), _ptr(grad_gate), _ptr(scratch),
-        0 if scratch is None else scratch.numel(), _ptr(ws), ws.numel(), _stream(stream)))
+        grad_y.data_ptr(), kind, y_perm.data_ptr(), n, dest_row.data_ptr(), topk_w.data_ptr(), T, k, H,
+        _ptr(shared), _ptr(weight), _ptr(gate), ctypes.byref(cfg), grad_y_perm.data_ptr(),
+        grad_topk_w.data_ptr(), _ptr(grad_shared), _ptr(grad_weight), _ptr(grad_gate), *_scratch(scratch),
+        ws.data_ptr(), ws.numel(), _stream(stream)))
 
 
 def moe_norm_backward(grad, x, weight, eps: float, grad_x, grad_weight, ws, scratch=None, dest_row=None,
@@ -1062,27 +1088,26 @@ def moe_norm_backward(grad, x, weight, eps: float, grad_x, grad_weight, ws, scra
     of grad (bf16 [n_rows, H]).  grad_weight fp32 [H] (with scratch) or None."""
     call = "moe_norm_backward"
     kind = _typed(x, "x")
-    _bf16(grad, "grad")
-    _need(grad_x, x.dtype, "grad_x")
-    if x.dim() != 2 or grad.dim() != 2 or grad_x.shape != x.shape or grad.shape[1] != x.shape[1]:
+    _needs(x.dtype, "grad_x residual_grad", grad_x, residual_grad)
+    _needs(_BF16T, "grad add", grad, add)
+    _needs(_F32T, "weight grad_weight", weight, grad_weight)
+    shape, rows, k = x.shape, grad.shape, 0
+    if len(shape) != 2 or len(rows) != 2 or rows[1] != shape[1]:
         raise ValueError("moe_norm_backward: inconsistent shapes")
-    T, H = x.shape
-    k = 0
+    T, H = shape
     if dest_row is not None:
-        _need(dest_row, torch.int32, "dest_row")
+        _needs(_I32T, "dest_row", dest_row)
         if dest_row.dim() != 2 or dest_row.shape[0] != T:
             raise ValueError("moe_norm_backward: inconsistent shapes")
         k = dest_row.shape[1]
-    _maybe(weight, torch.float32, (H,), "weight", call)
-    _maybe(add, torch.bfloat16, (T, H), "add", call)
-    _maybe(residual_grad, x.dtype, (T, H), "residual_grad", call)
-    _maybe(grad_weight, torch.float32, (H,), "grad_weight", call)
-    if scratch is not None:
-        _need(scratch, torch.uint8, "scratch")
+    elif rows[0] != T:
+        raise ValueError("moe_norm_backward: inconsistent shapes")
+    _shapes(call, shape, grad_x, add, residual_grad)
+    _shapes(call, (H,), weight, grad_weight)
     _check(call, lib().moe_norm_backward(
-        _ptr(grad), grad.shape[0], _ptr(dest_row), k, _ptr(add), _ptr(x), kind, T, H, _ptr(weight),
-        eps, _ptr(residual_grad), residual_scale, _ptr(grad_x), _ptr(grad_weight), _ptr(scratch),
-        0 if scratch is None else scratch.numel(), _ptr(ws), ws.numel(), _stream(stream)))
+        grad.data_ptr(), rows[0], _ptr(dest_row), k, _ptr(add), x.data_ptr(), kind, T, H, _ptr(weight),
+        eps, _ptr(residual_grad), residual_scale, grad_x.data_ptr(), _ptr(grad_weight),
+        *_scratch(scratch), ws.data_ptr(), ws.numel(), _stream(stream)))
 
 
 def moe_status_string(status: int) -> str:
