@@ -116,6 +116,8 @@ class MoELayer:
                 raise ValueError("int4 experts: the shared expert needs the routed experts' width")
         if block is None and (post_weight is not None or next_weight is not None):
             raise ValueError("post_weight and next_weight belong to a block")
+        if post_weight is not None and not block.post_norm:
+            raise ValueError("post_weight belongs to a block with post_norm")
         self.block, self.post_weight, self.next_weight = block, post_weight, next_weight
         if gate is not None and gate.k != k:
             raise ValueError("gate.k must be k")

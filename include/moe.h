@@ -738,7 +738,8 @@ moe_status moe_pack_weights_int4(const uint8_t *codes, const uint16_t *scales,
  *  w_packed    moe_pack_weights_int4 of the same E, N, K, group, zeros or none
  *              (has_zeros) and epilogue.
  *  out         device fp32 or bf16 (out_type) [n_rows, N or N/2], contiguous,
- *              16-byte aligned; rows outside every segment are left unwritten.
+ *              16-byte aligned, overlapping no input; rows outside every segment
+ *              are left unwritten.
  *  Limits: those of moe_pack_weights_int4, S <= 1024, n_rows < 2^31 - 64, and
  *  (n_rows / 8 + S) * N / 32 (SwiGLU: the same) below 2^31 - 65536 tiles.  ws: at
  *  least MOE_WS_STATUS_BYTES.  Device errors: MOE_ERR_DEVICE_INDEX (an expert id

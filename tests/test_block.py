@@ -285,6 +285,9 @@ CASES = [  # T, H, k, type, post, gate, shared, weight, drop, scale
     (7, 8200, 8, F32, True, True, True, True, 0.2, 0.25),
     (2, 16384, 16, BF, True, False, False, True, 0, 1.0),
     (700, 136, 5, BF, True, True, True, True, 0.1, 1.0),
+    # rows of which half have a place in shared memory at a time, or one team instead of two
+    (3, 8192, 16, F32, True, True, True, True, 0.2, 1.0),
+    (5, 4096, 16, F32, True, False, True, True, 0.2, 1.0),
 ]
 
 
@@ -565,6 +568,37 @@ def test_another_stream_and_a_replayed_graph():
     for a, b in zip(got, want):
         keep = slice(None) if a.shape != s["yp"].shape else s["landed"]
         assert torch.equal(a[keep], b[keep])
+
+
+@pytest.mark.gpu
+def test_no_expert_rows_at_all():
+    """An empty dispatched buffer: every assignment is dropped."""
+    s = inputs(5, 72, 2, BF, True, True, True, 0, seed=11)
+    s["dest"].fill_(-1)
+    e = {**s, "yp": s["yp"][:0], "grad": s["grad"][:0], "landed": s["landed"][:0]}
+    for f in (lambda q: forward(q, True, 0.5)[:2], lambda q: backward(q, True)[0].values(),
+              lambda q: norm_backward(q, False, 0.5)[:2]):
+        for a, b in zip(f(s), f(e)):
+            assert torch.equal(a[:b.shape[0]], b) and (a.shape == b.shape or (a == 7.0).all())
+
+
+@pytest.mark.gpu
+def test_calls_on_two_streams_at_once():
+    m = moe()
+    qs = [inputs(400, 2048, 4, BF, True, True, True, 0.1, seed=20 + i) for i in range(2)]
+    want = [[*backward(q, True)[0].values(), *norm_backward(q, False, 1.0)[:2]] for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        got = []
+        for q, st in zip(qs, streams):
+            with torch.cuda.stream(st):
+                got.append([*backward(q, True, stream=st)[0].values(), *norm_backward(q, False, 1.0, stream=st)[:2]])
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        for a, b in zip(g, w):
+            assert torch.equal(a.nan_to_num(), b.nan_to_num())
 
 
 @pytest.mark.gpu

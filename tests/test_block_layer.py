@@ -42,7 +42,7 @@ def test_refusals():
                 dict(int4=64, fp8_dispatch=True), dict(int4=64, I=96), dict(int4=128, H=320),
                 dict(int4=64, shared_w_gate_up=torch.empty(1, 64, 256)), dict(two, int4=64), dict(two, w_down=gu),
                 dict(two, shared_w_gate_up=torch.empty(1, 256, 256)), dict(post_weight=torch.ones(256)),
-                dict(next_weight=torch.ones(256))):
+                dict(next_weight=torch.ones(256)), dict(block=m.BlockCfg(0), post_weight=torch.ones(256))):
         with pytest.raises(ValueError):
             MoELayer(**{**base, **bad})
 
