@@ -1020,7 +1020,13 @@ __global__ void __launch_bounds__(kSumThreads)
 }
 
 // ------------------------------------------------------------------ host
-constexpr int kStreamThreads = 128;
+// Threads of the streaming kernels: at most 128, and such that their turns over a
+// row are full (H = 1416: 96 in two turns instead of 128 of which half the second
+// turn's idle).
+int stream_threads(int H) {
+  const int pieces = H / 8, turns = (pieces + 127) / 128;
+  return ((pieces + turns - 1) / turns + 31) / 32 * 32;
+}
 
 int row_chunks(int H) { return H <= kRowThreads * 2 * 8 ? 2 : 4; }
 int row_threads(int H) {
@@ -1133,7 +1139,7 @@ moe_status run_combine_norm(const CombineNormParams &p, cudaStream_t st) {
 template <typename X>
 moe_status run_combine_bwd(const CombineBwdParams &p, cudaStream_t st) {
   const unsigned g = stream_grid(p.T);
-  const int n = kStreamThreads;
+  const int n = stream_threads(p.H);
   if (p.k <= 2) return launch(combine_bwd_kernel<2, X>, g, n, st, p);
   if (p.k <= 4) return launch(combine_bwd_kernel<4, X>, g, n, st, p);
   if (p.k <= 8) return launch(combine_bwd_kernel<8, X>, g, n, st, p);
@@ -1166,7 +1172,7 @@ moe_status run_norm_bwd(const NormBwdParams &p, cudaStream_t st) {
 template <typename X>
 moe_status run_permute_bwd(const uint16_t *grad, const Rows &rows, const uint16_t *add, int64_t T,
                            int32_t k, int32_t H, void *gx, cudaStream_t st) {
-  const dim3 g(stream_grid(T)), b(kStreamThreads);
+  const dim3 g(stream_grid(T)), b((unsigned)stream_threads(H));
   const uint4 *in = reinterpret_cast<const uint4 *>(grad), *ad = reinterpret_cast<const uint4 *>(add);
   X *out = static_cast<X *>(gx);
   if (k <= 2) return moe_host::launch_pdl(permute_bwd_kernel<2, X>, g, b, 0, st, in, rows, ad, T, k, H, out);
