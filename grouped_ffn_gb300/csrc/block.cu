@@ -23,7 +23,10 @@
 namespace {
 
 // A token's team has up to 512 threads, each with U pieces of 8 elements: two for
-// rows of up to 8192, four beyond.  R of the U pieces have a place in shared memory.
+// rows of up to 8192, four beyond; in the forward pass one for rows of up to 1024,
+// with 64 registers and twice the threads an SM (4096 tokens of 1024, six experts,
+// combine with norms: 13.4 us against 16 with two pieces).
+// R of the U pieces have a place in shared memory.
 constexpr int kRowThreads = 512;
 constexpr int kMaxH = kRowThreads * 4 * 8;
 constexpr int kSmemLimit = 225 * 1024;
@@ -227,7 +230,10 @@ __device__ __forceinline__ float inv_rms(float sum, float inv_h, float eps) {
   return rsqrtf(fmaf(sum, inv_h, eps));
 }
 
-// The threads of one token.
+// The threads of one token: a CTA's (ALONE), or some of its warps with a barrier of
+// their own.  (A barrier whose number the compiler does not know reserves all 16,
+// and an SM has them for four CTAs only.)
+template <bool ALONE>
 struct Team {
   int index, threads, tid, warp, nw, lane;
   __device__ __forceinline__ explicit Team(int threads_) : threads(threads_) {
@@ -238,7 +244,10 @@ struct Team {
     lane = threadIdx.x & 31;
   }
   __device__ __forceinline__ void sync() const {
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + index), "r"(threads) : "memory");
+    if (ALONE)
+      __syncthreads();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + index), "r"(threads) : "memory");
   }
 };
 
@@ -259,7 +268,7 @@ struct Norm {
 };
 template <int U>
 __device__ __forceinline__ Norm row_norm(Pair (&x)[U][4], float inv_h, float eps, float *buf,
-                                         const Team &tm) {
+                                         const Team<true> &tm) {
   auto squares = [&]() {
     Pair s = mul(x[0][0], x[0][0]);
 #pragma unroll
@@ -324,7 +333,9 @@ __device__ __forceinline__ Meta load_meta(const int32_t *dest_row, const float *
   return m;
 }
 // Rows outside are reported and dropped; a dropped assignment weighs nothing.
-__device__ __forceinline__ void settle(Meta &m, const Rows &p, int64_t t, int k, const Team &tm) {
+template <bool ALONE>
+__device__ __forceinline__ void settle(Meta &m, const Rows &p, int64_t t, int k,
+                                       const Team<ALONE> &tm) {
   if (m.row != -1 && (m.row < 0 || m.row >= p.n_rows)) {
     if (tm.warp == 0)
       moe::report_error(p.status, MOE_ERR_DEVICE_INDEX, (int32_t)(t * k + tm.lane), moe::K_BLOCK);
@@ -345,12 +356,12 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, int step, const uint4 *r
 
 // out = x / rms(x) * weight.  R / U tokens are on their way.
 template <int U, int R, typename X>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, U <= 2 ? 2 : 1)
     norm_kernel(const X *x, int64_t T, int H, const float *__restrict__ weight, float eps,
                 __nv_bfloat16 *out) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float buf[2][32];
-  const Team tm((int)blockDim.x);
+  const Team<true> tm((int)blockDim.x);
   const int H8 = H / 8, slot = tm.threads * 16 * Chunk<X>::N;
   const float inv_h = 1.0f / (float)H;
   uint8_t *mine = smem + tm.warp * 512 * Chunk<X>::N;  // the warp's places
@@ -410,10 +421,11 @@ struct CombineNormParams {
 // c = shared + sum_j w_j Y[row_j], y = scale x + gate norm(c), next = norm(y).
 // One CTA a token at a time; c and then y stay in registers across the two sums.
 template <int U, int R, typename X>
-__global__ void __launch_bounds__(kRowThreads) combine_norm_kernel(const CombineNormParams p) {
+__global__ void __launch_bounds__(kRowThreads, U == 1 ? 2 : 1)
+    combine_norm_kernel(const CombineNormParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float buf[2][2][32];
-  const Team tm((int)blockDim.x);
+  const Team<true> tm((int)blockDim.x);
   const int H8 = p.H / 8, step = tm.threads * 16;
   const float inv_h = 1.0f / (float)p.H;
   const int at_res = p.k * step, at_shared = at_res + Chunk<X>::N * step;
@@ -488,6 +500,10 @@ __global__ void __launch_bounds__(kRowThreads) combine_norm_kernel(const Combine
       res[u].set(acc[u]);
       res[u].store(static_cast<X *>(p.y) + t * p.H, c, H8, tm.lane);
       res[u].get(acc[u]);  // as it is held
+      if (c >= H8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[u][i] = 0;
+      }
     }
     if (p.next) {
       const Norm n = row_norm(acc, inv_h, p.eps, buf[par][1], tm);
@@ -577,7 +593,7 @@ __global__ void __launch_bounds__(128) combine_bwd_kernel(const CombineBwdParams
 // to the CTA's partial row.  Uses the CTA's shared memory from its start.
 template <int U>
 __device__ __forceinline__ void put_partial(const Pair (&pw)[U][4], float *partial, int H, int teams,
-                                            float *smem, const Team &tm) {
+                                            float *smem, const Team<false> &tm) {
   __syncthreads();  // (all copies to shared memory have been waited for)
   const int H8 = H / 8;
   Chunk<float> o;
@@ -623,7 +639,7 @@ __global__ void __launch_bounds__(kRowThreads)
   constexpr int kSums = 2 * KMAX;
   constexpr int kBuf = (kSums + 2) * 32;
   extern __shared__ __align__(16) uint8_t smem[];
-  const Team tm(team_threads);
+  const Team<false> tm(team_threads);
   const int teams = blockDim.x / team_threads;
   const int H8 = p.H / 8, step = tm.threads * 16;
   const float inv_h = 1.0f / (float)p.H;
@@ -817,7 +833,7 @@ __global__ void __launch_bounds__(kRowThreads)
     norm_bwd_kernel(const NormBwdParams p, const int team_threads) {
   constexpr int kBuf = 2 * 32;
   extern __shared__ __align__(16) uint8_t smem[];
-  const Team tm(team_threads);
+  const Team<false> tm(team_threads);
   const int teams = blockDim.x / team_threads;
   const int H8 = p.H / 8, step = tm.threads * 16;
   const float inv_h = 1.0f / (float)p.H;
@@ -1029,10 +1045,9 @@ int stream_threads(int H) {
 }
 
 int row_chunks(int H) { return H <= kRowThreads * 2 * 8 ? 2 : 4; }
-int row_threads(int H) {
-  const int u = row_chunks(H);
-  return ((H / 8 + u - 1) / u + 31) / 32 * 32;
-}
+int fwd_pieces(int H) { return H <= 1024 ? 1 : row_chunks(H); }
+int threads_of(int H, int u) { return ((H / 8 + u - 1) / u + 31) / 32 * 32; }
+int row_threads(int H) { return threads_of(H, row_chunks(H)); }
 
 // CTAs of the streaming kernels, at most 32 an SM.
 unsigned stream_grid(int64_t T) {
@@ -1045,11 +1060,12 @@ int bwd_teams(int H) {
   const int n = kRowThreads / row_threads(H);
   return n < 1 ? 1 : n > 8 ? 8 : n;
 }
-// and the most CTAs that they run: one an SM with up to 128 registers a thread
-// (the norm weights' gradients have as many partial rows).
+// and the most CTAs that they run: 512 threads an SM with up to 128 registers (the
+// norm weights' gradients have as many partial rows).
 unsigned bwd_grid(int64_t T, int H) {
   const int teams = bwd_teams(H);
-  const int64_t cap = moe_host::sm_count(), need = (T + teams - 1) / teams;
+  const int64_t cap = (int64_t)moe_host::sm_count() * (kRowThreads / (teams * row_threads(H)));
+  const int64_t need = (T + teams - 1) / teams;
   return (unsigned)(need < cap ? need : cap);
 }
 
@@ -1072,7 +1088,8 @@ moe_status allow_smem(size_t bytes) {
 }
 
 // One CTA a token at a time: as many CTAs an SM as shared memory and `sm_threads`
-// threads allow.
+// threads allow (512 with up to 128 registers).  All run at once, each with its
+// share of the tokens.
 template <auto KERNEL, typename... A>
 moe_status launch_rows(int64_t T, int threads, int sm_threads, size_t smem, cudaStream_t st,
                        A... args) {
@@ -1089,9 +1106,11 @@ moe_status launch_rows(int64_t T, int threads, int sm_threads, size_t smem, cuda
 
 // A CTA of teams: for each, its sums twice and R pieces of all rows of a token
 // (`ring` bytes each), and together at least the norm weight's partial sums.
+// (No CTA waits for another to end: each has its share of the tokens.)
 template <typename P>
 struct TeamShape {
   int threads, teams, r;
+  unsigned grid;
   size_t smem;
   TeamShape(const P &p, size_t ring, int sum_values) : threads(row_threads(p.H)) {
     const size_t sums = (size_t)sum_values * 32 * 2 * 4;
@@ -1101,13 +1120,16 @@ struct TeamShape {
     smem = teams * (sums + r * ring);
     const size_t partial = (size_t)(teams - 1) * p.H * 4;
     if (p.partial && smem < partial) smem = partial;
+    grid = bwd_grid(p.T, p.H);
+    const int64_t fit = (int64_t)(kSmemLimit / (smem + 1024)) * moe_host::sm_count();
+    if (grid > fit) grid = (unsigned)fit;
   }
 };
 template <auto KERNEL, typename P>
 moe_status launch_teams(const P &p, const TeamShape<P> &s, cudaStream_t st) {
   if (moe_status e = allow_smem<KERNEL>(s.smem)) return e;
-  return moe_host::launch_pdl(KERNEL, dim3(bwd_grid(p.T, p.H)), dim3((unsigned)(s.teams * s.threads)),
-                              s.smem, st, p, s.threads);
+  return moe_host::launch_pdl(KERNEL, dim3(s.grid), dim3((unsigned)(s.teams * s.threads)), s.smem, st,
+                              p, s.threads);
 }
 
 bool bad_type(int32_t type) { return type != MOE_F32 && type != MOE_BF16; }
@@ -1129,11 +1151,13 @@ moe_status launch(void (*kernel)(P), unsigned grid, int threads, cudaStream_t st
 
 template <int U, typename X>
 moe_status run_combine_norm(const CombineNormParams &p, cudaStream_t st) {
-  const int n = row_threads(p.H);
+  const int n = threads_of(p.H, U);
   const size_t ring = (size_t)n * 16 * (p.k + Chunk<X>::N + (p.shared ? 1 : 0));
-  if (2 * ring <= kSmemLimit)
-    return launch_rows<combine_norm_kernel<U, 2, X>>(p.T, n, 640, 2 * ring, st, p);
-  return launch_rows<combine_norm_kernel<U, 1, X>>(p.T, n, 640, ring, st, p);
+  if constexpr (U > 1) {
+    if (2 * ring <= kSmemLimit)
+      return launch_rows<combine_norm_kernel<U, 2, X>>(p.T, n, 512, 2 * ring, st, p);
+  }
+  return launch_rows<combine_norm_kernel<U, 1, X>>(p.T, n, U == 1 ? 1024 : 512, ring, st, p);
 }
 
 template <typename X>
@@ -1147,24 +1171,26 @@ moe_status run_combine_bwd(const CombineBwdParams &p, cudaStream_t st) {
 }
 
 template <int KMAX, int U, typename X>
-moe_status run_combine_norm_bwd_k(const CombineBwdParams &p, cudaStream_t st) {
+moe_status run_combine_norm_bwd_k(const CombineBwdParams &p, unsigned &grid, cudaStream_t st) {
   const int n = p.k + Chunk<X>::N + (p.shared ? 1 : 0);
   const TeamShape<CombineBwdParams> s(p, (size_t)row_threads(p.H) * 16 * n, 2 * KMAX + 2);
+  grid = s.grid;
   return s.r == 2 ? launch_teams<combine_norm_bwd_kernel<KMAX, U, 2, X>>(p, s, st)
                   : launch_teams<combine_norm_bwd_kernel<KMAX, U, 1, X>>(p, s, st);
 }
 template <int U, typename X>
-moe_status run_combine_norm_bwd(const CombineBwdParams &p, cudaStream_t st) {
-  if (p.k <= 2) return run_combine_norm_bwd_k<2, U, X>(p, st);
-  if (p.k <= 4) return run_combine_norm_bwd_k<4, U, X>(p, st);
-  if (p.k <= 8) return run_combine_norm_bwd_k<8, U, X>(p, st);
-  return run_combine_norm_bwd_k<16, U, X>(p, st);
+moe_status run_combine_norm_bwd(const CombineBwdParams &p, unsigned &grid, cudaStream_t st) {
+  if (p.k <= 2) return run_combine_norm_bwd_k<2, U, X>(p, grid, st);
+  if (p.k <= 4) return run_combine_norm_bwd_k<4, U, X>(p, grid, st);
+  if (p.k <= 8) return run_combine_norm_bwd_k<8, U, X>(p, grid, st);
+  return run_combine_norm_bwd_k<16, U, X>(p, grid, st);
 }
 
 template <int U, typename X>
-moe_status run_norm_bwd(const NormBwdParams &p, cudaStream_t st) {
+moe_status run_norm_bwd(const NormBwdParams &p, unsigned &grid, cudaStream_t st) {
   const int n = p.k + Chunk<X>::N * (p.rgrad ? 2 : 1) + (p.add ? 1 : 0);
   const TeamShape<NormBwdParams> s(p, (size_t)row_threads(p.H) * 16 * n, 2);
+  grid = s.grid;
   return s.r == 2 ? launch_teams<norm_bwd_kernel<U, 2, X>>(p, s, st)
                   : launch_teams<norm_bwd_kernel<U, 1, X>>(p, s, st);
 }
@@ -1184,9 +1210,9 @@ moe_status run_permute_bwd(const uint16_t *grad, const Rows &rows, const uint16_
 template <int U, typename X>
 moe_status run_norm(const void *x, int64_t T, int32_t H, const float *weight, float eps, uint16_t *out,
                     cudaStream_t st) {
-  const int n = row_threads(H);
+  const int n = threads_of(H, U);
   constexpr int R = 2 * U;
-  return launch_rows<norm_kernel<U, R, X>>(T, n, 1024, (size_t)n * 16 * R * Chunk<X>::N, st,
+  return launch_rows<norm_kernel<U, R, X>>(T, n, U <= 2 ? 1024 : 512, (size_t)n * 16 * R * Chunk<X>::N, st,
                                            static_cast<const X *>(x), T, (int)H, weight, eps,
                                            reinterpret_cast<__nv_bfloat16 *>(out));
 }
@@ -1225,7 +1251,10 @@ extern "C" moe_status moe_norm(const void *x, int32_t x_type, int64_t T, int32_t
   if (T == 0) return MOE_OK;
   if (!x || !out || odd(x) || odd(out) || odd(weight)) return MOE_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (row_chunks(H) == 2)
+  if (fwd_pieces(H) == 1)
+    return x_type == MOE_F32 ? run_norm<1, float>(x, T, H, weight, eps, out, st)
+                             : run_norm<1, __nv_bfloat16>(x, T, H, weight, eps, out, st);
+  if (fwd_pieces(H) == 2)
     return x_type == MOE_F32 ? run_norm<2, float>(x, T, H, weight, eps, out, st)
                              : run_norm<2, __nv_bfloat16>(x, T, H, weight, eps, out, st);
   return x_type == MOE_F32 ? run_norm<4, float>(x, T, H, weight, eps, out, st)
@@ -1264,13 +1293,14 @@ extern "C" moe_status moe_norm_backward(const uint16_t *grad, int64_t n_rows,
   p.gx = grad_x;
   p.partial = grad_weight ? static_cast<float *>(scratch) : nullptr;
   const bool f32 = x_type == MOE_F32;
+  unsigned grid = 0;
   moe_status s;
   if (row_chunks(H) == 2)
-    s = f32 ? run_norm_bwd<2, float>(p, st) : run_norm_bwd<2, __nv_bfloat16>(p, st);
+    s = f32 ? run_norm_bwd<2, float>(p, grid, st) : run_norm_bwd<2, __nv_bfloat16>(p, grid, st);
   else
-    s = f32 ? run_norm_bwd<4, float>(p, st) : run_norm_bwd<4, __nv_bfloat16>(p, st);
+    s = f32 ? run_norm_bwd<4, float>(p, grid, st) : run_norm_bwd<4, __nv_bfloat16>(p, grid, st);
   if (s != MOE_OK || !grad_weight) return s;
-  return sum_partials(p.partial, bwd_grid(T, H), H, grad_weight, st);
+  return sum_partials(p.partial, grid, H, grad_weight, st);
 }
 
 extern "C" moe_status moe_permute_backward(const uint16_t *grad, int64_t n_rows,
@@ -1325,7 +1355,10 @@ extern "C" moe_status moe_combine_norm(const uint16_t *y_perm, int64_t n_rows,
   p.y = y;
   p.next = reinterpret_cast<uint4 *>(next_out);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (row_chunks(H) == 2)
+  if (fwd_pieces(H) == 1)
+    return x_type == MOE_F32 ? run_combine_norm<1, float>(p, st)
+                             : run_combine_norm<1, __nv_bfloat16>(p, st);
+  if (fwd_pieces(H) == 2)
     return x_type == MOE_F32 ? run_combine_norm<2, float>(p, st)
                              : run_combine_norm<2, __nv_bfloat16>(p, st);
   return x_type == MOE_F32 ? run_combine_norm<4, float>(p, st)
@@ -1371,13 +1404,14 @@ extern "C" moe_status moe_combine_norm_backward(
   p.ggate = grad_gate;
   p.partial = grad_weight ? static_cast<float *>(scratch) : nullptr;
   const bool f32 = x_type == MOE_F32;
+  unsigned grid = 0;
   moe_status s;
   if (row_chunks(H) == 2)
-    s = f32 ? run_combine_norm_bwd<2, float>(p, st) : run_combine_norm_bwd<2, __nv_bfloat16>(p, st);
+    s = f32 ? run_combine_norm_bwd<2, float>(p, grid, st) : run_combine_norm_bwd<2, __nv_bfloat16>(p, grid, st);
   else
-    s = f32 ? run_combine_norm_bwd<4, float>(p, st) : run_combine_norm_bwd<4, __nv_bfloat16>(p, st);
+    s = f32 ? run_combine_norm_bwd<4, float>(p, grid, st) : run_combine_norm_bwd<4, __nv_bfloat16>(p, grid, st);
   if (s != MOE_OK || !grad_weight) return s;
-  return sum_partials(p.partial, bwd_grid(T, H), H, grad_weight, st);
+  return sum_partials(p.partial, grid, H, grad_weight, st);
 }
 
 extern "C" moe_status moe_combine_backward(const void *grad_y, int32_t x_type,
