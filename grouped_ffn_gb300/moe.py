@@ -879,7 +879,7 @@ class Int4Weights:
 
     def __init__(self, data: torch.Tensor, E: int, N: int, K: int, group: int, has_zeros: bool, epilogue: int):
         self.data, self.E, self.N, self.K = data, E, N, K
-        self.group, self.has_zeros, self.epilogue = group, has_zeros, epilogue
+        self.group, self.has_zeros, self.epilogue = group, int(has_zeros), epilogue
 
 
 def pack_weights_int4(codes, scales, zeros, epilogue: int, stream=None) -> Int4Weights:
@@ -907,28 +907,20 @@ def pack_weights_int4(codes, scales, zeros, epilogue: int, stream=None) -> Int4W
 def moe_grouped_product_int4(x, seg_offsets, seg_expert, w: Int4Weights, out, ws, stream=None):
     """bf16 rows [n, K] in per-expert segments times the experts' 4-bit weights, with the epilogue
     that w was packed for: out fp32 or bf16 [n, N] (SwiGLU: [n, N/2])."""
-    _bf16(x, "x")
-    _need(seg_offsets, torch.int32, "seg_offsets")
-    _need(seg_expert, torch.int32, "seg_expert")
-    kind = _typed(out, "out")
+    call = "moe_grouped_product_int4"
+    kind = _kind(out, "out")
+    n, K = _rows_of(call, x, "x")
+    _tensors(call, (_BF16T, None, "x", (x,)), (_I32T, None, "seg_offsets seg_expert", (seg_offsets, seg_expert)),
+             (out.dtype, (n, w.N // 2 if w.epilogue == MOE_EPI_SWIGLU else w.N), "out", (out,)))
     S = seg_expert.numel()
-    cols = w.N // 2 if w.epilogue == MOE_EPI_SWIGLU else w.N
-    if x.dim() != 2 or x.shape[1] != w.K or out.shape != (x.shape[0], cols) or seg_offsets.numel() != S + 1:
+    if K != w.K or seg_offsets.numel() != S + 1:
         raise ValueError("moe_grouped_product_int4: inconsistent shapes")
-    _check("moe_grouped_product_int4", lib().moe_grouped_product_int4(
-        _ptr(x), x.shape[0], _ptr(seg_offsets), _ptr(seg_expert), S, w.E, _ptr(w.data), w.N, w.K, w.group,
-        int(w.has_zeros), w.epilogue, _ptr(out), kind, _ptr(ws), ws.numel(), _stream(stream)))
+    _check(call, lib().moe_grouped_product_int4(
+        x.data_ptr(), n, seg_offsets.data_ptr(), seg_expert.data_ptr(), S, w.E, w.data.data_ptr(), w.N, K, w.group,
+        w.has_zeros, w.epilogue, out.data_ptr(), kind, ws.data_ptr(), ws.numel(), _stream(stream)))
 
 
 # ------------------------------------------------------------------ the block around the experts
-def _typed(t: torch.Tensor, name: str) -> int:
-    """The element type code of a contiguous fp32 or bf16 CUDA tensor."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in _TYPES:
-        raise TypeError(f"{name}: expected a contiguous CUDA tensor of float32 or bfloat16")
-    _need(t, t.dtype, name)
-    return _TYPES[t.dtype]
-
-
 def _maybe(t: Optional[torch.Tensor], dtype, shape, name: str, call: str):
     """An optional tensor of a type and shape."""
     if t is not None:
@@ -948,87 +940,93 @@ def new_norm_scratch(T: int, H: int, device=None, stream=None) -> torch.Tensor:
         return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 
 
-def _needs(dtype, names: str, *tensors):
-    """_need for several tensors (None passes): a call each costs a quarter of a microsecond."""
+def _tensors(call: str, *groups):
+    """Checks groups (dtype, shape or None for any, names, tensors) of optional contiguous CUDA
+    tensors; one call for all, since each call costs a tenth of a microsecond."""
     try:
-        for t in tensors:
-            if t is not None and (t.dtype is not dtype or not t.is_cuda or not t.is_contiguous()):
-                raise AttributeError
+        for dtype, shape, _, tensors in groups:
+            for t in tensors:
+                if t is not None:
+                    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+                        raise AttributeError
+                    if shape is not None and t.shape != shape:
+                        raise ValueError(f"{call}: inconsistent shapes")
     except AttributeError:
-        for name, t in zip(names.split(), tensors):
-            if t is not None:
-                _need(t, dtype, name)
+        for dtype, _, names, tensors in groups:
+            for name, t in zip(names.split(), tensors):
+                if t is not None:
+                    _need(t, dtype, name)
         raise
 
 
-def _shapes(call: str, shape, *tensors):
-    """Optional tensors of one shape."""
-    for t in tensors:
-        if t is not None and t.shape != shape:
-            raise ValueError(f"{call}: inconsistent shapes")
+_F32T, _BF16T, _I32T, _U8T = torch.float32, torch.bfloat16, torch.int32, torch.uint8
 
 
-_F32T, _BF16T, _I32T = torch.float32, torch.bfloat16, torch.int32
+def _kind(t, name: str) -> int:
+    """The type code of a tensor of fp32 or bf16 (checked further with its group)."""
+    try:
+        return _TYPES[t.dtype]
+    except (AttributeError, KeyError):
+        raise TypeError(f"{name}: expected a contiguous CUDA tensor of float32 or bfloat16") from None
+
+
+def _rows_of(call: str, t, name: str):
+    """The shape of a matrix."""
+    shape = t.shape if isinstance(t, torch.Tensor) else None
+    if shape is None:
+        raise TypeError(f"{name}: expected a tensor")
+    if len(shape) != 2:
+        raise ValueError(f"{call}: inconsistent shapes")
+    return shape
 
 
 def moe_norm(x, weight, eps: float, out, stream=None):
     """out (bf16 [T, H]) = x / rms(x) * weight; x fp32 or bf16, weight fp32 [H]
     or None."""
-    kind = _typed(x, "x")
-    _needs(_BF16T, "out", out)
-    _needs(_F32T, "weight", weight)
-    shape = x.shape
-    if len(shape) != 2:
-        raise ValueError("moe_norm: inconsistent shapes")
-    T, H = shape
-    _shapes("moe_norm", shape, out)
-    _shapes("moe_norm", (H,), weight)
-    _check("moe_norm", lib().moe_norm(x.data_ptr(), kind, T, H, _ptr(weight), eps, out.data_ptr(),
-                                      _stream(stream)))
-
-
-def _block_shapes(call: str, row, y_perm, dest_row, topk_w):
-    """(T, k, H, n_rows) of a combine: row [T, H], y_perm [n_rows, H], dest_row and topk_w [T, k]
-    (dest_row may also be flat, as the layout writes it)."""
-    shape, rows, w = row.shape, y_perm.shape, topk_w.shape
-    if len(shape) != 2 or len(rows) != 2 or len(w) != 2 or w[0] != shape[0] or rows[1] != shape[1] \
-            or dest_row.numel() != w[0] * w[1]:
-        raise ValueError(f"{call}: inconsistent shapes")
-    return shape[0], w[1], shape[1], rows[0]
+    call = "moe_norm"
+    kind = _kind(x, "x")
+    shape = T, H = _rows_of(call, x, "x")
+    _tensors(call, (x.dtype, None, "x", (x,)), (_BF16T, shape, "out", (out,)), (_F32T, (H,), "weight", (weight,)))
+    _check(call, lib().moe_norm(x.data_ptr(), kind, T, H, None if weight is None else weight.data_ptr(), eps,
+                                out.data_ptr(), _stream(stream)))
 
 
 def moe_combine_norm(y_perm, dest_row, topk_w, residual, cfg: BlockCfg, y, ws, shared=None, weight=None,
                      gate=None, next_weight=None, next_out=None, stream=None):
     """y = residual_scale * residual + gate * norm(shared + weighted sum of the experts' rows), and
     next_out = moe_norm of y.  residual and y fp32 or bf16 [T, H] (y may be residual); weight,
-    next_weight fp32 [H] or None; gate fp32 [T] or None; dest_row -1 is a drop."""
+    next_weight fp32 [H] or None; gate fp32 [T] or None; dest_row -1 is a drop, [T, k] or flat."""
     call = "moe_combine_norm"
-    kind = _typed(residual, "residual")
-    _needs(residual.dtype, "y", y)
-    _needs(_BF16T, "y_perm shared next_out", y_perm, shared, next_out)
-    _needs(_F32T, "topk_w weight gate next_weight", topk_w, weight, gate, next_weight)
-    _needs(_I32T, "dest_row", dest_row)
-    T, k, H, n = _block_shapes(call, residual, y_perm, dest_row, topk_w)
-    _shapes(call, (T, H), y, shared, next_out)
-    _shapes(call, (H,), weight, next_weight)
-    _shapes(call, (T,), gate)
+    kind = _kind(residual, "residual")
+    row = T, H = _rows_of(call, residual, "residual")
+    n, h = _rows_of(call, y_perm, "y_perm")
+    t, k = _rows_of(call, topk_w, "topk_w")
+    _tensors(call, (residual.dtype, row, "residual y", (residual, y)),
+             (_BF16T, None, "y_perm", (y_perm,)), (_BF16T, row, "shared next_out", (shared, next_out)),
+             (_F32T, None, "topk_w", (topk_w,)), (_F32T, (H,), "weight next_weight", (weight, next_weight)),
+             (_F32T, (T,), "gate", (gate,)), (_I32T, None, "dest_row", (dest_row,)))
+    if h != H or t != T or dest_row.numel() != T * k:
+        raise ValueError("moe_combine_norm: inconsistent shapes")
     _check(call, lib().moe_combine_norm(
-        y_perm.data_ptr(), n, dest_row.data_ptr(), topk_w.data_ptr(), T, k, H, _ptr(shared),
-        residual.data_ptr(), kind, _ptr(weight), _ptr(gate), ctypes.byref(cfg), y.data_ptr(),
-        _ptr(next_weight), _ptr(next_out), ws.data_ptr(), ws.numel(), _stream(stream)))
+        y_perm.data_ptr(), n, dest_row.data_ptr(), topk_w.data_ptr(), T, k, H,
+        None if shared is None else shared.data_ptr(), residual.data_ptr(), kind,
+        None if weight is None else weight.data_ptr(), None if gate is None else gate.data_ptr(),
+        ctypes.byref(cfg), y.data_ptr(), None if next_weight is None else next_weight.data_ptr(),
+        None if next_out is None else next_out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
 
 
 def moe_combine_backward(grad_y, y_perm, dest_row, topk_w, grad_y_perm, grad_topk_w, ws, stream=None):
     """Gradients of moe_combine's expert rows and weights for grad_y (fp32 or bf16 [T, H]); rows of
     grad_y_perm that no assignment lands on are left as they are."""
     call = "moe_combine_backward"
-    kind = _typed(grad_y, "grad_y")
-    _needs(_BF16T, "y_perm grad_y_perm", y_perm, grad_y_perm)
-    _needs(_F32T, "topk_w grad_topk_w", topk_w, grad_topk_w)
-    _needs(_I32T, "dest_row", dest_row)
-    T, k, H, n = _block_shapes(call, grad_y, y_perm, dest_row, topk_w)
-    _shapes(call, (n, H), grad_y_perm)
-    _shapes(call, (T, k), grad_topk_w)
+    kind = _kind(grad_y, "grad_y")
+    T, H = _rows_of(call, grad_y, "grad_y")
+    rows = n, h = _rows_of(call, y_perm, "y_perm")
+    w = t, k = _rows_of(call, topk_w, "topk_w")
+    _tensors(call, (grad_y.dtype, None, "grad_y", (grad_y,)), (_BF16T, rows, "y_perm grad_y_perm", (y_perm, grad_y_perm)),
+             (_F32T, w, "topk_w grad_topk_w", (topk_w, grad_topk_w)), (_I32T, None, "dest_row", (dest_row,)))
+    if h != H or t != T or dest_row.numel() != T * k:
+        raise ValueError("moe_combine_backward: inconsistent shapes")
     _check(call, lib().moe_combine_backward(
         grad_y.data_ptr(), kind, y_perm.data_ptr(), n, dest_row.data_ptr(), topk_w.data_ptr(), T, k, H,
         grad_y_perm.data_ptr(), grad_topk_w.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
@@ -1038,23 +1036,17 @@ def moe_permute_backward(grad, dest_row, grad_x, ws, add=None, stream=None):
     """grad_x (fp32 or bf16 [T, H]) = add + the sum of grad (bf16 [n_rows, H]) over each token's
     rows; dest_row int32 [T, k]."""
     call = "moe_permute_backward"
-    kind = _typed(grad_x, "grad_x")
-    _needs(_BF16T, "grad add", grad, add)
-    _needs(_I32T, "dest_row", dest_row)
-    shape, rows, d = grad_x.shape, grad.shape, dest_row.shape
-    if len(shape) != 2 or len(rows) != 2 or len(d) != 2 or d[0] != shape[0] or rows[1] != shape[1]:
+    kind = _kind(grad_x, "grad_x")
+    row = T, H = _rows_of(call, grad_x, "grad_x")
+    n, h = _rows_of(call, grad, "grad")
+    t, k = _rows_of(call, dest_row, "dest_row")
+    _tensors(call, (grad_x.dtype, None, "grad_x", (grad_x,)), (_BF16T, None, "grad", (grad,)),
+             (_BF16T, row, "add", (add,)), (_I32T, None, "dest_row", (dest_row,)))
+    if h != H or t != T:
         raise ValueError("moe_permute_backward: inconsistent shapes")
-    _shapes(call, shape, add)
     _check(call, lib().moe_permute_backward(
-        grad.data_ptr(), rows[0], dest_row.data_ptr(), _ptr(add), shape[0], d[1], shape[1],
+        grad.data_ptr(), n, dest_row.data_ptr(), None if add is None else add.data_ptr(), T, k, H,
         grad_x.data_ptr(), kind, ws.data_ptr(), ws.numel(), _stream(stream)))
-
-
-def _scratch(scratch):
-    if scratch is None:
-        return None, 0
-    _need(scratch, torch.uint8, "scratch")
-    return scratch.data_ptr(), scratch.numel()
 
 
 def moe_combine_norm_backward(grad_y, y_perm, dest_row, topk_w, cfg: BlockCfg, grad_y_perm, grad_topk_w,
@@ -1063,21 +1055,26 @@ def moe_combine_norm_backward(grad_y, y_perm, dest_row, topk_w, cfg: BlockCfg, g
     """Gradients of moe_combine_norm's expert rows, weights, shared rows, norm weight and gate for
     grad_y; the last three are written where a tensor is given (grad_weight needs scratch)."""
     call = "moe_combine_norm_backward"
-    kind = _typed(grad_y, "grad_y")
-    _needs(_BF16T, "y_perm grad_y_perm shared grad_shared", y_perm, grad_y_perm, shared, grad_shared)
-    _needs(_F32T, "topk_w grad_topk_w weight gate grad_weight grad_gate", topk_w, grad_topk_w, weight, gate,
-           grad_weight, grad_gate)
-    _needs(_I32T, "dest_row", dest_row)
-    T, k, H, n = _block_shapes(call, grad_y, y_perm, dest_row, topk_w)
-    _shapes(call, (n, H), grad_y_perm)
-    _shapes(call, (T, k), grad_topk_w)
-    _shapes(call, (T, H), shared, grad_shared)
-    _shapes(call, (H,), weight, grad_weight)
-    _shapes(call, (T,), gate, grad_gate)
+    kind = _kind(grad_y, "grad_y")
+    row = T, H = _rows_of(call, grad_y, "grad_y")
+    rows = n, h = _rows_of(call, y_perm, "y_perm")
+    w = t, k = _rows_of(call, topk_w, "topk_w")
+    _tensors(call, (grad_y.dtype, None, "grad_y", (grad_y,)), (_BF16T, rows, "y_perm grad_y_perm", (y_perm, grad_y_perm)),
+             (_BF16T, row, "shared grad_shared", (shared, grad_shared)),
+             (_F32T, w, "topk_w grad_topk_w", (topk_w, grad_topk_w)),
+             (_F32T, (H,), "weight grad_weight", (weight, grad_weight)),
+             (_F32T, (T,), "gate grad_gate", (gate, grad_gate)), (_I32T, None, "dest_row", (dest_row,)),
+             (_U8T, None, "scratch", (scratch,)))
+    if h != H or t != T or dest_row.numel() != T * k:
+        raise ValueError("moe_combine_norm_backward: inconsistent shapes")
     _check(call, lib().moe_combine_norm_backward(
         grad_y.data_ptr(), kind, y_perm.data_ptr(), n, dest_row.data_ptr(), topk_w.data_ptr(), T, k, H,
-        _ptr(shared), _ptr(weight), _ptr(gate), ctypes.byref(cfg), grad_y_perm.data_ptr(),
-        grad_topk_w.data_ptr(), _ptr(grad_shared), _ptr(grad_weight), _ptr(grad_gate), *_scratch(scratch),
+        None if shared is None else shared.data_ptr(), None if weight is None else weight.data_ptr(),
+        None if gate is None else gate.data_ptr(), ctypes.byref(cfg), grad_y_perm.data_ptr(),
+        grad_topk_w.data_ptr(), None if grad_shared is None else grad_shared.data_ptr(),
+        None if grad_weight is None else grad_weight.data_ptr(),
+        None if grad_gate is None else grad_gate.data_ptr(),
+        None if scratch is None else scratch.data_ptr(), 0 if scratch is None else scratch.numel(),
         ws.data_ptr(), ws.numel(), _stream(stream)))
 
 
@@ -1087,27 +1084,24 @@ def moe_norm_backward(grad, x, weight, eps: float, grad_x, grad_weight, ws, scra
     add + grad (bf16 [T, H]), or with dest_row (int32 [T, k]) for add + the sum of each token's rows
     of grad (bf16 [n_rows, H]).  grad_weight fp32 [H] (with scratch) or None."""
     call = "moe_norm_backward"
-    kind = _typed(x, "x")
-    _needs(x.dtype, "grad_x residual_grad", grad_x, residual_grad)
-    _needs(_BF16T, "grad add", grad, add)
-    _needs(_F32T, "weight grad_weight", weight, grad_weight)
-    shape, rows, k = x.shape, grad.shape, 0
-    if len(shape) != 2 or len(rows) != 2 or rows[1] != shape[1]:
+    kind = _kind(x, "x")
+    row = T, H = _rows_of(call, x, "x")
+    n, h = _rows_of(call, grad, "grad")
+    t, k = (n, 0) if dest_row is None else _rows_of(call, dest_row, "dest_row")
+    _tensors(call, (x.dtype, row, "x grad_x residual_grad", (x, grad_x, residual_grad)),
+             (_BF16T, None, "grad", (grad,)), (_BF16T, row, "add", (add,)),
+             (_F32T, (H,), "weight grad_weight", (weight, grad_weight)), (_I32T, None, "dest_row", (dest_row,)),
+             (_U8T, None, "scratch", (scratch,)))
+    if h != H or t != T:
         raise ValueError("moe_norm_backward: inconsistent shapes")
-    T, H = shape
-    if dest_row is not None:
-        _needs(_I32T, "dest_row", dest_row)
-        if dest_row.dim() != 2 or dest_row.shape[0] != T:
-            raise ValueError("moe_norm_backward: inconsistent shapes")
-        k = dest_row.shape[1]
-    elif rows[0] != T:
-        raise ValueError("moe_norm_backward: inconsistent shapes")
-    _shapes(call, shape, grad_x, add, residual_grad)
-    _shapes(call, (H,), weight, grad_weight)
     _check(call, lib().moe_norm_backward(
-        grad.data_ptr(), rows[0], _ptr(dest_row), k, _ptr(add), x.data_ptr(), kind, T, H, _ptr(weight),
-        eps, _ptr(residual_grad), residual_scale, grad_x.data_ptr(), _ptr(grad_weight),
-        *_scratch(scratch), ws.data_ptr(), ws.numel(), _stream(stream)))
+        grad.data_ptr(), n, None if dest_row is None else dest_row.data_ptr(), k,
+        None if add is None else add.data_ptr(), x.data_ptr(), kind, T, H,
+        None if weight is None else weight.data_ptr(), eps,
+        None if residual_grad is None else residual_grad.data_ptr(), residual_scale, grad_x.data_ptr(),
+        None if grad_weight is None else grad_weight.data_ptr(),
+        None if scratch is None else scratch.data_ptr(), 0 if scratch is None else scratch.numel(),
+        ws.data_ptr(), ws.numel(), _stream(stream)))
 
 
 def moe_status_string(status: int) -> str:
