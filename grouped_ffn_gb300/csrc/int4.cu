@@ -47,58 +47,62 @@ __device__ __forceinline__ int weight_row(int nb, int r, int N, int swiglu) {
   return j < N / 2 ? j + (r & 8 ? N / 2 : 0) : -1;
 }
 
-// Codes, scales and zeros to the packed steps; a thread writes 16 bytes of
-// codes, or one scale and zero.  Within a lane's 16 bytes (lane = 4 g + p) word
-// 2 h + s holds K = 64 half + 32 h + 8 p + 4 s + {0, 1, 2, 3} of rows g and
-// g + 8, nibbles in the order (g, 0) (g + 8, 0) (g, 2) (g + 8, 2) and the same
-// of the odd elements: the four operands are nibble i of each 16-bit half.
+// Codes, scales and zeros to the packed steps.  A CTA takes a block of weight rows
+// and walks along K, two steps at a time; a thread writes 16 bytes of codes, then
+// its share of the scales and zeros.  Within a lane's 16 bytes (lane = 4 g + p)
+// word 2 h + s holds K = 64 half + 32 h + 8 p + 4 s + {0, 1, 2, 3} of rows g and
+// g + 8, nibbles in the order (g, 0) (g + 8, 0) (g, 2) (g + 8, 2) and the same of
+// the odd elements: the four operands are nibble i of each 16-bit half.
 __global__ void __launch_bounds__(kPackThreads)
     pack_int4_kernel(const uint8_t *__restrict__ codes, const uint16_t *__restrict__ scales,
-                     const uint8_t *__restrict__ zeros, int64_t n_steps, int N, int K, int ng,
-                     int nbn, int nst, int swiglu, uint8_t *__restrict__ packed) {
-  const int units = kStepCodes / 16, sunits = kBlockRows * ng;
-  const int64_t total = n_steps * (units + sunits);
+                     const uint8_t *__restrict__ zeros, int N, int K, int ng, int nbn, int nst,
+                     int swiglu, uint8_t *__restrict__ packed) {
+  constexpr int kUnits = kStepCodes / 16, kSteps = kPackThreads / kUnits;
   const int bytes = step_bytes(ng, zeros != nullptr);
   const int groups = K / (kStepK / ng);  // of a row
-  for (int64_t i = (int64_t)blockIdx.x * kPackThreads + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * kPackThreads) {
-    const int64_t step = i / (units + sunits);
-    int u = (int)(i - step * (units + sunits));
-    const int st = (int)(step % nst), nb = (int)(step / nst % nbn);
-    const int64_t e = step / nst / nbn;
-    uint8_t *out = packed + step * bytes;
-    if (u < units) {
-      const int m = u >> 6, half = u >> 5 & 1, lane = u & 31, g = lane >> 2, p = lane & 3;
-      uint32_t w[4] = {0, 0, 0, 0};
+  const int64_t e = blockIdx.x / nbn;
+  const int nb = (int)(blockIdx.x - e * nbn);
+  uint8_t *out = packed + (int64_t)blockIdx.x * nst * bytes;
+  const int u = threadIdx.x % kUnits, s0 = threadIdx.x / kUnits;
+  const int m = u >> 6, half = u >> 5 & 1, lane = u & 31, g = lane >> 2, p = lane & 3;
+  const uint8_t *src[2];
+  bool row_ok[2];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {  // rows g and g + 8
-        const int row = weight_row(nb, m * 16 + g + 8 * b, N, swiglu);
+  for (int b = 0; b < 2; ++b) {  // rows g and g + 8
+    const int row = weight_row(nb, m * 16 + g + 8 * b, N, swiglu);
+    row_ok[b] = row >= 0;
+    src[b] = codes + (e * N + max(row, 0)) * (int64_t)(K / 2);
+  }
+  for (int st = s0; st < nst; st += kSteps) {
+    uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int k = st * kStepK + half * 64 + h * 32 + p * 8;
-          if (row < 0 || k >= K) continue;
-          const uint32_t v = __ldg(reinterpret_cast<const uint32_t *>(
-              codes + (e * N + row) * (int64_t)(K / 2) + k / 2));
+    for (int b = 0; b < 2; ++b)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {  // element k + j
-            const uint32_t q = v >> (4 * j) & 15u;
-            const int nibble = (j >> 1 & 1) * 2 + b + (j & 1) * 4;
-            w[2 * h + (j >> 2)] |= q << (4 * nibble);
-          }
+      for (int h = 0; h < 2; ++h) {
+        const int k = st * kStepK + half * 64 + h * 32 + p * 8;
+        if (!row_ok[b] || k >= K) continue;
+        const uint32_t v = __ldg(reinterpret_cast<const uint32_t *>(src[b] + k / 2));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {  // element k + j
+          const uint32_t q = v >> (4 * j) & 15u;
+          const int nibble = (j >> 1 & 1) * 2 + b + (j & 1) * 4;
+          w[2 * h + (j >> 2)] |= q << (4 * nibble);
         }
       }
-      *reinterpret_cast<uint4 *>(out + u * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      u -= units;
-      // [g][tile][group][row g or g + 8]
-      const int b = u & 1, gi = u / 2 % ng, m = u / 2 / ng & 1, g = u / 4 / ng;
-      const int row = weight_row(nb, m * 16 + g + 8 * b, N, swiglu);
-      const int grp = st * ng + gi;
-      const bool ok = row >= 0 && grp < groups;
-      const int64_t at = (e * N + row) * (int64_t)groups + grp;
-      reinterpret_cast<uint16_t *>(out + kStepCodes)[u] = ok ? scales[at] : 0;
-      if (zeros) out[kStepCodes + scale_bytes(ng) + u] = ok ? zeros[at] & 127u : 0;
-    }
+    *reinterpret_cast<uint4 *>(out + (int64_t)st * bytes + u * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  const int sunits = kBlockRows * ng;
+  for (int64_t i = threadIdx.x; i < (int64_t)nst * sunits; i += kPackThreads) {
+    const int st = (int)(i / sunits), v = (int)(i - (int64_t)st * sunits);
+    // [g][tile][group][row g or g + 8]
+    const int b = v & 1, gi = v / 2 % ng, tile = v / 2 / ng & 1, gr = v / 4 / ng;
+    const int row = weight_row(nb, tile * 16 + gr + 8 * b, N, swiglu);
+    const int grp = st * ng + gi;
+    const bool ok = row >= 0 && grp < groups;
+    const int64_t at = (e * N + row) * (int64_t)groups + grp;
+    uint8_t *o = out + (int64_t)st * bytes + kStepCodes;
+    reinterpret_cast<uint16_t *>(o)[v] = ok ? scales[at] : 0;
+    if (zeros) o[scale_bytes(ng) + v] = ok ? zeros[at] & 127u : 0;
   }
 }
 
@@ -485,7 +489,9 @@ moe_status check_weights(int32_t E, int32_t N, int32_t K, int32_t group, int32_t
   if (E < 1 || N < 1 || K < 1) return MOE_ERR_INVALID_ARG;
   if (group != 32 && group != 64 && group != 128) return MOE_ERR_INVALID_ARG;
   if (epilogue != MOE_EPI_NONE && epilogue != MOE_EPI_SWIGLU) return MOE_ERR_INVALID_ARG;
-  if (K % group != 0 || K > (1 << 24) || N % (epilogue == MOE_EPI_SWIGLU ? 16 : 8) != 0)
+  const bool swi = epilogue == MOE_EPI_SWIGLU;
+  if (K % group != 0 || K > (1 << 24) || N % (swi ? 16 : 8) != 0 ||
+      (int64_t)E * blocks_of(N, swi) >= (int64_t)1 << 31)
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -542,10 +548,9 @@ extern "C" moe_status moe_pack_weights_int4(const uint8_t *codes, const uint16_t
       (reinterpret_cast<uintptr_t>(scales) & 1u))
     return MOE_ERR_INVALID_ARG;
   const bool swi = epilogue == MOE_EPI_SWIGLU;
-  pack_int4_kernel<<<(unsigned)moe_host::sm_count() * 16, kPackThreads, 0,
+  pack_int4_kernel<<<(unsigned)((int64_t)E * blocks_of(N, swi)), kPackThreads, 0,
                      static_cast<cudaStream_t>(stream)>>>(
-      codes, scales, zeros, all_steps(E, N, K, epilogue), N, K, kStepK / group, blocks_of(N, swi),
-      steps_of(K), swi, packed);
+      codes, scales, zeros, N, K, kStepK / group, blocks_of(N, swi), steps_of(K), swi, packed);
   return moe_host::launch_status();
 }
 

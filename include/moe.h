@@ -716,7 +716,8 @@ moe_status moe_grouped_product_fp4(const uint8_t *codes, const uint8_t *sf, int6
  * the product's: with MOE_EPI_SWIGLU rows 0..N/2-1 of an expert are gate, the
  * others up.  packed: device, moe_int4_packed_bytes bytes (0 for invalid
  * arguments), not overlapping the inputs; codes and packed 16-byte aligned.
- * Limits: K % group == 0, K <= 2^24, N % 8 == 0 (SwiGLU: N % 16 == 0). */
+ * Limits: K % group == 0, K <= 2^24, N % 8 == 0 (SwiGLU: N % 16 == 0), E times N / 32
+ * (rounded up) < 2^31. */
 size_t moe_int4_packed_bytes(int32_t E, int32_t N, int32_t K, int32_t group, int32_t has_zeros,
                              int32_t epilogue);
 moe_status moe_pack_weights_int4(const uint8_t *codes, const uint16_t *scales,
