@@ -211,18 +211,37 @@ __device__ __forceinline__ void warp_sums(float (&v)[N], int lane) {
   for (int s = 16 / N; s > 0; s >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], s);
 }
 
-// A warp's sums to buf[value][warp], and a value's total from there: every
-// warp adds the same numbers in the same order, so all threads agree.
+// A warp's sums to buf[value][warp], and a value's total from there, warps that are
+// not there counting zero (clear_sums): all threads add the same numbers in the
+// same order.  (A team has at most 16 warps; lines of 20 floats let lanes read 16
+// bytes of lines of their own without bank conflicts.)
+constexpr int kLine = 20;
+// Floats of n values' lines, whole 128-byte lines: a warp's 512 bytes of a ring after
+// them then lie in four (not aligned, 4096 x 7168 with eight experts took 114 us
+// instead of 109).
+__host__ __device__ constexpr int sums_floats(int n) { return (n * kLine + 31) / 32 * 32; }
 template <int N>
 __device__ __forceinline__ void put_sums(float (&v)[N], float *buf, int warp, int lane) {
   warp_sums(v, lane);
-  if (lane % (32 / N) == 0) buf[lane / (32 / N) * 32 + warp] = v[0];
+  if (lane % (32 / N) == 0) buf[lane / (32 / N) * kLine + warp] = v[0];
 }
-__device__ __forceinline__ float total(const float *buf, int value, int nw, int lane) {
-  float x = lane < nw ? buf[value * 32 + lane] : 0.0f;
+// of up to eight warps
+__device__ __forceinline__ float total_few(const float *buf, int value) {
+  const float4 *b = reinterpret_cast<const float4 *>(buf + value * kLine);
+  const float4 v = b[0], w = b[1];
+  return ((v.x + v.y) + (v.z + v.w)) + ((w.x + w.y) + (w.z + w.w));
+}
+__device__ __forceinline__ float total_many(const float *buf, int value, int nw, int lane) {
+  float x = lane < nw ? buf[value * kLine + lane] : 0.0f;
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
   return x;
+}
+__device__ __forceinline__ float total(const float *buf, int value, int nw, int lane) {
+  return nw <= 8 ? total_few(buf, value) : total_many(buf, value, nw, lane);
+}
+__device__ __forceinline__ void clear_sums(float *buf, int n, int tid, int threads) {
+  for (int i = tid; i < n; i += threads) buf[i] = 0.0f;
 }
 
 // (rsqrtf is within two units of its last place)
@@ -278,7 +297,8 @@ __device__ __forceinline__ Norm row_norm(Pair (&x)[U][4], float inv_h, float eps
     float v[1] = {sum(s)};
     put_sums(v, buf, tm.warp, tm.lane);
     tm.sync();
-    return total(buf, 0, tm.nw, tm.lane);
+    // (a team of one piece a thread has at most four warps)
+    return U == 1 ? total_few(buf, 0) : total_many(buf, 0, tm.nw, tm.lane);
   };
   float s = squares();
   Norm n{1.0f, 0.0f};
@@ -359,13 +379,17 @@ template <int U, int R, typename X>
 __global__ void __launch_bounds__(kRowThreads, U <= 2 ? 2 : 1)
     norm_kernel(const X *x, int64_t T, int H, const float *__restrict__ weight, float eps,
                 __nv_bfloat16 *out) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float buf[2][32];
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(16) float buf[2][kLine];
   const Team<true> tm((int)blockDim.x);
   const int H8 = H / 8, slot = tm.threads * 16 * Chunk<X>::N;
   const float inv_h = 1.0f / (float)H;
   uint8_t *mine = smem + tm.warp * 512 * Chunk<X>::N;  // the warp's places
   const uint32_t dst = smem_u32(mine);
+  if constexpr (U == 1) {
+    clear_sums(buf[0], 2 * kLine, tm.tid, tm.threads);
+    __syncthreads();
+  }
   moe::pdl_wait();
   moe::pdl_trigger();
   auto fetch = [&](int64_t t, int u, int at) {
@@ -423,8 +447,8 @@ struct CombineNormParams {
 template <int U, int R, typename X>
 __global__ void __launch_bounds__(kRowThreads, U == 1 ? 2 : 1)
     combine_norm_kernel(const CombineNormParams p) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float buf[2][2][32];
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(16) float buf[2][2][kLine];
   const Team<true> tm((int)blockDim.x);
   const int H8 = p.H / 8, step = tm.threads * 16;
   const float inv_h = 1.0f / (float)p.H;
@@ -433,6 +457,10 @@ __global__ void __launch_bounds__(kRowThreads, U == 1 ? 2 : 1)
   uint8_t *mine = smem + tm.tid * 16;
   const uint32_t dst = smem_u32(mine);
   const int warp_res = at_res + (tm.warp * Chunk<X>::N * 32 - tm.tid) * 16;  // from `mine`
+  if constexpr (U == 1) {
+    clear_sums(buf[0][0], 4 * kLine, tm.tid, tm.threads);
+    __syncthreads();
+  }
   moe::pdl_wait();
   moe::pdl_trigger();
   auto meta = [&](int64_t t) {
@@ -546,10 +574,12 @@ struct CombineBwdParams {
 // waits for the sums, so the row streams through in chunks.
 template <int KMAX, typename X>
 __global__ void __launch_bounds__(128) combine_bwd_kernel(const CombineBwdParams p) {
-  __shared__ float buf[2][KMAX * 32];
+  __shared__ __align__(16) float buf[2][KMAX * kLine];
+  clear_sums(buf[0], 2 * KMAX * kLine, threadIdx.x, blockDim.x);
+  __syncthreads();
   moe::pdl_wait();
   moe::pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5, H8 = p.H / 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, H8 = p.H / 8;
   int par = 0;
   for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, par ^= 1) {
     int32_t r[KMAX];
@@ -582,10 +612,7 @@ __global__ void __launch_bounds__(128) combine_bwd_kernel(const CombineBwdParams
     }
     put_sums(sums, buf[par], warp, lane);
     __syncthreads();
-    for (int j = warp; j < p.k; j += nw) {
-      const float d = total(buf[par], j, nw, lane);
-      if (lane == 0) p.gw[t * p.k + j] = d;
-    }
+    if ((int)threadIdx.x < p.k) p.gw[t * p.k + threadIdx.x] = total_few(buf[par], threadIdx.x);
   }
 }
 
@@ -637,8 +664,8 @@ template <int KMAX, int U, int R, typename X>
 __global__ void __launch_bounds__(kRowThreads)
     combine_norm_bwd_kernel(const CombineBwdParams p, const int team_threads) {
   constexpr int kSums = 2 * KMAX;
-  constexpr int kBuf = (kSums + 2) * 32;
-  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int kBuf = sums_floats(kSums + 2);
+  extern __shared__ __align__(128) uint8_t smem[];
   const Team<false> tm(team_threads);
   const int teams = blockDim.x / team_threads;
   const int H8 = p.H / 8, step = tm.threads * 16;
@@ -650,6 +677,8 @@ __global__ void __launch_bounds__(kRowThreads)
   uint8_t *mine = rings + tm.index * R * slot + tm.tid * 16;
   const uint32_t dst = smem_u32(mine);
   const int warp_gy = at_gy + (tm.warp * Chunk<X>::N * 32 - tm.tid) * 16;  // from `mine`
+  clear_sums(buf, 2 * kBuf, tm.tid, tm.threads);
+  __syncthreads();
   moe::pdl_wait();
   moe::pdl_trigger();
   auto meta = [&](int64_t t) {
@@ -726,7 +755,7 @@ __global__ void __launch_bounds__(kRowThreads)
     }
     float *b = buf + par * kBuf;
     put_sums(d, b, tm.warp, tm.lane);
-    put_sums(s, b + kSums * 32, tm.warp, tm.lane);
+    put_sums(s, b + kSums * kLine, tm.warp, tm.lane);
     tm.sync();
     const float g = now.g;
     float s1 = total(b, kSums, tm.nw, tm.lane), s2 = total(b, kSums + 1, tm.nw, tm.lane);
@@ -768,7 +797,7 @@ __global__ void __launch_bounds__(kRowThreads)
         }
         tm.sync();
         put_sums(d, b, tm.warp, tm.lane);
-        put_sums(s, b + kSums * 32, tm.warp, tm.lane);
+        put_sums(s, b + kSums * kLine, tm.warp, tm.lane);
         tm.sync();
         s1 = total(b, kSums, tm.nw, tm.lane);
         s2 = total(b, kSums + 1, tm.nw, tm.lane);
@@ -831,8 +860,8 @@ struct NormBwdParams {
 template <int U, int R, typename X>
 __global__ void __launch_bounds__(kRowThreads)
     norm_bwd_kernel(const NormBwdParams p, const int team_threads) {
-  constexpr int kBuf = 2 * 32;
-  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int kBuf = sums_floats(2);
+  extern __shared__ __align__(128) uint8_t smem[];
   const Team<false> tm(team_threads);
   const int teams = blockDim.x / team_threads;
   const int H8 = p.H / 8, step = tm.threads * 16;
@@ -845,6 +874,8 @@ __global__ void __launch_bounds__(kRowThreads)
   uint8_t *mine = rings + tm.index * R * slot + tm.tid * 16;
   const uint32_t dst = smem_u32(mine);
   const int warp_at = (tm.warp * Chunk<X>::N * 32 - tm.tid) * 16;  // the warp's places, from `mine`
+  clear_sums(buf, 2 * kBuf, tm.tid, tm.threads);
+  __syncthreads();
   moe::pdl_wait();
   moe::pdl_trigger();
   auto meta = [&](int64_t t) {
@@ -1113,7 +1144,7 @@ struct TeamShape {
   unsigned grid;
   size_t smem;
   TeamShape(const P &p, size_t ring, int sum_values) : threads(row_threads(p.H)) {
-    const size_t sums = (size_t)sum_values * 32 * 2 * 4;
+    const size_t sums = (size_t)sums_floats(sum_values) * 2 * 4;
     teams = bwd_teams(p.H);
     while (teams > 1 && teams * (sums + 2 * ring) > kSmemLimit) --teams;
     r = teams * (sums + 2 * ring) <= kSmemLimit ? 2 : 1;
