@@ -13,7 +13,7 @@
 // in shared memory (cp.async, no barrier), and as soon as it has used a piece it
 // asks for the next token's: the reads go on while a token's sums meet and its
 // results are written.  With plain loads into registers instead, 4096 tokens of
-// 7168 with eight rows each, shared expert and next norm took 165 us.
+// 7168 with eight rows each, shared expert and next norm took 165 us; now 108 us.
 #include <cuda_bf16.h>
 #include <float.h>
 #include <math.h>
@@ -374,7 +374,8 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, int step, const uint4 *r
   }
 }
 
-// out = x / rms(x) * weight.  R / U tokens are on their way.
+// out = x / rms(x) * weight.  R / U tokens are on their way.  Bound by HBM: 16384
+// rows of 4096 in fp32 59 us, 6.8 TB/s; 4096 rows of 1024 in bf16 4.6 us.
 template <int U, int R, typename X>
 __global__ void __launch_bounds__(kRowThreads, U <= 2 ? 2 : 1)
     norm_kernel(const X *x, int64_t T, int H, const float *__restrict__ weight, float eps,
@@ -444,6 +445,9 @@ struct CombineNormParams {
 
 // c = shared + sum_j w_j Y[row_j], y = scale x + gate norm(c), next = norm(y).
 // One CTA a token at a time; c and then y stay in registers across the two sums.
+// Bound by HBM where there are rows enough: 4096 tokens of 7168, eight experts, a
+// shared one and next norm 108 us, 6.5 TB/s; 16384 of 4096 in fp32, four experts,
+// 163 us, 6.6 TB/s.  A single token takes 4.2 us in a graph, most of it the launch.
 template <int U, int R, typename X>
 __global__ void __launch_bounds__(kRowThreads, U == 1 ? 2 : 1)
     combine_norm_kernel(const CombineNormParams p) {
@@ -571,7 +575,8 @@ struct CombineBwdParams {
 };
 
 // y = sum_j w_j Y[row_j]: dY[row_j] = w_j dy, dw_j = dy . Y[row_j].  Nothing
-// waits for the sums, so the row streams through in chunks.
+// waits for the sums, so the row streams through in chunks.  Bound by HBM: 4096
+// tokens of 7168, eight experts, 148 us, 6.7 TB/s.
 template <int KMAX, typename X>
 __global__ void __launch_bounds__(128) combine_bwd_kernel(const CombineBwdParams p) {
   __shared__ __align__(16) float buf[2][KMAX * kLine];
@@ -659,7 +664,10 @@ __device__ __forceinline__ void put_partial(const Pair (&pw)[U][4], float *parti
 // once and need not be kept:
 //   dc = gate r (e - c m),  m = r^2 mean(e c),  dw_j = gate r (e . Y_j - m c . Y_j).
 // The weight's gradient is kept per thread over the CTA's tokens and added up
-// by sum_partials_kernel in a fixed order.
+// by sum_partials_kernel in a fixed order.  16384 tokens of 4096 in fp32, four
+// experts: 245 us, 5.5 TB/s; 4096 of 1440, six experts: 49 us, 3.6 TB/s.  Bound by
+// issue at 16 warps an SM (128 registers; at 80 they spill, 434 us): leaving out one
+// of the two dots, the weight's gradient or the stores saves a tenth each.
 template <int KMAX, int U, int R, typename X>
 __global__ void __launch_bounds__(kRowThreads)
     combine_norm_bwd_kernel(const CombineBwdParams p, const int team_threads) {
@@ -857,6 +865,7 @@ struct NormBwdParams {
 
 // u = add + the sum of the copies' gradients (or grad's own row), e = u weight:
 //   gx = scale rgrad + r (e - x r^2 mean(e x)),  weight's gradient sum_t u x r.
+// 16384 rows of 4096 in fp32, four copies each: 245 us, 6.0 TB/s.
 template <int U, int R, typename X>
 __global__ void __launch_bounds__(kRowThreads)
     norm_bwd_kernel(const NormBwdParams p, const int team_threads) {
@@ -1000,7 +1009,8 @@ __global__ void __launch_bounds__(kRowThreads)
   if (p.partial) put_partial(pw, p.partial, p.H, teams, reinterpret_cast<float *>(smem), tm);
 }
 
-// grad_x[t] = add[t] + sum_j grad[row_j].
+// grad_x[t] = add[t] + sum_j grad[row_j].  Bound by HBM: 4096 tokens of 7168, eight
+// copies each, 84 us, 7.0 TB/s (results still in L2).
 template <int KMAX, typename X>
 __global__ void __launch_bounds__(128)
     permute_bwd_kernel(const uint4 *__restrict__ grad, Rows rows, const uint4 *__restrict__ add,
