@@ -342,9 +342,16 @@ __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm)
   const int total = pre[p.S] * p.nbn;  // below 2^31 by the host's check
 
   // Task t: a segment's tasks follow one another, a block's row tiles together.
-  // Tasks are asked for in ascending order; s is the last one's segment.
+  // Tasks are asked for in ascending order; s is the last one's segment.  (Most
+  // segments may be empty: the next one is found by halves.)
   auto decode = [&](int t, int &s) {
-    while ((int64_t)pre[s + 1] * p.nbn <= t) ++s;
+    if (pre[s + 1] * p.nbn <= t) {
+      int hi = p.S;  // the last segment that begins at t or before
+      for (++s; hi - s > 1;) {
+        const int mid = (s + hi) >> 1;
+        if (pre[mid] * p.nbn <= t) s = mid; else hi = mid;
+      }
+    }
     const int tiles = pre[s + 1] - pre[s], local = t - pre[s] * p.nbn;
     const int nb = tiles == 1 ? local : local / tiles, rt = local - nb * tiles;
     Task k;

@@ -75,6 +75,8 @@ CASES = [  # rows per segment, first row, E, N, K, group, zeros, swiglu
     ((1,) * 300, 0, 7, 16, 64, 32, False, False),
     ((2, 1), 0, 2, 72, 8192, 128, False, False),
     ((7,), 1, 3, 1000, 192, 64, True, False),
+    # most segments empty, none of them first or last alone
+    ((0,) * 500 + (3,) + (0,) * 100 + (1, 2) + (0,) * 400 + (9,) + (0,) * 20, 0, 9, 144, 128, 32, False, True),
 ]
 
 
