@@ -273,19 +273,24 @@ __device__ __forceinline__ void step_products(const uint8_t *st, int g, int lane
   }
 }
 
-// log2 of the warps that split a task's K: those for which the slowest warp has least to do,
-// counting a task's end as 2.5 steps; the larger of almost equal ones (within
-// 5%), whose tasks spread better.  128 rows over 64 experts, 8192 -> 2 x 2048: 1, 2,
-// 4, 8 warps 201, 197, 188, 220 us; 8 rows over 8 experts, 7168 -> 2 x 2048: 55,
-// 33, 35, 38 us; 512 rows over 256 experts, 2048 -> 7168: 360, 385, 437, 750 us.
+// log2 of the warps that split a task's K: those for which the slowest warp has
+// least to do, a task's end counting as a step; where warps have eight tasks and
+// more of 16 steps at least, the larger of almost equal ones (within 5%), whose tasks
+// spread better.
+// With 1, 2, 4, 8 warps: 128 rows over 64 experts, 8192 -> 2 x 2048, 191, 189, 183,
+// 202 us; 8 rows over 8 experts, 7168 -> 2 x 2048, 51, 30, 32, 34 us; 512 rows over
+// 256 experts, 2048 -> 7168, 363, 403, 479, 654 us; 333 rows over 5 experts, 1440 ->
+// 712, 20.6, 13.4, 9.4, 11.5 us.
 __device__ __forceinline__ int team_log(int total, int steps, int warps) {
   int best = 0;
   float least = 0.0f;
 #pragma unroll
   for (int l = 0; 1 << l <= kWarps; ++l) {
     const float turns = ceilf((float)total * (float)(1 << l) / (float)warps);
-    const float cost = turns * ((float)((steps + (1 << l) - 1) >> l) + 2.5f);
-    if (l == 0 || cost <= 1.05f * least) best = l;
+    const float cost = turns * ((float)((steps + (1 << l) - 1) >> l) + 1.0f);
+    if (l == 0 || cost < least ||
+        (turns >= 8.0f && steps >> l >= 16 && cost <= 1.05f * least))
+      best = l;
     if (l == 0 || cost < least) least = cost;
   }
   return best;
@@ -300,9 +305,9 @@ __device__ __forceinline__ int team_log(int total, int steps, int warps) {
 // the product does not reach the others, and is not stored.
 // Bound by the expansion of the codes (of 289 instructions for 2 KB of them 112 are
 // shifts and and-ors, 64 subtractions, at 64 lanes a clock each), then by HBM: 128
-// rows over 64 experts, 8192 -> 2 x 2048, 194 us, 4.8 TB/s; 512 rows over 256
-// experts, 2048 -> 7168, 362 us, 5.2 TB/s; one token's eight rows over eight experts,
-// 7168 -> 2 x 2048, 32 us, 3.8 TB/s; without the shifts (wrong results) 166, 297, 27.
+// rows over 64 experts, 8192 -> 2 x 2048, 184 us, 5.1 TB/s; 512 rows over 256
+// experts, 2048 -> 7168, 363 us, 5.1 TB/s; one token's eight rows over eight experts,
+// 7168 -> 2 x 2048, 30 us, 4.1 TB/s.
 template <int NT, int NG, bool ZEROS>
 __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm)
     int4_product_kernel(const Params p) {
