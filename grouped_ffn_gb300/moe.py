@@ -894,6 +894,7 @@ def pack_weights_int4(codes, scales, zeros, epilogue: int, stream=None) -> Int4W
     if group * scales.shape[2] != K:
         raise ValueError("pack_weights_int4: inconsistent shapes")
     _maybe(zeros, torch.uint8, scales.shape, "zeros", "pack_weights_int4")
+    _on_current("pack_weights_int4", codes)
     has = zeros is not None
     n = int(lib().moe_int4_packed_bytes(E, N, K, group, int(has), epilogue))
     # allocated on the stream that writes it, see pack_weights_fp4
@@ -940,9 +941,15 @@ def new_norm_scratch(T: int, H: int, device=None, stream=None) -> torch.Tensor:
         return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 
 
+def _on_current(call: str, t):
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{call}: tensors of another device than the current one")
+
+
 def _tensors(call: str, *groups):
     """Checks groups (dtype, shape or None for any, names, tensors) of optional contiguous CUDA
-    tensors; one call for all, since each call costs a tenth of a microsecond."""
+    tensors, the first one's device against the current one; one call for all, since each call
+    costs a tenth of a microsecond."""
     try:
         for dtype, shape, _, tensors in groups:
             for t in tensors:
@@ -957,6 +964,7 @@ def _tensors(call: str, *groups):
                 if t is not None:
                     _need(t, dtype, name)
         raise
+    _on_current(call, groups[0][3][0])
 
 
 _F32T, _BF16T, _I32T, _U8T = torch.float32, torch.bfloat16, torch.int32, torch.uint8

@@ -583,6 +583,32 @@ def test_no_expert_rows_at_all():
 
 
 @pytest.mark.gpu
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """Calls launch on the current device (here it is said to be another one than the tensors')."""
+    m = moe()
+    s = inputs(3, 64, 2, BF, False, False, True, 0, seed=12)
+    ws, sc = m.new_workspace(3, 2, 1), m.new_norm_scratch(3, 64)
+    y, gw = torch.empty_like(s["x"]), torch.empty_like(s["w"])
+    codes, scales = torch.zeros(1, 8, 16, dtype=torch.uint8, device="cuda"), torch.ones(1, 8, 1, device="cuda").to(BF)
+    w = m.pack_weights_int4(codes, scales, None, m.MOE_EPI_NONE)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    x4, o4, off, exp = torch.zeros(1, 32, device="cuda").to(BF), torch.zeros(1, 8, device="cuda"), i32(0, 1), i32(0)
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    for f in (lambda: m.moe_norm(s["x"], None, EPS, y),
+              lambda: m.moe_combine_norm(s["yp"], s["dest"], s["w"], s["x"], m.BlockCfg(), y, ws),
+              lambda: m.moe_combine_backward(s["gy"], s["yp"], s["dest"], s["w"], torch.empty_like(s["yp"]), gw, ws),
+              lambda: m.moe_permute_backward(s["grad"], s["dest"], y, ws),
+              lambda: m.moe_combine_norm_backward(s["gy"], s["yp"], s["dest"], s["w"], m.BlockCfg(),
+                                                  torch.empty_like(s["yp"]), gw, ws, sc),
+              lambda: m.moe_norm_backward(s["grad"], s["x"], None, EPS, y, None, ws, sc, dest_row=s["dest"]),
+              lambda: m.pack_weights_int4(codes, scales, None, m.MOE_EPI_NONE),
+              lambda: m.moe_grouped_product_int4(x4, off, exp, w, o4, ws)):
+        with pytest.raises(ValueError, match="device"):
+            f()
+
+
+@pytest.mark.gpu
 def test_calls_on_two_streams_at_once():
     m = moe()
     qs = [inputs(400, 2048, 4, BF, True, True, True, 0.1, seed=20 + i) for i in range(2)]
