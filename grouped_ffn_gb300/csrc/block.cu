@@ -18,18 +18,13 @@
 #include <float.h>
 #include <math.h>
 
+#include "block_shape.cuh"
 #include "common.cuh"
 
 namespace {
 
-// A token's team has up to 512 threads, each with U pieces of 8 elements: two for
-// rows of up to 8192, four beyond; in the forward pass one for rows of up to 1024,
-// with 64 registers and twice the threads an SM (4096 tokens of 1024, six experts,
-// combine with norms: 13.4 us against 16 with two pieces).
-// R of the U pieces have a place in shared memory.
-constexpr int kRowThreads = 512;
-constexpr int kMaxH = kRowThreads * 4 * 8;
-constexpr int kSmemLimit = 225 * 1024;
+using namespace block_shape;
+
 constexpr float kShrink = 0x1p-70f;
 
 struct Rows {
@@ -213,13 +208,7 @@ __device__ __forceinline__ void warp_sums(float (&v)[N], int lane) {
 
 // A warp's sums to buf[value][warp], and a value's total from there, warps that are
 // not there counting zero (clear_sums): all threads add the same numbers in the
-// same order.  (A team has at most 16 warps; lines of 20 floats let lanes read 16
-// bytes of lines of their own without bank conflicts.)
-constexpr int kLine = 20;
-// Floats of n values' lines, whole 128-byte lines: a warp's 512 bytes of a ring after
-// them then lie in four (not aligned, 4096 x 7168 with eight experts took 114 us
-// instead of 109).
-__host__ __device__ constexpr int sums_floats(int n) { return (n * kLine + 31) / 32 * 32; }
+// same order.
 template <int N>
 __device__ __forceinline__ void put_sums(float (&v)[N], float *buf, int warp, int lane) {
   warp_sums(v, lane);
@@ -1077,39 +1066,6 @@ __global__ void __launch_bounds__(kSumThreads)
 }
 
 // ------------------------------------------------------------------ host
-// Threads of the streaming kernels: at most 128, and such that their turns over a
-// row are full (H = 1416: 96 in two turns instead of 128 of which half the second
-// turn's idle).
-int stream_threads(int H) {
-  const int pieces = H / 8, turns = (pieces + 127) / 128;
-  return ((pieces + turns - 1) / turns + 31) / 32 * 32;
-}
-
-int row_chunks(int H) { return H <= kRowThreads * 2 * 8 ? 2 : 4; }
-int fwd_pieces(int H) { return H <= 1024 ? 1 : row_chunks(H); }
-int threads_of(int H, int u) { return ((H / 8 + u - 1) / u + 31) / 32 * 32; }
-int row_threads(int H) { return threads_of(H, row_chunks(H)); }
-
-// CTAs of the streaming kernels, at most 32 an SM.
-unsigned stream_grid(int64_t T) {
-  const int64_t cap = (int64_t)moe_host::sm_count() * 32;
-  return (unsigned)(T < cap ? T : cap);
-}
-
-// Teams of a CTA of the gradients: what 512 threads hold, at most 8.
-int bwd_teams(int H) {
-  const int n = kRowThreads / row_threads(H);
-  return n < 1 ? 1 : n > 8 ? 8 : n;
-}
-// and the most CTAs that they run: 512 threads an SM with up to 128 registers (the
-// norm weights' gradients have as many partial rows).
-unsigned bwd_grid(int64_t T, int H) {
-  const int teams = bwd_teams(H);
-  const int64_t cap = (int64_t)moe_host::sm_count() * (kRowThreads / (teams * row_threads(H)));
-  const int64_t need = (T + teams - 1) / teams;
-  return (unsigned)(need < cap ? need : cap);
-}
-
 // Dynamic shared memory that with the static passes 48 KB, asked for once a
 // kernel and device.
 template <auto KERNEL>
@@ -1128,46 +1084,16 @@ moe_status allow_smem(size_t bytes) {
   return MOE_OK;
 }
 
-// One CTA a token at a time: as many CTAs an SM as shared memory and `sm_threads`
-// threads allow (512 with up to 128 registers).  All run at once, each with its
-// share of the tokens.
 template <auto KERNEL, typename... A>
 moe_status launch_rows(int64_t T, int threads, int sm_threads, size_t smem, cudaStream_t st,
                        A... args) {
   if (moe_status s = allow_smem<KERNEL>(smem)) return s;
-  int64_t per_sm = (int64_t)(kSmemLimit / (smem + 1280));
-  if (per_sm > sm_threads / threads) per_sm = sm_threads / threads;
-  if (per_sm > 30) per_sm = 30;
-  if (per_sm < 1) per_sm = 1;
-  int64_t grid = per_sm * moe_host::sm_count();
-  if (grid > T) grid = T;
-  return moe_host::launch_pdl(KERNEL, dim3((unsigned)grid), dim3((unsigned)threads), smem, st,
-                              args...);
+  const unsigned grid = rows_grid(T, threads, sm_threads, smem, moe_host::sm_count());
+  return moe_host::launch_pdl(KERNEL, dim3(grid), dim3((unsigned)threads), smem, st, args...);
 }
 
-// A CTA of teams: for each, its sums twice and R pieces of all rows of a token
-// (`ring` bytes each), and together at least the norm weight's partial sums.
-// (No CTA waits for another to end: each has its share of the tokens.)
-template <typename P>
-struct TeamShape {
-  int threads, teams, r;
-  unsigned grid;
-  size_t smem;
-  TeamShape(const P &p, size_t ring, int sum_values) : threads(row_threads(p.H)) {
-    const size_t sums = (size_t)sums_floats(sum_values) * 2 * 4;
-    teams = bwd_teams(p.H);
-    while (teams > 1 && teams * (sums + 2 * ring) > kSmemLimit) --teams;
-    r = teams * (sums + 2 * ring) <= kSmemLimit ? 2 : 1;
-    smem = teams * (sums + r * ring);
-    const size_t partial = (size_t)(teams - 1) * p.H * 4;
-    if (p.partial && smem < partial) smem = partial;
-    grid = bwd_grid(p.T, p.H);
-    const int64_t fit = (int64_t)(kSmemLimit / (smem + 1024)) * moe_host::sm_count();
-    if (grid > fit) grid = (unsigned)fit;
-  }
-};
 template <auto KERNEL, typename P>
-moe_status launch_teams(const P &p, const TeamShape<P> &s, cudaStream_t st) {
+moe_status launch_teams(const P &p, const TeamShape &s, cudaStream_t st) {
   if (moe_status e = allow_smem<KERNEL>(s.smem)) return e;
   return moe_host::launch_pdl(KERNEL, dim3(s.grid), dim3((unsigned)(s.teams * s.threads)), s.smem, st,
                               p, s.threads);
@@ -1203,7 +1129,7 @@ moe_status run_combine_norm(const CombineNormParams &p, cudaStream_t st) {
 
 template <typename X>
 moe_status run_combine_bwd(const CombineBwdParams &p, cudaStream_t st) {
-  const unsigned g = stream_grid(p.T);
+  const unsigned g = stream_grid(p.T, moe_host::sm_count());
   const int n = stream_threads(p.H);
   if (p.k <= 2) return launch(combine_bwd_kernel<2, X>, g, n, st, p);
   if (p.k <= 4) return launch(combine_bwd_kernel<4, X>, g, n, st, p);
@@ -1214,7 +1140,7 @@ moe_status run_combine_bwd(const CombineBwdParams &p, cudaStream_t st) {
 template <int KMAX, int U, typename X>
 moe_status run_combine_norm_bwd_k(const CombineBwdParams &p, unsigned &grid, cudaStream_t st) {
   const int n = p.k + Chunk<X>::N + (p.shared ? 1 : 0);
-  const TeamShape<CombineBwdParams> s(p, (size_t)row_threads(p.H) * 16 * n, 2 * KMAX + 2);
+  const TeamShape s(p.T, p.H, n, 2 * KMAX + 2, p.partial != nullptr, moe_host::sm_count());
   grid = s.grid;
   return s.r == 2 ? launch_teams<combine_norm_bwd_kernel<KMAX, U, 2, X>>(p, s, st)
                   : launch_teams<combine_norm_bwd_kernel<KMAX, U, 1, X>>(p, s, st);
@@ -1230,7 +1156,7 @@ moe_status run_combine_norm_bwd(const CombineBwdParams &p, unsigned &grid, cudaS
 template <int U, typename X>
 moe_status run_norm_bwd(const NormBwdParams &p, unsigned &grid, cudaStream_t st) {
   const int n = p.k + Chunk<X>::N * (p.rgrad ? 2 : 1) + (p.add ? 1 : 0);
-  const TeamShape<NormBwdParams> s(p, (size_t)row_threads(p.H) * 16 * n, 2);
+  const TeamShape s(p.T, p.H, n, 2, p.partial != nullptr, moe_host::sm_count());
   grid = s.grid;
   return s.r == 2 ? launch_teams<norm_bwd_kernel<U, 2, X>>(p, s, st)
                   : launch_teams<norm_bwd_kernel<U, 1, X>>(p, s, st);
@@ -1239,7 +1165,7 @@ moe_status run_norm_bwd(const NormBwdParams &p, unsigned &grid, cudaStream_t st)
 template <typename X>
 moe_status run_permute_bwd(const uint16_t *grad, const Rows &rows, const uint16_t *add, int64_t T,
                            int32_t k, int32_t H, void *gx, cudaStream_t st) {
-  const dim3 g(stream_grid(T)), b((unsigned)stream_threads(H));
+  const dim3 g(stream_grid(T, moe_host::sm_count())), b((unsigned)stream_threads(H));
   const uint4 *in = reinterpret_cast<const uint4 *>(grad), *ad = reinterpret_cast<const uint4 *>(add);
   X *out = static_cast<X *>(gx);
   if (k <= 2) return moe_host::launch_pdl(permute_bwd_kernel<2, X>, g, b, 0, st, in, rows, ad, T, k, H, out);
@@ -1282,7 +1208,7 @@ moe_status zero_gradient(float *grad_weight, int32_t H, cudaStream_t st) {
 
 extern "C" size_t moe_norm_scratch_bytes(int64_t T, int32_t H) {
   if (T < 1 || H < 8 || H % 8 != 0 || H > kMaxH) return 0;
-  return (size_t)bwd_grid(T, H) * (size_t)H * 4;
+  return (size_t)bwd_grid(T, H, moe_host::sm_count()) * (size_t)H * 4;
 }
 
 extern "C" moe_status moe_norm(const void *x, int32_t x_type, int64_t T, int32_t H,
