@@ -1074,10 +1074,10 @@ moe_status allow_smem(size_t bytes) {
   static bool done[kMaxDevices] = {false};
   if (bytes <= 40 * 1024) return MOE_OK;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+  if (moe_host::refused(cudaGetDevice(&dev))) return MOE_ERR_CUDA;
   if (dev < 0 || dev >= kMaxDevices || !done[dev]) {
-    if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) !=
-        cudaSuccess)
+    if (moe_host::refused(cudaFuncSetAttribute(
+            KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit)))
       return MOE_ERR_CUDA;
     if (dev >= 0 && dev < kMaxDevices) done[dev] = true;
   }
@@ -1201,7 +1201,7 @@ moe_status check_scratch(const float *grad_weight, int64_t T, int32_t H, void *s
 }
 moe_status zero_gradient(float *grad_weight, int32_t H, cudaStream_t st) {
   if (!grad_weight) return MOE_OK;
-  return cudaMemsetAsync(grad_weight, 0, (size_t)H * 4, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return moe_host::refused(cudaMemsetAsync(grad_weight, 0, (size_t)H * 4, st)) ? MOE_ERR_CUDA : MOE_OK;
 }
 
 }  // namespace

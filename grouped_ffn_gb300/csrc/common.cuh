@@ -101,6 +101,14 @@ inline int32_t *status_ptr(void *ws) { return reinterpret_cast<int32_t *>(ws); }
 // Number of SMs of the current device (cached per device id).
 int sm_count();
 
+// Whether the runtime refused a call.  The error is taken from the thread's last error
+// too: the next launch would be reported as failed otherwise.
+inline bool refused(cudaError_t e) {
+  if (e == cudaSuccess) return false;
+  cudaGetLastError();
+  return true;
+}
+
 // Maps the last CUDA launch error to a status.
 inline moe_status launch_status() {
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
@@ -122,8 +130,7 @@ inline moe_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, si
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return MOE_ERR_CUDA;
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return refused(cudaLaunchKernelEx(&cfg, kernel, args...)) ? MOE_ERR_CUDA : MOE_OK;
 }
 
 // Cooperative launch (every CTA resident at once, so CTAs may wait for one
@@ -143,8 +150,7 @@ inline moe_status launch_coop_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 bloc
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return MOE_ERR_CUDA;
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return refused(cudaLaunchKernelEx(&cfg, kernel, args...)) ? MOE_ERR_CUDA : MOE_OK;
 }
 
 inline moe_status check_ws(void *ws, size_t ws_bytes, size_t need) {

@@ -523,11 +523,11 @@ moe_status launch(const Params &p, cudaStream_t st) {
   constexpr int kMaxDevices = 64;
   static bool done[kMaxDevices] = {false};
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+  if (moe_host::refused(cudaGetDevice(&dev))) return MOE_ERR_CUDA;
   if (dev < 0 || dev >= kMaxDevices || !done[dev]) {
-    if (cudaFuncSetAttribute(int4_product_kernel<NT, NG, ZEROS>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)C::smem(kMaxSegs)) != cudaSuccess)
+    if (moe_host::refused(cudaFuncSetAttribute(int4_product_kernel<NT, NG, ZEROS>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)C::smem(kMaxSegs))))
       return MOE_ERR_CUDA;
     if (dev >= 0 && dev < kMaxDevices) done[dev] = true;
   }
