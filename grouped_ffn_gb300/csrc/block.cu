@@ -25,7 +25,9 @@ namespace {
 
 using namespace block_shape;
 
-constexpr float kShrink = 0x1p-70f;
+// Rows whose squares pass fp32's range are brought down by this first: 16384 squares
+// of (2^128 2^-72) add up to 2^126, and the row's largest element is still above 2^-15.
+constexpr float kShrink = 0x1p-72f;
 
 struct Rows {
   const int32_t *dest_row;
@@ -269,7 +271,7 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p) {
 }
 
 // The sum of squares of a row held in registers and 1 / its root mean square.
-// Where the squares pass fp32's range, the row is brought down by 2^-70 first
+// Where the squares pass fp32's range, the row is brought down by 2^-72 first
 // (eps vanishes next to such a row): rows of any finite values have a norm.
 struct Norm {
   float pre, r;  // the row's factor, and 1 / rms of the row times it
@@ -760,7 +762,7 @@ __global__ void __launch_bounds__(kRowThreads)
     if (p.post) {
       float eps = p.eps;
       if (!(s1 <= FLT_MAX)) {
-        // squares beyond fp32's range: the same sums with c and Y_j times 2^-70
+        // squares beyond fp32's range: the same sums with c and Y_j times 2^-72
         const Pair shrink = both(kShrink);
         pre = kShrink;
         eps = 0.0f;
