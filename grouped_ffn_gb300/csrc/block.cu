@@ -271,8 +271,8 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p) {
 }
 
 // The sum of squares of a row held in registers and 1 / its root mean square.
-// Where the squares pass fp32's range, the row is brought down by 2^-72 first
-// (eps vanishes next to such a row): rows of any finite values have a norm.
+// Where the squares pass fp32's range, the row is brought down by 2^-72 first and eps
+// by 2^-144: rows of any finite values have a norm.
 struct Norm {
   float pre, r;  // the row's factor, and 1 / rms of the row times it
 };
@@ -301,7 +301,7 @@ __device__ __forceinline__ Norm row_norm(Pair (&x)[U][4], float inv_h, float eps
       for (int i = 0; i < 4; ++i) x[u][i] = mul(x[u][i], both(kShrink));
     tm.sync();
     s = squares();
-    eps = 0.0f;
+    eps *= kShrink * kShrink;
   }
   n.r = inv_rms(s, inv_h, eps);
   return n;
@@ -765,7 +765,7 @@ __global__ void __launch_bounds__(kRowThreads)
         // squares beyond fp32's range: the same sums with c and Y_j times 2^-72
         const Pair shrink = both(kShrink);
         pre = kShrink;
-        eps = 0.0f;
+        eps *= kShrink * kShrink;
         s[0] = s[1] = 0.0f;
 #pragma unroll
         for (int j = 0; j < kSums; ++j) d[j] = 0.0f;
@@ -952,7 +952,7 @@ __global__ void __launch_bounds__(kRowThreads)
     float pre = 1.0f, eps = p.eps;
     if (!(s1 <= FLT_MAX)) {  // as in row_norm
       pre = kShrink;
-      eps = 0.0f;
+      eps *= kShrink * kShrink;
       s[0] = s[1] = 0.0f;
 #pragma unroll
       for (int u = 0; u < U; ++u) {

@@ -77,3 +77,17 @@ def test_largest_rows(H, dt):
     near(y, *Block(s, T, H, True, 1.0).forward(), "y")
     near(nx, *Norm(f64(y)).out(f64(s["next_weight"])), "next")
     check_after(s)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_large_eps_beside_large_rows(dt):
+    """eps counts next to squares that pass the range as it does next to others."""
+    m = moe()
+    H, eps = 8, 1e38
+    x = (1e19 * signs(3, H)).to(dt)
+    out = torch.empty(3, H, dtype=BF, device="cuda")
+    m.moe_norm(x, None, eps, out)
+    v = f64(x)
+    want = v / np.sqrt((v * v).mean(1, keepdims=True) + eps)
+    near(out, want, (SUM + OPS) * np.abs(want), "norm")
