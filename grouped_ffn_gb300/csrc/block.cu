@@ -803,9 +803,16 @@ __global__ void __launch_bounds__(kRowThreads)
       }
       rc = inv_rms(s1, inv_h, eps);
       m = rc * rc * (s2 * inv_h);
+    } else {
+      // dc = gate gy does not depend on c, which may be infinite or NaN
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[u][i] = 0;
     }
     for (int j = tm.warp; j < p.k; j += tm.nw) {
-      const float ey = total(b, j, tm.nw, tm.lane), cy = total(b, KMAX + j, tm.nw, tm.lane);
+      const float ey = total(b, j, tm.nw, tm.lane);
+      const float cy = p.post ? total(b, KMAX + j, tm.nw, tm.lane) : 0.0f;
       if (tm.lane == j) p.gw[t * p.k + j] = now.row < 0 ? 0.0f : g * rc * (ey - m * cy);
     }
     if (p.ggate && tm.tid == 0) p.ggate[t] = s2 * rc;

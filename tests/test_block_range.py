@@ -91,3 +91,28 @@ def test_large_eps_beside_large_rows(dt):
     v = f64(x)
     want = v / np.sqrt((v * v).mean(1, keepdims=True) + eps)
     near(out, want, (SUM + OPS) * np.abs(want), "norm")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_no_norm_and_large_rows(dt):
+    """Without a norm the gradients do not depend on the sum c: products with it may pass the range,
+    and c itself may be infinite."""
+    T, H, k = 4, 4096, 3
+    s = inputs(T, H, k, dt, True, True, False, 0, seed=31)
+    r = s["dest"][1].long()
+    s["yp"][r] = (s["yp"][r].float() * 1e18).to(BF)
+    out, ws = backward(s, False)
+    moe().moe_check_device_status(ws)
+    want = Block(s, T, H, False, 1.0).backward()
+    near(out["w"], *want["w"], "w")
+    near(out["rows"][s["dest"].long()], *want["rows"], "rows")
+    near(out["shared"], *want["shared"], "shared")
+    bad = s["dest"][2, 1].long()
+    s["yp"][bad, 9] = float("inf")
+    got, _ = backward(s, False)
+    assert torch.equal(got["rows"][s["landed"]], out["rows"][s["landed"]])
+    assert torch.equal(got["shared"], out["shared"])
+    keep = torch.ones(T, k, dtype=torch.bool)
+    keep[2, 1] = False
+    assert torch.equal(got["w"][keep], out["w"][keep]) and not torch.isfinite(got["w"][2, 1])
