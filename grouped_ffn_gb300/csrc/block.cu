@@ -210,12 +210,14 @@ __device__ __forceinline__ void warp_sums(float (&v)[N], int lane) {
 
 // A warp's sums to buf[value][warp], and a value's total from there, warps that are
 // not there counting zero (clear_sums): all threads add the same numbers in the
-// same order.
+// same order.  v[0] is then a warp's sum, and small() says of it that a total of 16
+// such is within fp32's range (false for NaN).
 template <int N>
 __device__ __forceinline__ void put_sums(float (&v)[N], float *buf, int warp, int lane) {
   warp_sums(v, lane);
   if (lane % (32 / N) == 0) buf[lane / (32 / N) * kLine + warp] = v[0];
 }
+__device__ __forceinline__ bool small(float warp_sum) { return fabsf(warp_sum) <= FLT_MAX / 32.0f; }
 // of up to eight warps
 __device__ __forceinline__ float total_few(const float *buf, int value) {
   const float4 *b = reinterpret_cast<const float4 *>(buf + value * kLine);
@@ -258,6 +260,16 @@ struct Team {
       __syncthreads();
     else
       asm volatile("bar.sync %0, %1;" ::"r"(1 + index), "r"(threads) : "memory");
+  }
+  // the barrier, and whether any thread came with true
+  __device__ __forceinline__ bool any(bool mine) const {
+    int r;
+    asm volatile(
+        "{ .reg .pred p, q; setp.ne.s32 p, %3, 0; bar.red.or.pred q, %1, %2, p; selp.s32 %0, 1, 0, q; }"
+        : "=r"(r)
+        : "r"(1 + index), "r"(threads), "r"((int)mine)
+        : "memory");
+    return r;
   }
 };
 
@@ -755,67 +767,110 @@ __global__ void __launch_bounds__(kRowThreads)
     float *b = buf + par * kBuf;
     put_sums(d, b, tm.warp, tm.lane);
     put_sums(s, b + kSums * kLine, tm.warp, tm.lane);
-    tm.sync();
+    const bool wide = tm.any(!(small(d[0]) && small(s[0])));
     const float g = now.g;
     float s1 = total(b, kSums, tm.nw, tm.lane), s2 = total(b, kSums + 1, tm.nw, tm.lane);
     float pre = 1.0f, rc = 1.0f, m = 0.0f;
-    if (p.post) {
-      float eps = p.eps;
-      if (!(s1 <= FLT_MAX)) {
-        // squares beyond fp32's range: the same sums with c and Y_j times 2^-72
-        const Pair shrink = both(kShrink);
-        pre = kShrink;
-        eps *= kShrink * kShrink;
+    float hat, ec;  // c / rms(c) is acc * hat; the sum of e with it
+    if (!wide) {
+      if (p.post) {
+        rc = inv_rms(s1, inv_h, p.eps);
+        m = rc * rc * (s2 * inv_h);
+      }
+      hat = rc;
+      ec = s2 * rc;
+      for (int j = tm.warp; j < p.k; j += tm.nw) {
+        const float ey = total(b, j, tm.nw, tm.lane), cy = total(b, KMAX + j, tm.nw, tm.lane);
+        if (tm.lane == j) p.gw[t * p.k + j] = now.row < 0 ? 0.0f : g * rc * (ey - m * cy);
+      }
+    } else {
+      // A sum is not within fp32's range: of c^2, e c, or products with rows far larger
+      // than c.  c is brought to rms 1 first, after which e's mean with it is no larger
+      // than e, and dw_j comes from a pass over o = e - c mean(e c) and Y_j, with Y_j as
+      // it is and times 2^-72.  Without the norm c takes no part, and may be infinite or
+      // NaN.  (Rare, but here and not in a function that is called, whose conventions
+      // cost the other tokens registers: 16384 x 4096, four experts, 457 us.)
+      ec = s2;
+      if (p.post) {
+        float eps = p.eps;
+        auto sum_again = [&]() {
+          tm.sync();
+          put_sums(s, b + kSums * kLine, tm.warp, tm.lane);
+          tm.sync();
+        };
         s[0] = s[1] = 0.0f;
+        if (!(s1 <= FLT_MAX)) {
+          pre = kShrink;
+          eps *= kShrink * kShrink;
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[u][i] = mul(acc[u][i], both(kShrink));
+            s[0] += dot(acc[u], acc[u]);
+          }
+          sum_again();
+          s1 = total(b, kSums, tm.nw, tm.lane);
+        }
+        rc = inv_rms(s1, inv_h, eps);
+        s[0] = 0.0f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          Pair e[4], f[4];
+          load_weight(p.weight, min(tm.tid + u * tm.threads, H8 - 1), f);
+          gin[u].get(e);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            acc[u][i] = mul(acc[u][i], both(rc));
+            e[i] = mul(e[i], f[i]);
+            f[i] = mul(acc[u][i], both(inv_h));
+          }
+          s[0] += dot(e, f);
+        }
+        sum_again();
+        m = total(b, kSums, tm.nw, tm.lane);
+        ec = m * (float)p.H;
 #pragma unroll
         for (int j = 0; j < kSums; ++j) d[j] = 0.0f;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int c = tm.tid + u * tm.threads;
-          Pair e[4], f[4];
+          Pair o[4], f[4];
           load_weight(p.weight, min(c, H8 - 1), f);
-          gin[u].get(e);
+          gin[u].get(o);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            e[i] = mul(e[i], f[i]);
-            acc[u][i] = mul(acc[u][i], shrink);
-          }
-          s[0] += dot(acc[u], acc[u]);
-          s[1] += dot(e, acc[u]);
+          for (int i = 0; i < 4; ++i) o[i] = fma(both(-m), acc[u][i], mul(o[i], f[i]));
 #pragma unroll
           for (int j = 0; j < KMAX; ++j) {
             const int32_t r = __shfl_sync(0xffffffffu, now.row, j);
             if (c < H8 && r >= 0) {
               unpack(moe::ld_stream_u4(p.yp + (int64_t)r * H8 + c), f);
+              d[j] += dot(o, f);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) f[i] = mul(f[i], shrink);
-              d[j] += dot(e, f);
-              d[KMAX + j] += dot(acc[u], f);
+              for (int i = 0; i < 4; ++i) f[i] = mul(f[i], both(kShrink));
+              d[KMAX + j] += dot(o, f);
             }
           }
         }
-        tm.sync();
         put_sums(d, b, tm.warp, tm.lane);
-        put_sums(s, b + kSums * kLine, tm.warp, tm.lane);
         tm.sync();
-        s1 = total(b, kSums, tm.nw, tm.lane);
-        s2 = total(b, kSums + 1, tm.nw, tm.lane);
+        for (int j = tm.warp; j < p.k; j += tm.nw) {
+          const float y = total(b, j, tm.nw, tm.lane), less = total(b, KMAX + j, tm.nw, tm.lane);
+          const float dw = fabsf(y) <= FLT_MAX ? g * rc * y * pre : g * rc * less * (pre / kShrink);
+          if (tm.lane == j) p.gw[t * p.k + j] = now.row < 0 ? 0.0f : dw;
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[u][i] = 0;
+        for (int j = tm.warp; j < p.k; j += tm.nw) {
+          const float ey = total(b, j, tm.nw, tm.lane);
+          if (tm.lane == j) p.gw[t * p.k + j] = now.row < 0 ? 0.0f : g * ey;
+        }
       }
-      rc = inv_rms(s1, inv_h, eps);
-      m = rc * rc * (s2 * inv_h);
-    } else {
-      // dc = gate gy does not depend on c, which may be infinite or NaN
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[u][i] = 0;
+      hat = 1.0f;
     }
-    for (int j = tm.warp; j < p.k; j += tm.nw) {
-      const float ey = total(b, j, tm.nw, tm.lane);
-      const float cy = p.post ? total(b, KMAX + j, tm.nw, tm.lane) : 0.0f;
-      if (tm.lane == j) p.gw[t * p.k + j] = now.row < 0 ? 0.0f : g * rc * (ey - m * cy);
-    }
-    if (p.ggate && tm.tid == 0) p.ggate[t] = s2 * rc;
+    if (p.ggate && tm.tid == 0) p.ggate[t] = ec;
     const Pair a = both(g * rc * pre), minus_m = both(-m);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -827,7 +882,7 @@ __global__ void __launch_bounds__(kRowThreads)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (p.partial)
-          pw[u][i] = fma(mul(both(g), gy[i]), mul(acc[u][i], both(rc)), pw[u][i]);
+          pw[u][i] = fma(mul(both(g), gy[i]), mul(acc[u][i], both(hat)), pw[u][i]);
         gy[i] = mul(a, fma(minus_m, acc[u][i], mul(gy[i], o[i])));
       }
       if (in && p.gshared) p.gshared[t * H8 + c] = pack(gy);
@@ -954,33 +1009,53 @@ __global__ void __launch_bounds__(kRowThreads)
     }
     float *b = buf + par * kBuf;
     put_sums(s, b, tm.warp, tm.lane);
-    tm.sync();
-    float s1 = total(b, 0, tm.nw, tm.lane), s2 = total(b, 1, tm.nw, tm.lane);
-    float pre = 1.0f, eps = p.eps;
-    if (!(s1 <= FLT_MAX)) {  // as in row_norm
-      pre = kShrink;
-      eps *= kShrink * kShrink;
+    const bool wide = tm.any(!small(s[0]));
+    float s1 = total(b, 0, tm.nw, tm.lane);
+    const float s2 = total(b, 1, tm.nw, tm.lane);
+    float pre = 1.0f, rc, m, hat;
+    if (!wide) {
+      rc = hat = inv_rms(s1, inv_h, p.eps);
+      m = rc * rc * (s2 * inv_h);
+    } else {
+      // sums beyond fp32's range: x is brought to rms 1 first, and e's mean with it is
+      // no larger than e
+      float eps = p.eps;
+      auto sum_again = [&]() {
+        tm.sync();
+        put_sums(s, b, tm.warp, tm.lane);
+        tm.sync();
+        return total(b, 0, tm.nw, tm.lane);
+      };
       s[0] = s[1] = 0.0f;
+      if (!(s1 <= FLT_MAX)) {  // as in row_norm
+        pre = kShrink;
+        eps *= kShrink * kShrink;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[u][i] = mul(x[u][i], both(kShrink));
+          s[0] += dot(x[u], x[u]);
+        }
+        s1 = sum_again();
+      }
+      rc = inv_rms(s1, inv_h, eps);
+      s[0] = 0.0f;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        Pair e[4];
+        Pair e[4], f[4];
         load_weight(p.weight, min(tm.tid + u * tm.threads, H8 - 1), e);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          x[u][i] = mul(x[u][i], both(kShrink));
+          x[u][i] = mul(x[u][i], both(rc));
           e[i] = mul(acc[u][i], e[i]);
+          f[i] = mul(x[u][i], both(inv_h));
         }
-        s[0] += dot(x[u], x[u]);
-        s[1] += dot(e, x[u]);
+        s[0] += dot(e, f);
       }
-      tm.sync();
-      put_sums(s, b, tm.warp, tm.lane);
-      tm.sync();
-      s1 = total(b, 0, tm.nw, tm.lane);
-      s2 = total(b, 1, tm.nw, tm.lane);
+      m = sum_again();
+      hat = 1.0f;
     }
-    const float rc = inv_rms(s1, inv_h, eps);
-    const Pair a = both(rc * pre), minus_m = both(-(rc * rc * (s2 * inv_h)));
+    const Pair a = both(rc * pre), minus_m = both(-m);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c = tm.tid + u * tm.threads;
@@ -988,7 +1063,7 @@ __global__ void __launch_bounds__(kRowThreads)
       load_weight(p.weight, min(c, H8 - 1), wt);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (p.partial) pw[u][i] = fma(acc[u][i], mul(x[u][i], both(rc)), pw[u][i]);
+        if (p.partial) pw[u][i] = fma(acc[u][i], mul(x[u][i], both(hat)), pw[u][i]);
         wt[i] = mul(a, fma(minus_m, x[u][i], mul(acc[u][i], wt[i])));
       }
       if (p.rgrad) {

@@ -116,3 +116,30 @@ def test_no_norm_and_large_rows(dt):
     keep = torch.ones(T, k, dtype=torch.bool)
     keep[2, 1] = False
     assert torch.equal(got["w"][keep], out["w"][keep]) and not torch.isfinite(got["w"][2, 1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("H,k", [(256, 2), (4096, 8), (8192, 3), (16384, 12)])
+def test_products_past_the_range_beside_a_norm(H, k, dt):
+    """Sums of squares within fp32's range, products with the rows or with the gradient beyond it."""
+    T = 5
+    s = inputs(T, H, k, dt, True, True, True, 0, seed=32)
+    # experts' rows far larger than their weighted sum
+    r = s["dest"][1].long()
+    s["yp"][r] = (s["yp"][r].float() * 1e30).to(BF)
+    s["w"][1] *= 1e-25
+    # one of them alone, with the others' rows of ordinary size or small
+    s["yp"][s["dest"][2, 0].long()] = (s["yp"][s["dest"][2, 0].long()].float() * 1e33).to(BF)
+    s["w"][2, 0] = 1e-28
+    s["yp"][s["dest"][2, 1].long()] = (s["yp"][s["dest"][2, 1].long()].float() * 1e-20).to(BF)
+    check_after(s)
+    # a large sum and a large gradient
+    r = s["dest"][3].long()
+    s["yp"][r] = (s["yp"][r].float() * 1e16).to(BF)
+    s["gy"][3] = (s["gy"][3].float() * 1e24).to(dt)
+    check_after(s)
+    s["x"][0] = (s["x"][0].float() * 1e16).to(dt)
+    g = s["dest"][0].long()
+    s["grad"][g] = (s["grad"][g].float() * 1e24).to(BF)
+    check_before(s)
