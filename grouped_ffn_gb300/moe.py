@@ -894,7 +894,7 @@ def pack_weights_int4(codes, scales, zeros, epilogue: int, stream=None) -> Int4W
     if group * scales.shape[2] != K:
         raise ValueError("pack_weights_int4: inconsistent shapes")
     _maybe(zeros, torch.uint8, scales.shape, "zeros", "pack_weights_int4")
-    _on_current("pack_weights_int4", codes)
+    _on_current("pack_weights_int4", codes, scales, zeros)
     has = zeros is not None
     n = int(lib().moe_int4_packed_bytes(E, N, K, group, int(has), epilogue))
     # allocated on the stream that writes it, see pack_weights_fp4
@@ -911,14 +911,15 @@ def moe_grouped_product_int4(x, seg_offsets, seg_expert, w: Int4Weights, out, ws
     call = "moe_grouped_product_int4"
     kind = _kind(out, "out")
     n, K = _rows_of(call, x, "x")
-    _tensors(call, (_BF16T, None, "x", (x,)), (_I32T, None, "seg_offsets seg_expert", (seg_offsets, seg_expert)),
-             (out.dtype, (n, w.N // 2 if w.epilogue == MOE_EPI_SWIGLU else w.N), "out", (out,)))
+    dev = _tensors(call, (_BF16T, None, "x", (x,)), (_I32T, None, "seg_offsets seg_expert", (seg_offsets, seg_expert)),
+                   (out.dtype, (n, w.N // 2 if w.epilogue == MOE_EPI_SWIGLU else w.N), "out", (out,)),
+                   (_U8T, None, "w.data ws", (w.data, ws)))
     S = seg_expert.numel()
     if K != w.K or seg_offsets.numel() != S + 1:
         raise ValueError("moe_grouped_product_int4: inconsistent shapes")
     _check(call, lib().moe_grouped_product_int4(
         x.data_ptr(), n, seg_offsets.data_ptr(), seg_expert.data_ptr(), S, w.E, w.data.data_ptr(), w.N, K, w.group,
-        w.has_zeros, w.epilogue, out.data_ptr(), kind, ws.data_ptr(), ws.numel(), _stream(stream)))
+        w.has_zeros, w.epilogue, out.data_ptr(), kind, ws.data_ptr(), ws.numel(), _stream_on(stream, dev)))
 
 
 # ------------------------------------------------------------------ the block around the experts
@@ -941,15 +942,24 @@ def new_norm_scratch(T: int, H: int, device=None, stream=None) -> torch.Tensor:
         return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 
 
-def _on_current(call: str, t):
-    if t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"{call}: tensors of another device than the current one")
+def _on_current(call: str, *tensors):
+    """Each tensor lies on the current device, where the call launches."""
+    dev = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{call}: tensors of another device than the current one")
+    return dev
+
+
+_devices = None   # how many there are
 
 
 def _tensors(call: str, *groups):
     """Checks groups (dtype, shape or None for any, names, tensors) of optional contiguous CUDA
-    tensors, the first one's device against the current one; one call for all, since each call
-    costs a tenth of a microsecond."""
+    tensors, all on the current device, which is returned; one call for all, since each call costs
+    a tenth of a microsecond (and each tensor's device half of that: where there is one device,
+    the first tensor's says it all)."""
+    global _devices
     try:
         for dtype, shape, _, tensors in groups:
             for t in tensors:
@@ -964,7 +974,15 @@ def _tensors(call: str, *groups):
                 if t is not None:
                     _need(t, dtype, name)
         raise
-    _on_current(call, groups[0][3][0])
+    if _devices is None:
+        _devices = torch.cuda.device_count()
+    if _devices > 1:
+        return _on_current(call, *(t for g in groups for t in g[3]))
+    return _on_current(call, groups[0][3][0])
+
+
+def _stream_on(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 _F32T, _BF16T, _I32T, _U8T = torch.float32, torch.bfloat16, torch.int32, torch.uint8
@@ -994,9 +1012,9 @@ def moe_norm(x, weight, eps: float, out, stream=None):
     call = "moe_norm"
     kind = _kind(x, "x")
     shape = T, H = _rows_of(call, x, "x")
-    _tensors(call, (x.dtype, None, "x", (x,)), (_BF16T, shape, "out", (out,)), (_F32T, (H,), "weight", (weight,)))
+    dev = _tensors(call, (x.dtype, None, "x", (x,)), (_BF16T, shape, "out", (out,)), (_F32T, (H,), "weight", (weight,)))
     _check(call, lib().moe_norm(x.data_ptr(), kind, T, H, None if weight is None else weight.data_ptr(), eps,
-                                out.data_ptr(), _stream(stream)))
+                                out.data_ptr(), _stream_on(stream, dev)))
 
 
 def moe_combine_norm(y_perm, dest_row, topk_w, residual, cfg: BlockCfg, y, ws, shared=None, weight=None,
@@ -1009,10 +1027,10 @@ def moe_combine_norm(y_perm, dest_row, topk_w, residual, cfg: BlockCfg, y, ws, s
     row = T, H = _rows_of(call, residual, "residual")
     n, h = _rows_of(call, y_perm, "y_perm")
     t, k = _rows_of(call, topk_w, "topk_w")
-    _tensors(call, (residual.dtype, row, "residual y", (residual, y)),
-             (_BF16T, None, "y_perm", (y_perm,)), (_BF16T, row, "shared next_out", (shared, next_out)),
-             (_F32T, None, "topk_w", (topk_w,)), (_F32T, (H,), "weight next_weight", (weight, next_weight)),
-             (_F32T, (T,), "gate", (gate,)), (_I32T, None, "dest_row", (dest_row,)))
+    dev = _tensors(call, (residual.dtype, row, "residual y", (residual, y)),
+                   (_BF16T, None, "y_perm", (y_perm,)), (_BF16T, row, "shared next_out", (shared, next_out)),
+                   (_F32T, None, "topk_w", (topk_w,)), (_F32T, (H,), "weight next_weight", (weight, next_weight)),
+                   (_F32T, (T,), "gate", (gate,)), (_I32T, None, "dest_row", (dest_row,)), (_U8T, None, "ws", (ws,)))
     if h != H or t != T or dest_row.numel() != T * k:
         raise ValueError("moe_combine_norm: inconsistent shapes")
     _check(call, lib().moe_combine_norm(
@@ -1020,7 +1038,7 @@ def moe_combine_norm(y_perm, dest_row, topk_w, residual, cfg: BlockCfg, y, ws, s
         None if shared is None else shared.data_ptr(), residual.data_ptr(), kind,
         None if weight is None else weight.data_ptr(), None if gate is None else gate.data_ptr(),
         ctypes.byref(cfg), y.data_ptr(), None if next_weight is None else next_weight.data_ptr(),
-        None if next_out is None else next_out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
+        None if next_out is None else next_out.data_ptr(), ws.data_ptr(), ws.numel(), _stream_on(stream, dev)))
 
 
 def moe_combine_backward(grad_y, y_perm, dest_row, topk_w, grad_y_perm, grad_topk_w, ws, stream=None):
@@ -1031,13 +1049,15 @@ def moe_combine_backward(grad_y, y_perm, dest_row, topk_w, grad_y_perm, grad_top
     T, H = _rows_of(call, grad_y, "grad_y")
     rows = n, h = _rows_of(call, y_perm, "y_perm")
     w = t, k = _rows_of(call, topk_w, "topk_w")
-    _tensors(call, (grad_y.dtype, None, "grad_y", (grad_y,)), (_BF16T, rows, "y_perm grad_y_perm", (y_perm, grad_y_perm)),
-             (_F32T, w, "topk_w grad_topk_w", (topk_w, grad_topk_w)), (_I32T, None, "dest_row", (dest_row,)))
+    dev = _tensors(call, (grad_y.dtype, None, "grad_y", (grad_y,)),
+                   (_BF16T, rows, "y_perm grad_y_perm", (y_perm, grad_y_perm)),
+                   (_F32T, w, "topk_w grad_topk_w", (topk_w, grad_topk_w)), (_I32T, None, "dest_row", (dest_row,)),
+                   (_U8T, None, "ws", (ws,)))
     if h != H or t != T or dest_row.numel() != T * k:
         raise ValueError("moe_combine_backward: inconsistent shapes")
     _check(call, lib().moe_combine_backward(
         grad_y.data_ptr(), kind, y_perm.data_ptr(), n, dest_row.data_ptr(), topk_w.data_ptr(), T, k, H,
-        grad_y_perm.data_ptr(), grad_topk_w.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
+        grad_y_perm.data_ptr(), grad_topk_w.data_ptr(), ws.data_ptr(), ws.numel(), _stream_on(stream, dev)))
 
 
 def moe_permute_backward(grad, dest_row, grad_x, ws, add=None, stream=None):
@@ -1048,13 +1068,13 @@ def moe_permute_backward(grad, dest_row, grad_x, ws, add=None, stream=None):
     row = T, H = _rows_of(call, grad_x, "grad_x")
     n, h = _rows_of(call, grad, "grad")
     t, k = _rows_of(call, dest_row, "dest_row")
-    _tensors(call, (grad_x.dtype, None, "grad_x", (grad_x,)), (_BF16T, None, "grad", (grad,)),
-             (_BF16T, row, "add", (add,)), (_I32T, None, "dest_row", (dest_row,)))
+    dev = _tensors(call, (grad_x.dtype, None, "grad_x", (grad_x,)), (_BF16T, None, "grad", (grad,)),
+                   (_BF16T, row, "add", (add,)), (_I32T, None, "dest_row", (dest_row,)), (_U8T, None, "ws", (ws,)))
     if h != H or t != T:
         raise ValueError("moe_permute_backward: inconsistent shapes")
     _check(call, lib().moe_permute_backward(
         grad.data_ptr(), n, dest_row.data_ptr(), None if add is None else add.data_ptr(), T, k, H,
-        grad_x.data_ptr(), kind, ws.data_ptr(), ws.numel(), _stream(stream)))
+        grad_x.data_ptr(), kind, ws.data_ptr(), ws.numel(), _stream_on(stream, dev)))
 
 
 def moe_combine_norm_backward(grad_y, y_perm, dest_row, topk_w, cfg: BlockCfg, grad_y_perm, grad_topk_w,
@@ -1067,12 +1087,13 @@ def moe_combine_norm_backward(grad_y, y_perm, dest_row, topk_w, cfg: BlockCfg, g
     row = T, H = _rows_of(call, grad_y, "grad_y")
     rows = n, h = _rows_of(call, y_perm, "y_perm")
     w = t, k = _rows_of(call, topk_w, "topk_w")
-    _tensors(call, (grad_y.dtype, None, "grad_y", (grad_y,)), (_BF16T, rows, "y_perm grad_y_perm", (y_perm, grad_y_perm)),
-             (_BF16T, row, "shared grad_shared", (shared, grad_shared)),
-             (_F32T, w, "topk_w grad_topk_w", (topk_w, grad_topk_w)),
-             (_F32T, (H,), "weight grad_weight", (weight, grad_weight)),
-             (_F32T, (T,), "gate grad_gate", (gate, grad_gate)), (_I32T, None, "dest_row", (dest_row,)),
-             (_U8T, None, "scratch", (scratch,)))
+    dev = _tensors(call, (grad_y.dtype, None, "grad_y", (grad_y,)),
+                   (_BF16T, rows, "y_perm grad_y_perm", (y_perm, grad_y_perm)),
+                   (_BF16T, row, "shared grad_shared", (shared, grad_shared)),
+                   (_F32T, w, "topk_w grad_topk_w", (topk_w, grad_topk_w)),
+                   (_F32T, (H,), "weight grad_weight", (weight, grad_weight)),
+                   (_F32T, (T,), "gate grad_gate", (gate, grad_gate)), (_I32T, None, "dest_row", (dest_row,)),
+                   (_U8T, None, "ws scratch", (ws, scratch)))
     if h != H or t != T or dest_row.numel() != T * k:
         raise ValueError("moe_combine_norm_backward: inconsistent shapes")
     _check(call, lib().moe_combine_norm_backward(
@@ -1083,7 +1104,7 @@ def moe_combine_norm_backward(grad_y, y_perm, dest_row, topk_w, cfg: BlockCfg, g
         None if grad_weight is None else grad_weight.data_ptr(),
         None if grad_gate is None else grad_gate.data_ptr(),
         None if scratch is None else scratch.data_ptr(), 0 if scratch is None else scratch.numel(),
-        ws.data_ptr(), ws.numel(), _stream(stream)))
+        ws.data_ptr(), ws.numel(), _stream_on(stream, dev)))
 
 
 def moe_norm_backward(grad, x, weight, eps: float, grad_x, grad_weight, ws, scratch=None, dest_row=None,
@@ -1096,10 +1117,10 @@ def moe_norm_backward(grad, x, weight, eps: float, grad_x, grad_weight, ws, scra
     row = T, H = _rows_of(call, x, "x")
     n, h = _rows_of(call, grad, "grad")
     t, k = (n, 0) if dest_row is None else _rows_of(call, dest_row, "dest_row")
-    _tensors(call, (x.dtype, row, "x grad_x residual_grad", (x, grad_x, residual_grad)),
-             (_BF16T, None, "grad", (grad,)), (_BF16T, row, "add", (add,)),
-             (_F32T, (H,), "weight grad_weight", (weight, grad_weight)), (_I32T, None, "dest_row", (dest_row,)),
-             (_U8T, None, "scratch", (scratch,)))
+    dev = _tensors(call, (x.dtype, row, "x grad_x residual_grad", (x, grad_x, residual_grad)),
+                   (_BF16T, None, "grad", (grad,)), (_BF16T, row, "add", (add,)),
+                   (_F32T, (H,), "weight grad_weight", (weight, grad_weight)), (_I32T, None, "dest_row", (dest_row,)),
+                   (_U8T, None, "ws scratch", (ws, scratch)))
     if h != H or t != T:
         raise ValueError("moe_norm_backward: inconsistent shapes")
     _check(call, lib().moe_norm_backward(
@@ -1109,7 +1130,7 @@ def moe_norm_backward(grad, x, weight, eps: float, grad_x, grad_weight, ws, scra
         None if residual_grad is None else residual_grad.data_ptr(), residual_scale, grad_x.data_ptr(),
         None if grad_weight is None else grad_weight.data_ptr(),
         None if scratch is None else scratch.data_ptr(), 0 if scratch is None else scratch.numel(),
-        ws.data_ptr(), ws.numel(), _stream(stream)))
+        ws.data_ptr(), ws.numel(), _stream_on(stream, dev)))
 
 
 def moe_status_string(status: int) -> str:
