@@ -119,6 +119,8 @@ class MoELayer:
         if post_weight is not None and not block.post_norm:
             raise ValueError("post_weight belongs to a block with post_norm")
         self.block, self.post_weight, self.next_weight = block, post_weight, next_weight
+        # whether the last step had a residual, and whether captured ones had
+        self._had_residual, self._captured = block is not None, set()
         if gate is not None and gate.k != k:
             raise ValueError("gate.k must be k")
         if gate_bias is not None and gate is None:
@@ -370,17 +372,25 @@ class MoELayer:
                               grad_logits, self.ws, stream)
 
     def combine_backward(self, grad_y, grad_y_perm, grad_topk_w, gate=None, grad_shared=None,
-                         grad_weight=None, grad_gate=None, stream=None):
+                         grad_weight=None, grad_gate=None, stream=None, residual: Optional[bool] = None):
         """Gradients of the last step's expert rows (grad_y_perm, of y_perm's first n_rows) and
-        weights for a gradient of its output: moe_combine_norm_backward with a block (the gate that
-        forward was given; the residual's gradient is residual_scale * grad_y), else
-        moe_combine_backward, where the shared rows' gradient is grad_y itself."""
+        weights for a gradient of its output: moe_combine_norm_backward where forward had a residual
+        (the gate that forward was given; the residual's gradient is residual_scale * grad_y), else
+        moe_combine_backward, where the shared rows' gradient is grad_y itself.  residual says which
+        of the two where steps of both kinds are in use and some are replayed from graphs."""
         T = grad_y.shape[0]
         rows, w = self.y_perm[:grad_y_perm.shape[0]], self.topk_w[:T]
         dest = self.dest_row[:T * self.k]
-        if self.block is None:
+        if residual is None:
+            residual = self._had_residual
+            if self._captured - {residual}:
+                raise ValueError("combine_backward: a captured step differs in its residual from the last "
+                                 "forward: residual=True or False says which step's gradient is asked for")
+        elif residual and self.block is None:
+            raise ValueError("combine_backward: a residual needs a block")
+        if not residual:
             if gate is not None or grad_shared is not None or grad_weight is not None or grad_gate is not None:
-                raise ValueError("combine_backward: no block")
+                raise ValueError("combine_backward: a step without residual has no gate and no norm")
             moe.moe_combine_backward(grad_y, rows, dest, w, grad_y_perm, grad_topk_w, self.ws, stream)
             return
         moe.moe_combine_norm_backward(grad_y, rows, dest, w, self.block, grad_y_perm, grad_topk_w, self.ws,
@@ -459,6 +469,9 @@ class MoELayer:
         if residual is None and (gate is not None or next_out is not None):
             raise ValueError("gate and next_out belong to a residual")
         tail = (residual, gate, next_out)
+        self._had_residual = residual is not None
+        if self.block is not None and torch.cuda.is_current_stream_capturing():
+            self._captured.add(self._had_residual)
         A = T * self.k
         ids, w = self.topk_ids[:T], self.topk_w[:T]
         if self.gate is not None:
