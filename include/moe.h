@@ -743,7 +743,9 @@ moe_status moe_pack_weights_int4(const uint8_t *codes, const uint16_t *scales,
  *              are left unwritten.
  *  Limits: those of moe_pack_weights_int4, S <= 1024, n_rows < 2^31 - 64, and
  *  (n_rows / 8 + S) * N / 32 (SwiGLU: the same) below 2^31 - 65536 tiles.  ws: at
- *  least MOE_WS_STATUS_BYTES.  Device errors: MOE_ERR_DEVICE_INDEX (an expert id
+ *  least MOE_WS_STATUS_BYTES.  The same call gives the same bits; a row's last bits
+ *  may differ with the rows beside it, since the number of a call's tasks (blocks of
+ *  weights times row tiles) chooses into how many parts K is summed.  Device errors: MOE_ERR_DEVICE_INDEX (an expert id
  *  or a segment outside its range: the segment is skipped; offsets that decrease:
  *  nothing is computed). */
 moe_status moe_grouped_product_int4(const uint16_t *x, int64_t n_rows, const int32_t *seg_offsets,
