@@ -667,10 +667,15 @@ __device__ __forceinline__ void put_partial(const Pair (&pw)[U][4], float *parti
 // once and need not be kept:
 //   dc = gate r (e - c m),  m = r^2 mean(e c),  dw_j = gate r (e . Y_j - m c . Y_j).
 // The weight's gradient is kept per thread over the CTA's tokens and added up
-// by sum_partials_kernel in a fixed order.  16384 tokens of 4096 in fp32, four
-// experts: 245 us, 5.5 TB/s; 4096 of 1440, six experts: 49 us, 3.6 TB/s.  Bound by
-// issue at 16 warps an SM (128 registers; at 80 they spill, 434 us): leaving out one
-// of the two dots, the weight's gradient or the stores saves a tenth each.
+// by sum_partials_kernel in a fixed order.  With that kernel, 16384 tokens of 4096 in
+// fp32, four experts: 243 us, 5.5 TB/s; 4096 of 7168, eight experts and a shared one:
+// 216 us, 6.0 TB/s; 4096 of 1440, six and a shared one: 46 us, 3.9 TB/s.  Bound by
+// latency at 16 warps an SM (128 registers; at 80 they spill, 434 us): issue is at 60%,
+// HBM at 61%, and of the 6.6 cycles from a warp's instruction to its next 1.7 wait for
+// a result of fixed latency, 1.2 for shared memory and 0.6 for global memory.  Leaving
+// out one of the two dots, the weight's gradient or the stores saves a tenth each.
+// Rows beyond 8192, or more than eight experts, spill: 2048 tokens of 12288 with four
+// experts 161 us (2.8 TB/s), with 16 experts 581 us (2.9 TB/s).
 template <int KMAX, int U, int R, typename X>
 __global__ void __launch_bounds__(kRowThreads)
     combine_norm_bwd_kernel(const CombineBwdParams p, const int team_threads) {
@@ -918,7 +923,8 @@ struct NormBwdParams {
 
 // u = add + the sum of the copies' gradients (or grad's own row), e = u weight:
 //   gx = scale rgrad + r (e - x r^2 mean(e x)),  weight's gradient sum_t u x r.
-// 16384 rows of 4096 in fp32, four copies each: 245 us, 6.0 TB/s.
+// With sum_partials_kernel, 16384 rows of 4096 in fp32, four copies each: 231 us,
+// 6.4 TB/s; 2048 of 12288 (which spill) 100 us, 3.5 TB/s.
 template <int U, int R, typename X>
 __global__ void __launch_bounds__(kRowThreads)
     norm_bwd_kernel(const NormBwdParams p, const int team_threads) {

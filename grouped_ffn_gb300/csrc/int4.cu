@@ -303,11 +303,16 @@ __device__ __forceinline__ int team_log(int total, int steps, int warps) {
 // task while a task ends.  Rows of x come from L1 and L2, a step ahead in registers.
 // A lane whose row lies past the tile reads the tile's last row instead: a column of
 // the product does not reach the others, and is not stored.
-// Bound by the expansion of the codes (of 289 instructions for 2 KB of them 112 are
-// shifts and and-ors, 64 subtractions, at 64 lanes a clock each), then by HBM: 128
-// rows over 64 experts, 8192 -> 2 x 2048, 184 us, 5.1 TB/s; 512 rows over 256
-// experts, 2048 -> 7168, 363 us, 5.1 TB/s; one token's eight rows over eight experts,
-// 7168 -> 2 x 2048, 30 us, 4.1 TB/s.
+// Bound by the length of a warp's chain of instructions at 16 warps an SM, not by one
+// unit: 289 instructions for 2 KB of codes (112 shifts and and-ors, 64 subtractions), and
+// issue is at 63%, the ALU at 60%, HBM at 63%, tensor cores at 27%.  Of 6.2 cycles from a
+// warp's instruction to its next 1.2 wait for a result of fixed latency, 1.1 for a busy
+// unit, 1.1 for other warps to issue and 0.7 for loads.  128 rows over 64 experts, 8192
+// -> 2 x 2048, 184 us, 5.1 TB/s; 512 rows over 256 experts, 2048 -> 7168, 361 us, 5.1
+// TB/s; one token's eight rows over eight experts, 7168 -> 2 x 2048, 29.4 us, 4.1 TB/s
+// (2048 of 2432 warps have one task's half each, 28 steps, and start and end are
+// exposed).  Many rows expand the weights again for each 16 of a segment: 32768 rows over
+// 256 experts, 7168 -> 2 x 2048, 6.8 ms, 282 TFLOP/s.
 template <int NT, int NG, bool ZEROS>
 __global__ void __launch_bounds__(32 * kWarps, kCtasPerSm)
     int4_product_kernel(const Params p) {

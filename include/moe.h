@@ -726,9 +726,9 @@ moe_status moe_pack_weights_int4(const uint8_t *codes, const uint16_t *scales,
 
 /* Grouped product of bf16 rows with 4-bit integer expert weights, one segment an
  * expert ("14. Serving Mixture-of-Experts Models", "Follow one token", step 3),
- * for decode steps: the weights are streamed once for up to 16 rows of a segment
- * and again (from L2) for more, so large segments are better served by the
- * bf16 or FP4 experts.  For segment s, e = seg_expert[s], row r in
+ * for decode steps: the weights are streamed and expanded once for up to 16 rows
+ * of a segment and again (from L2) for each 16 more.  Prompts run, at 0.27 PFLOP/s;
+ * where large segments matter, the bf16 or FP4 experts serve them better.  For segment s, e = seg_expert[s], row r in
  * [seg_offsets[s], seg_offsets[s+1]) (no weight is rounded, fp32 accumulation,
  * one rounding):
  *   MOE_EPI_NONE    out[r, n] = sum_K x[r, K] w[e, n, K],  n < N
@@ -815,7 +815,7 @@ typedef struct moe_block_cfg {
  *          may be x itself when x is bf16.
  *  weight  device fp32 [H], 16-byte aligned, or NULL for ones.
  *  Rows of finite values have a finite norm whatever their size (squares beyond
- *  fp32's range are summed scaled down).  Limits: H % 8 == 0, H <= 16384. */
+ *  fp32's range are summed scaled down, and eps with them).  Limits: H % 8 == 0, H <= 16384. */
 moe_status moe_norm(const void *x, int32_t x_type, int64_t T, int32_t H, const float *weight,
                     float eps, uint16_t *out, void *stream);
 
@@ -884,7 +884,10 @@ size_t moe_norm_scratch_bytes(int64_t T, int32_t H);
  *   grad_weight[h] = sum_t gate dy c r
  * and the gradient of the residual is residual_scale * grad_y (see
  * moe_norm_backward).  Sums are fp32 in an order fixed by the sizes and the
- * device: the same call gives the same bits.
+ * device: the same call gives the same bits.  A token whose c^2, e c or products
+ * with the rows add up to more than fp32's range, while its gradients do not, is
+ * summed scaled; an infinity or NaN stays in its token (but for grad_weight, a sum
+ * over tokens).  Without post_norm only grad_gate depends on c.
  *  grad_shared device bf16 [T, H], grad_weight fp32 [H] (post_norm only) and
  *  grad_gate fp32 [T] may each be NULL; grad_weight needs scratch of
  *  moe_norm_scratch_bytes, 16-byte aligned.  Outputs overlap no input.  Other
