@@ -1191,7 +1191,9 @@ moe_status launch_teams(const P &p, const TeamShape &s, cudaStream_t st) {
 
 bool bad_type(int32_t type) { return type != MOE_F32 && type != MOE_BF16; }
 bool odd(const void *p) { return !moe_host::aligned16(p); }
-bool bad_eps(float eps) { return !(eps > 0.0f) || !isfinite(eps); }
+// The gradients take 1 / eps (of rows of zeros), the norms mean(x^2) + eps with a mean of
+// up to 2^125: both stay within fp32's range.
+bool bad_eps(float eps) { return !(eps >= 0x1p-126f && eps <= 0x1p127f); }
 
 moe_status check_sizes(int64_t T, int32_t k, int32_t H, int64_t n_rows) {
   if (T < 0 || H < 1 || k < 1 || n_rows < 0) return MOE_ERR_INVALID_ARG;

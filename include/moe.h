@@ -799,7 +799,7 @@ moe_status moe_combine_merged(const uint16_t *y_perm, const int32_t *dest_row, c
 /* The block around the experts: an RMS norm before it, and after it the
  * weighted sum of the experts' rows through a norm, a gate and a residual.
  *  post_norm       1: the sum is normalised; 0: it is taken as it is.
- *  eps             of the norms, positive and finite.
+ *  eps             of the norms, from 2^-126 to 2^127 (in the other calls too).
  *  residual_scale  factor of the residual, finite. */
 typedef struct moe_block_cfg {
   int32_t post_norm;
