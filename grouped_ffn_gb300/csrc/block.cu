@@ -786,7 +786,10 @@ __global__ void __launch_bounds__(kRowThreads)
       ec = s2 * rc;
       for (int j = tm.warp; j < p.k; j += tm.nw) {
         const float ey = total(b, j, tm.nw, tm.lane), cy = total(b, KMAX + j, tm.nw, tm.lane);
-        if (tm.lane == j) p.gw[t * p.k + j] = now.row < 0 ? 0.0f : g * rc * (ey - m * cy);
+        float dw = g * rc * (ey - m * cy);
+        // (the product of two sums may pass the range where that with gate and r does not)
+        if (!(fabsf(m * cy) <= FLT_MAX)) dw = g * rc * ey - g * rc * m * cy;
+        if (tm.lane == j) p.gw[t * p.k + j] = now.row < 0 ? 0.0f : dw;
       }
     } else {
       // A sum is not within fp32's range: of c^2, e c, or products with rows far larger

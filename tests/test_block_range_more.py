@@ -65,6 +65,23 @@ def test_smallest_eps(dt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("H", [1024, 16384])
+def test_product_of_sums_beyond_the_range(H, dt):
+    """e . Y = 0, e . c and c . Y within the range, their product beyond it, and a gate that brings the
+    weight's gradient back."""
+    T, k = 3, 2
+    s = inputs(T, H, k, dt, True, True, True, 0, seed=41)
+    s["gy"][1, :H // 2] = (1e20 * s["gy"][1, :H // 2].float()).to(dt)
+    s["gy"][1, H // 2:] = 0
+    row = s["dest"][1, 0].long()
+    s["yp"][row, :H // 2] = 0
+    s["yp"][row, H // 2:] = (1e20 * s["yp"][row, H // 2:].float()).to(BF)
+    s["w"][1, 0], s["gate"][1] = 1e-22, 1e-12
+    check_after(s)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,H,k,dt", [(8000, 256, 2, BF), (5000, 264, 5, F32), (700, 8192, 3, BF), (400, 12288, 2, F32)])
 def test_tokens_of_every_size_in_turn(T, H, k, dt):
     """Several tokens a team, those with sums beyond the range among others."""
